@@ -28,7 +28,8 @@ LIB_PATH = os.path.join(_HERE, "libafd.so")
 OK, ERR_ARG, ERR_STATE, ERR_BUCKET, ERR_RECEIPT = 0, 1, 2, 3, 4
 ERR_ROUTE_RANGE, ERR_ROUTE_DUP, ERR_CUDA, ERR_OOM, ERR_CAPTURING, ERR_UNSUPPORTED = 5, 6, 7, 8, 9, 10
 ERR_TIMEOUT = 11
-BF16, FP8_E4M3 = 0, 1
+BF16, FP8_E4M3, FP32 = 0, 1, 2
+SCORINGS = {"softmax": 0, "sigmoid": 1}
 COMBINE_FUSED, COMBINE_TWO_STAGE, COMBINE_TWO_STAGE_FP8 = 0, 1, 2
 
 EXPORTS = ("afd_create", "afd_destroy", "afd_source_dispatch", "afd_source_dispatch_cached",
@@ -37,7 +38,8 @@ EXPORTS = ("afd_create", "afd_destroy", "afd_source_dispatch", "afd_source_dispa
            "afd_clear_error",
            "afd_reset_exchange", "afd_status_string", "afd_error_detail", "afd_arena_rows",
            "afd_recv_rows_for_bucket", "afd_version", "afd_route_layout_noalloc",
-           "afd_set_wait_limit", "afd_phase_stamps", "afd_l2_flush")
+           "afd_set_wait_limit", "afd_phase_stamps", "afd_l2_flush", "afd_route_topk",
+           "afd_grouped_linear", "afd_gated_rows", "afd_adapter_add")
 
 
 class AfdError(RuntimeError):
@@ -100,6 +102,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "afd_set_wait_limit": (i32, [v, i32]),
         "afd_phase_stamps": (i32, [v, P(u64), i64, i32]),
         "afd_l2_flush": (i32, [v, i64, v]),
+        "afd_route_topk": (i32, [v, i32, i64, v, v, i32, i32, i32, i32, i32, ctypes.c_float, v, v, v]),
+        "afd_grouped_linear": (i32, [v, i64, v, v, v, v, i32, i32, i64, i32, i32, i32, i32, v, i64, v, v]),
+        "afd_gated_rows": (i32, [v, i64, v, i32, i32, i64, i32, v, i64, v]),
+        "afd_adapter_add": (i32, [v, i64, v, i64, v, v, v, v, v, v, i32, i32, i64, i32, i32, i32, i32,
+                                  i32, v, i64, v]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -421,3 +428,179 @@ def route_layout_noalloc(ids: torch.Tensor, num_experts: int, num_workers: int,
                                       _ptr(error), _stream_handle(stream, ids.device))
     if st != OK:
         raise AfdError(st, "afd_route_layout_noalloc: " + lib.afd_status_string(st).decode())
+
+
+# -- the experts' side of an exchange (afd.h: no context, no state) -----------
+def _call(name: str, device, stream, *args) -> None:
+    """Calls a context-free entry point on `device`'s stream, with that device
+    current (the library works on the current one)."""
+    lib = load_library()
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = getattr(lib, name)(*args, _stream_handle(stream, device))
+    else:
+        st = getattr(lib, name)(*args, _stream_handle(stream, device))
+    if st != OK:
+        raise AfdError(st, f"{name}: {lib.afd_status_string(st).decode()}")
+
+
+def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> None:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise AfdError(ERR_ARG, f"{name} must be contiguous {dtype} {list(shape)}, "
+                       f"got {t.dtype} {list(t.shape)}")
+
+
+def _want_rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> int:
+    """Checks a [rows, columns] tensor whose rows may be strided; returns the
+    row stride in elements."""
+    if t.dtype != dtype or t.shape != shape or (shape[1] > 1 and t.stride(1) != 1) \
+            or (shape[0] > 1 and t.stride(0) < shape[1]):
+        raise AfdError(ERR_ARG, f"{name} must be {dtype} {list(shape)} with dense rows, "
+                       f"got {t.dtype} {list(t.shape)}")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def route_topk(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
+               bias: Optional[torch.Tensor] = None, renormalize: bool = True, scale: float = 1.0,
+               live_tokens: Optional[torch.Tensor] = None, ids: Optional[torch.Tensor] = None,
+               weights: Optional[torch.Tensor] = None, stream=None):
+    """The router: ``(ids, weights)`` of every token's `top_k` experts, int64
+    and float32 [T, top_k], as :meth:`Buffer.source_dispatch` takes them.
+
+    `logits` is [T, E], bf16 or float32. Scores are softmax or sigmoid of the
+    logits; `bias` (float32 [E]) is added to them for the selection only.
+    Ties go to the lowest index; NaN and -inf are never selected and slots
+    without an expert get ID -1 and weight 0. `live_tokens` (int32 [1], on the
+    device) makes the tokens from there on padding. See afd_route_topk in
+    include/afd.h."""
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise AfdError(ERR_ARG, f"logits must be bfloat16 or float32 [T, E], got {logits.dtype}")
+    if scoring not in SCORINGS:
+        raise AfdError(ERR_ARG, f"scoring must be one of {sorted(SCORINGS)}, got {scoring!r}")
+    T, E = logits.shape
+    stride = _want_rows(logits, "logits", logits.dtype, (T, E))
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (E,))
+    if live_tokens is not None:
+        _want(live_tokens, "live_tokens", torch.int32, (1,))
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int64, device=logits.device)
+    else:
+        _want(ids, "ids", torch.int64, (T, top_k))
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    else:
+        _want(weights, "weights", torch.float32, (T, top_k))
+    _call("afd_route_topk", ids.device, stream, logits.data_ptr() if T else None,
+          FP32 if logits.dtype == torch.float32 else BF16, stride, _ptr(bias), _ptr(live_tokens), T, E, top_k,
+          SCORINGS[scoring], int(bool(renormalize)), scale, ids.data_ptr() if T else None,
+          weights.data_ptr() if T else None)
+    return ids, weights
+
+
+def grouped_linear(x: torch.Tensor, weight: torch.Tensor, ends: torch.Tensor, *, expert_alignment: int = 1,
+                   gated: bool = False, x_scale: Optional[torch.Tensor] = None,
+                   weight_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   error: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The experts' matrix product over received rows: ``out[r] = x[r] @
+    weight[l].T`` for the rows of every expert l, BF16.
+
+    `x` is [R, K] and `weight` [E/F, N, K], both bf16, or both float8_e4m3fn
+    with `x_scale` [R, K/128] and `weight_scale` [E/F, N/128, K/128]. `ends`
+    and `expert_alignment` are those of the exchange
+    (:attr:`Receive.ends`). With `gated` the weight has the gate's rows first
+    and the up projection's after them ([E/F, 2N, K]) and ``out = silu(gate) *
+    up``. Rows outside every expert's range are left as they were (`out`) or
+    unspecified (without `out`). `error` (int32 [1]) receives ERR_TIMEOUT if a
+    bounded wait of the kernel gave up. See afd_grouped_linear in
+    include/afd.h."""
+    if x.dim() != 2 or weight.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise AfdError(ERR_ARG, "x must be [R, K] bfloat16 or float8_e4m3fn and weight [G, N, K]")
+    R, K = x.shape
+    G, W = weight.shape[0], weight.shape[1]
+    fp8 = x.dtype == torch.float8_e4m3fn
+    if gated and W % 2:
+        raise AfdError(ERR_ARG, f"a gated weight has an even number of rows, got {W}")
+    N = W // 2 if gated else W
+    x_stride = _want_rows(x, "x", x.dtype, (R, K))
+    _want(weight, "weight", x.dtype, (G, W, K))
+    _want(ends, "ends", torch.int32, (G,))
+    if fp8:
+        if x_scale is None or weight_scale is None or K % 128 or N % 128:
+            raise AfdError(ERR_ARG, "float8_e4m3fn takes x_scale, weight_scale and K, N that are multiples of 128")
+        _want(x_scale, "x_scale", torch.float32, (R, K // 128))
+        _want(weight_scale, "weight_scale", torch.float32, (G, W // 128, K // 128))
+    elif x_scale is not None or weight_scale is not None:
+        raise AfdError(ERR_ARG, "bfloat16 rows take no scales")
+    if out is None:
+        out = torch.empty((R, N), dtype=torch.bfloat16, device=x.device)
+        out_stride = N
+    else:
+        out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
+    if error is not None:
+        _want(error, "error", torch.int32, (1,))
+    _call("afd_grouped_linear", x.device, stream, x.data_ptr(), x_stride, _ptr(x_scale), weight.data_ptr(),
+          _ptr(weight_scale), ends.data_ptr(), G, expert_alignment, R, K, N, FP8_E4M3 if fp8 else BF16,
+          int(bool(gated)), out.data_ptr(), out_stride, _ptr(error))
+    return out
+
+
+def gated_rows(h: torch.Tensor, ends: torch.Tensor, *, expert_alignment: int = 1,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gated activation over received rows, BF16: ``out[r] = silu(h[r, :N])
+    * h[r, N:]`` for `h` [R, 2N]; rows outside every expert's range are left
+    as they were. `out` may be ``h[:, :N]``. See afd_gated_rows in
+    include/afd.h."""
+    if h.dim() != 2 or h.shape[1] % 2:
+        raise AfdError(ERR_ARG, "h must be bfloat16 [R, 2N]")
+    R, N = h.shape[0], h.shape[1] // 2
+    h_stride = _want_rows(h, "h", torch.bfloat16, (R, 2 * N))
+    if ends.dim() != 1:
+        raise AfdError(ERR_ARG, "ends must be int32 [G]")
+    _want(ends, "ends", torch.int32, (ends.shape[0],))
+    if out is None:
+        out = torch.empty((R, N), dtype=torch.bfloat16, device=h.device)
+    out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
+    _call("afd_gated_rows", ends.device, stream, h.data_ptr(), h_stride, ends.data_ptr(), ends.shape[0],
+          expert_alignment, R, N, out.data_ptr(), out_stride)
+    return out
+
+
+def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: torch.Tensor,
+                token_slots: torch.Tensor, scales: torch.Tensor, *, row_src: Optional[torch.Tensor] = None,
+                ends: Optional[torch.Tensor] = None, top_k: int = 1, out: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """Low-rank adapters of many requests beside a shared projection, BF16:
+    ``out[r] = base[r] + scales[a] * up[a] @ (down[a] @ x[r])`` with a =
+    ``token_slots[row_src[r] // top_k]`` (received rows: `row_src`, `ends` and
+    `top_k` of the exchange, token_slots over [A * bucket] tokens) or
+    ``token_slots[r]`` (a source's own tokens). A slot outside [0, S) means no
+    adapter. `down` is [S, rank, K], `up` [S, N, rank]; `out` defaults to
+    `base` (in place). See afd_adapter_add in include/afd.h."""
+    if base.dim() != 2 or x.dim() != 2 or down.dim() != 3:
+        raise AfdError(ERR_ARG, "base must be [R, N], x [R, K], down [S, rank, K] and up [S, N, rank]")
+    (R, N), K, (S, rank) = base.shape, x.shape[1], down.shape[:2]
+    base_stride = _want_rows(base, "base", torch.bfloat16, (R, N))
+    x_stride = _want_rows(x, "x", torch.bfloat16, (R, K))
+    _want(down, "down", torch.bfloat16, (S, rank, K))
+    _want(up, "up", torch.bfloat16, (S, N, rank))
+    _want(scales, "scales", torch.float32, (S,))
+    tokens = token_slots.numel()
+    _want(token_slots, "token_slots", torch.int32, (tokens,))
+    G = 0
+    if row_src is not None:
+        if ends is None or ends.dim() != 1:
+            raise AfdError(ERR_ARG, "row_src needs the exchange's ends, int32 [G]")
+        G = ends.shape[0]
+        _want(row_src, "row_src", torch.int32, (R,))
+        _want(ends, "ends", torch.int32, (G,))
+    elif tokens < R:
+        raise AfdError(ERR_ARG, f"token_slots has {tokens} entries for {R} rows")
+    if out is None:
+        out, out_stride = base, base_stride
+    else:
+        out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
+    _call("afd_adapter_add", base.device, stream, base.data_ptr(), base_stride, x.data_ptr(), x_stride,
+          down.data_ptr(), up.data_ptr(), token_slots.data_ptr(), scales.data_ptr(), _ptr(row_src),
+          _ptr(ends) if G else None, G, top_k, R, tokens, S, rank, K, N, out.data_ptr(), out_stride)
+    return out

@@ -22,6 +22,9 @@
 
 #include "afd.h"
 #include "afd_device.cuh"
+#include "afd_pointers.cuh"
+
+using afd::device_view;
 
 namespace {
 
@@ -187,30 +190,6 @@ afd_status scratch_for_current_device(int32_t** out) {
   }
   *out = g_scratch_ptr[dev];
   return AFD_OK;
-}
-
-// The address a kernel on the current device uses for a caller buffer: the
-// buffer itself in that device's memory or in managed memory, the mapped
-// device address of page-locked host memory. Pageable host memory, and
-// memory of another device, are refused before anything is enqueued.
-template <typename T>
-bool device_view(T* p, T** out) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  cudaPointerAttributes a = {};
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  if ((a.type == cudaMemoryTypeDevice && a.device == dev) || a.type == cudaMemoryTypeManaged) {
-    *out = p;
-    return true;
-  }
-  if (a.type == cudaMemoryTypeHost && a.devicePointer) {
-    *out = static_cast<T*>(a.devicePointer);
-    return true;
-  }
-  return false;
 }
 
 }  // namespace

@@ -83,7 +83,7 @@ typedef enum afd_status {
                                error, through afd_get_error; the outputs are unspecified) */
 } afd_status;
 
-enum { AFD_BF16 = 0, AFD_FP8_E4M3 = 1 };
+enum { AFD_BF16 = 0, AFD_FP8_E4M3 = 1, AFD_FP32 = 2 /* router logits only */ };
 
 /* How the combine sums a token's reply rows (afd_config.combine_mode).
  * FUSED: one FP32 fused multiply-add chain over the routes in ascending k,
@@ -387,6 +387,134 @@ AFD_API afd_status afd_route_layout_noalloc(const int64_t* ids, int32_t num_toke
                                             int32_t num_experts, int32_t num_workers,
                                             int32_t expert_alignment, int32_t* ends,
                                             int32_t* slots, int32_t* error, afd_stream stream);
+
+/* The experts' side of an exchange: the router that makes a dispatch's IDs
+ * and weights, and the products a worker computes between worker_receive and
+ * worker_reply. These calls take no context and keep no state: they allocate
+ * nothing, never synchronize, and may run at the same time on any streams, in
+ * any number of captured graphs, as long as their buffers do not overlap.
+ * Work is enqueued on `stream`, a stream of the current device, on which
+ * every buffer must be reachable (a buffer of another device returns
+ * AFD_ERR_ARG and enqueues nothing). */
+
+/* How afd_route_topk scores an expert. */
+enum { AFD_SCORE_SOFTMAX = 0, AFD_SCORE_SIGMOID = 1 };
+
+/* Router: the top_k experts of every token, in the form afd_source_dispatch
+ * takes (no counterpart in the pages, which start from given IDs).
+ *   score_e = softmax(logits)_e over all experts, or sigmoid(logits_e)
+ *   key_e   = score_e + bias_e (bias given), else logits_e
+ * The experts with the largest keys are selected, in descending order, a tie
+ * going to the lowest index; bias moves the selection only. Keys are compared
+ * as if in 64 bits. Then
+ *   weight = scale * score                          (renormalize = 0)
+ *   weight = scale * score / sum of selected scores (renormalize = 1; the
+ *            scores' common factor cancels before it can underflow)
+ * An expert whose logit (or bias) is NaN or -infinity is never selected and
+ * adds nothing to the softmax; +infinity counts as the largest finite value.
+ * A slot for which no expert is left gets ID -1 and weight 0, which a
+ * dispatch skips.
+ *   logits       device [num_tokens, num_experts], BF16 or FP32 (logits_dtype),
+ *                row t at logits + t * row_stride elements
+ *   bias         device FP32 [num_experts], or NULL
+ *   live_tokens  device int32 [1], or NULL: tokens t >= *live_tokens (a
+ *                bucket's padding) get IDs -1 and weights 0; their logits are
+ *                not read
+ *   ids, weights device int64 / FP32 [num_tokens, top_k] out
+ * Limits: top_k <= min(32, num_experts), num_experts <= 1024.
+ * Buffers may be device, managed or page-locked host memory.
+ * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (num_experts), AFD_ERR_CUDA. */
+AFD_API afd_status afd_route_topk(const void* logits, int32_t logits_dtype, int64_t row_stride,
+                                  const float* bias, const int32_t* live_tokens, int32_t num_tokens,
+                                  int32_t num_experts, int32_t top_k, int32_t scoring,
+                                  int32_t renormalize, float scale, int64_t* ids, float* weights,
+                                  afd_stream stream);
+
+/* The experts' matrix product over received rows: for every row r of expert l
+ * (rows [align_up(ends[l-1], expert_alignment), ends[l]), as afd_recv gives
+ * them)
+ *   y[r][n] = sum over k of x[r][k] * weight[l][n][k]
+ *   out[r]  = y[r]                              (gated = 0)
+ *   out[r][n] = silu(y[r][n]) * y[r][N + n]     (gated = 1, N = out_features;
+ *               weight then has 2N rows per expert, the gate's first)
+ * with FP32 sums and one rounding to BF16. FP8: x and weight are E4M3 with
+ * FP32 scales for blocks of 128, and the sum is that of x_scale[r][k/128] *
+ * weight_scale[l][n/128][k/128] * x * weight.
+ * Rows of `out` outside every expert's range are left as they were; rows of
+ * `x` there are never used for a result, whatever they hold. Ends beyond
+ * num_rows are taken as num_rows.
+ *   x             device [num_rows, in_features] BF16 or E4M3 (dtype), row r at
+ *                 x + r * x_stride elements
+ *   x_scale       device FP32 [num_rows, in_features/128] (FP8), else NULL
+ *   weight        device [num_groups, N or 2N, in_features], contiguous
+ *   weight_scale  device FP32 [num_groups, (N or 2N)/128, in_features/128]
+ *                 (FP8), else NULL
+ *   ends          device int32 [num_groups], non-decreasing
+ *   out           device BF16 [num_rows, out_features], row r at out + r *
+ *                 out_stride elements; must not overlap the inputs
+ *   error         device int32 [1], or NULL: set to AFD_ERR_TIMEOUT if a
+ *                 bounded wait of the kernel gave up (the rows of `out` are
+ *                 then unspecified), else left as it was
+ * Buffers are device memory of the current device (the rows and weights move
+ * by bulk copies). x, weight, x_stride and the rows of weight are multiples
+ * of 16 bytes; FP8 takes in_features and out_features that are multiples of
+ * 128. num_groups <= 1024.
+ * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (sizes or alignments above),
+ * AFD_ERR_CUDA. */
+AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride, const float* x_scale,
+                                      const void* weight, const float* weight_scale,
+                                      const int32_t* ends, int32_t num_groups,
+                                      int32_t expert_alignment, int64_t num_rows,
+                                      int32_t in_features, int32_t out_features, int32_t dtype,
+                                      int32_t gated, void* out, int64_t out_stride, int32_t* error,
+                                      afd_stream stream);
+
+/* The gated activation over received rows, for products whose activation
+ * cannot be part of them (afd_adapter_add between the two): for every row r
+ * of an expert's range (as in afd_grouped_linear)
+ *   out[r][n] = silu(h[r][n]) * h[r][features + n]
+ * computed in FP32 and rounded once. Other rows are left as they were.
+ *   h    device BF16 [num_rows, 2 * features], row r at h + r * h_stride
+ *   out  device BF16 [num_rows, features], row r at out + r * out_stride; may
+ *        be the first half of h itself
+ * Buffers may be device, managed or page-locked host memory.
+ * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (num_groups > 1024), AFD_ERR_CUDA. */
+AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t* ends,
+                                  int32_t num_groups, int32_t expert_alignment, int64_t num_rows,
+                                  int32_t features, void* out, int64_t out_stride,
+                                  afd_stream stream);
+
+/* Low-rank adapters of many requests beside a shared projection: row r of the
+ * request whose adapter is a gets
+ *   out[r] = base[r] + scales[a] * up[a] (down[a] x[r])
+ * in FP32 with one rounding to BF16 (the low-rank product down[a] x[r] is
+ * kept to at least 16 bits of precision between the two).
+ * The adapter of a row: a = token_slots[t], where t = row_src[r] / top_k for
+ * received rows (row_src as afd_recv gives it), or t = r without row_src. A
+ * slot outside [0, num_slots) means no adapter: out[r] = base[r].
+ * With row_src, rows r >= ends[num_groups-1] and rows whose row_src is
+ * negative or names a token outside [0, num_tokens) are left as they were.
+ *   base, out    device BF16 [num_rows, out_features], row strides
+ *                base_stride / out_stride; out may be base (in place)
+ *   x            device BF16 [num_rows, in_features], row stride x_stride
+ *   down         device BF16 [num_slots, rank, in_features], contiguous
+ *   up           device BF16 [num_slots, out_features, rank], contiguous
+ *   token_slots  device int32 [num_tokens]
+ *   scales       device FP32 [num_slots]
+ *   row_src      device int32 [num_rows] with ends, or NULL (then num_tokens
+ *                >= num_rows, and ends may be NULL)
+ * Limits: rank 8, 16, 32 or 64; in_features a multiple of 16; out_features a
+ * multiple of 8; base, out, x, down, up and the strides multiples of 16
+ * bytes. Buffers may be device, managed or page-locked host memory.
+ * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (limits), AFD_ERR_CUDA. */
+AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const void* x,
+                                   int64_t x_stride, const void* down, const void* up,
+                                   const int32_t* token_slots, const float* scales,
+                                   const int32_t* row_src, const int32_t* ends, int32_t num_groups,
+                                   int32_t top_k, int64_t num_rows, int32_t num_tokens,
+                                   int32_t num_slots, int32_t rank, int32_t in_features,
+                                   int32_t out_features, void* out, int64_t out_stride,
+                                   afd_stream stream);
 
 /* Library version, (major << 16) | minor. */
 AFD_API int32_t afd_version(void);
