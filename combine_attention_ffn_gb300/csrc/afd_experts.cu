@@ -1,86 +1,450 @@
-// afd_grouped_linear: the experts' matrix product over received rows.
+// afd_grouped_linear: the experts' matrix product over received rows, on the
+// fifth-generation tensor cores.
+//
+// The product is computed transposed, out^T = W x^T: a pair of CTAs holds 256
+// weight rows (the products' M, 128 a CTA) against up to 256 received rows
+// (their N, any multiple of 32). An expert's rows are cut into equal tiles, so
+// a ragged expert wastes at most 31 columns a tile, where rows as M would be
+// padded to 128 or 256 (a prefill bucket has 256 +- 16 rows an expert), and a
+// decode step streams the touched experts' weights past a 32-column product.
+// Each CTA of a pair loads its 128 weight rows and half the received rows, and
+// the tensor cores read both halves: half the L2 traffic of single CTAs.
+//
+// Persistent pairs walk the tiles (expert, weight tile, row tile) with these
+// roles per CTA: warp 0 loads by tiled bulk copies (K blocks of 128 bytes, a
+// ring of stages), warp 1 of the even CTA issues the products, eight warps
+// drain the accumulators, which are double-buffered in TMEM (2 x 256 columns):
+// the next tile's products run while the last one's are stored.
+//
+// Gated: a bulk copy with dimensions (k, half, row) interleaves gate and up
+// rows in shared memory, so the two sums of an output sit in neighbouring
+// lanes and one shuffle brings them together.
+//
+// FP8: each 128-wide K block has scales of its own, so it gets an accumulator
+// of its own; the draining warps add it, scaled, to FP32 sums in registers.
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <climits>
 
 #include "afd.h"
 #include "afd_device.cuh"
 #include "afd_pointers.cuh"
 #include "afd_ragged.cuh"
+#include "afd_tcgen05.cuh"
 
 namespace {
 
+constexpr int kPairRows = 256;    // weight rows of a tile (two CTAs)
+constexpr int kCtaRows = 128;
+constexpr int kTileRows = 256;    // received rows of a tile, at most
+constexpr int kBlockBytes = 128;  // bytes of K per stage and row
+constexpr int kStages = 6;
+constexpr int kHalfBytes = kCtaRows * kBlockBytes;  // one operand of a stage
+constexpr int kStageBytes = 2 * kHalfBytes;
+constexpr int kDrainWarps = 8;
+constexpr int kThreads = 128 + 32 * kDrainWarps;
+constexpr int kColumns = 512;     // all of TMEM: two accumulators
+constexpr int kColStep = 32;      // received rows of a product come in multiples of this
+constexpr int kRowMaps = 4;       // boxes of 16, 32, 64 and 128 received rows
+constexpr int kScalePad = kTileRows + 4;
+
+struct Maps {
+  CUtensorMap w;
+  CUtensorMap x[kRowMaps];
+};
+
 struct ExpertParams {
-  const uint8_t* x;
-  int64_t x_stride;
   const float* x_scale;
-  const uint8_t* w;
   const float* w_scale;
   const int32_t* ends;
-  int32_t G, alpha, R, K, N, gated;
+  int32_t G, alpha, R, K, N;
+  int32_t m_tiles;   // weight tiles of an expert
+  int32_t k_blocks;
+  int32_t vec;       // out takes 4-byte stores of two columns
   uint16_t* out;
   int64_t out_stride;
   int32_t* error;
 };
 
-template <bool FP8>
-__device__ __forceinline__ float element(const uint8_t* p, int64_t i) {
-  if (FP8) {
-    uint32_t h;
-    asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h) : "r"((uint32_t)p[i]));
-    float f;
-    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.f32.f16 %0, lo; }" : "=f"(f) : "r"(h));
-    return f;
+struct Shared {
+  alignas(8) uint64_t full[kStages], empty[kStages], drain_full[2], drain_empty[2];
+  uint32_t tmem;
+  int gave_up;
+  int end[afd::kMaxExperts];
+  int first_tile[afd::kMaxExperts + 1];
+  alignas(16) float scale[2][2][kScalePad];  // [block parity][gate / up][row]
+};
+
+constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + sizeof(Shared);
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+
+struct Tile {
+  int group, m, row, rows, cols;  // cols: rows rounded up to kColStep
+};
+
+__device__ __forceinline__ int row_tiles(int count) { return (count + kTileRows - 1) / kTileRows; }
+
+__device__ __forceinline__ Tile find_tile(const Shared& sh, const ExpertParams& p, int t) {
+  int lo = 0, hi = p.G - 1;  // the last group whose first tile is at or before t, skipping empty ones
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sh.first_tile[mid] <= t) lo = mid; else hi = mid - 1;
   }
-  return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << 16);
+  const int start = lo ? afd::group_start(sh.end[lo - 1], p.alpha, p.R) : 0;
+  const int count = sh.end[lo] - start, n = row_tiles(count);
+  const int i = t - sh.first_tile[lo];
+  const int width = ((count + n - 1) / n + kColStep - 1) & -kColStep;
+  Tile tile;
+  tile.group = lo;
+  tile.m = i / n;
+  const int off = (i - tile.m * n) * width;
+  tile.row = start + off;
+  tile.rows = min(width, count - off);  // at least 1: (n - 1) * width < count
+  tile.cols = (tile.rows + kColStep - 1) & -kColStep;
+  return tile;
 }
 
-// 64 rows x 64 columns a block, 4 x 4 sums a thread, 32 of K at a time.
-template <bool FP8>
-__global__ void __launch_bounds__(256) grouped_simple_kernel(const ExpertParams p) {
-  __shared__ float xs[32][65], ws[2][32][65];
-  const int n0 = blockIdx.x * 64, g = blockIdx.y;
-  const int start = g ? afd::group_start(p.ends[g - 1], p.alpha, p.R) : 0, end = afd::group_end(p.ends[g], p.R);
-  const int W = p.gated ? 2 * p.N : p.N, halves = p.gated ? 2 : 1;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int r0 = start + blockIdx.z * 64; r0 < end; r0 += gridDim.z * 64) {
-    float acc[2][4][4] = {};
-    for (int k0 = 0; k0 < p.K; k0 += 32) {
-      for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-        const int k = k0 + (i & 31), r = r0 + (i >> 5), n = n0 + (i >> 5);
-        float v = 0.f;
-        if (k < p.K && r < end) {
-          v = element<FP8>(p.x, r * p.x_stride + k);
-          if (FP8) v *= p.x_scale[(int64_t)r * (p.K / 128) + k / 128];
-        }
-        xs[i & 31][i >> 5] = v;
-        for (int h = 0; h < halves; ++h) {
-          float u = 0.f;
-          if (k < p.K && n < p.N) {
-            const int64_t row = (int64_t)g * W + h * p.N + n;
-            u = element<FP8>(p.w, row * p.K + k);
-            if (FP8) u *= p.w_scale[row / 128 * (p.K / 128) + k / 128];
-          }
-          ws[h][i & 31][i >> 5] = u;
-        }
-      }
-      __syncthreads();
-      for (int k = 0; k < 32; ++k)
-        for (int h = 0; h < halves; ++h)
-          for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) acc[h][i][j] = fmaf(xs[k][ty * 4 + i], ws[h][k][tx * 4 + j], acc[h][i][j]);
-      __syncthreads();
+// Stores 16 received rows x 32 lanes of sums: lane = weight row, v[i] = row i.
+// Pairs of rows are exchanged between neighbouring lanes, so that each lane
+// stores two columns of one row (plain), or completes one output (gated).
+template <bool GATED>
+__device__ __forceinline__ void store16(const ExpertParams& p, const Tile& tile, int c0, int n0, int lane,
+                                        const float (&v)[16]) {
+  const int odd = lane & 1;
+  const int left = tile.rows - c0;
+  uint16_t* out = p.out + (int64_t)(tile.row + c0) * p.out_stride;
+  if (GATED) {
+    const int f = n0 + (lane >> 1);
+    float a[8];  // outputs of row 2 i + odd
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+      a[i] = odd ? afd::silu_mul(other, v[2 * i + 1]) : afd::silu_mul(v[2 * i], other);
     }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int r = r0 + ty * 4 + i, n = n0 + tx * 4 + j;
-        if (r < end && n < p.N)
-          p.out[r * p.out_stride + n] =
-              (uint16_t)afd::pack_bf16(p.gated ? afd::silu_mul(acc[0][i][j], acc[1][i][j]) : acc[0][i][j], 0.f);
+    if (p.vec) {
+      const int upper = (lane >> 1) & 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float other = __shfl_xor_sync(0xffffffffu, upper ? a[2 * i] : a[2 * i + 1], 2);
+        const int r = 4 * i + 2 * upper + odd;
+        const uint32_t two = upper ? afd::pack_bf16(other, a[2 * i + 1]) : afd::pack_bf16(a[2 * i], other);
+        if (r < left && f < p.N) *reinterpret_cast<uint32_t*>(out + r * p.out_stride + (f & ~1)) = two;
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (2 * i + odd < left && f < p.N)
+          out[(2 * i + odd) * p.out_stride + f] = (uint16_t)afd::pack_bf16(a[i], 0.f);
+    }
+  } else {
+    const int n = n0 + lane;
+    if (p.vec) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float other = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+        const uint32_t two = odd ? afd::pack_bf16(other, v[2 * i + 1]) : afd::pack_bf16(v[2 * i], other);
+        if (2 * i + odd < left && n < p.N)
+          *reinterpret_cast<uint32_t*>(out + (2 * i + odd) * p.out_stride + (n & ~1)) = two;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < left && n < p.N) out[i * p.out_stride + n] = (uint16_t)afd::pack_bf16(v[i], 0.f);
+    }
   }
+}
+
+// A barrier of the draining warps that also tells whether any thread says so.
+__device__ __forceinline__ bool any_of_drain_warps(bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.or.pred p, 1, %2, q;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(any)
+      : "r"((uint32_t)mine), "n"(32 * kDrainWarps)
+      : "memory");
+  return any != 0;
+}
+
+template <bool FP8, bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    grouped_linear_kernel(const __grid_constant__ Maps maps, const ExpertParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t smem = (afd::smem_u32(smem_raw) + 1023) & ~1023u;
+  Shared& sh = *reinterpret_cast<Shared*>(smem_raw + (smem - afd::smem_u32(smem_raw)) + kStages * kStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = afd::cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t full = afd::smem_u32(sh.full), empty = afd::smem_u32(sh.empty);
+  const uint32_t drain_full = afd::smem_u32(sh.drain_full), drain_empty = afd::smem_u32(sh.drain_empty);
+
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      afd::mbar_init(full + 8 * i, 1);
+      afd::mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      afd::mbar_init(drain_full + 8 * i, 1);
+      afd::mbar_init(drain_empty + 8 * i, 2 * kDrainWarps);
+    }
+    sh.gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) afd::tmem_alloc_pair(afd::smem_u32(&sh.tmem), kColumns);
+  // every group's end, then the prefix sums of the groups' tiles
+  for (int g = threadIdx.x; g < p.G; g += kThreads) sh.end[g] = afd::group_end(p.ends[g], p.R);
+  __syncthreads();
+  if (warp == 2) {
+    int carry = 0;
+    for (int g0 = 0; g0 < p.G; g0 += 32) {
+      const int g = g0 + lane;
+      int tiles = 0;
+      if (g < p.G) {
+        const int start = g ? afd::group_start(sh.end[g - 1], p.alpha, p.R) : 0;
+        tiles = row_tiles(max(sh.end[g] - start, 0)) * p.m_tiles;
+      }
+      const int incl = afd::warp_inclusive_scan(tiles);
+      if (g < p.G) sh.first_tile[g] = carry + incl - tiles;
+      carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) sh.first_tile[p.G] = carry;
+  }
+  afd::tcgen05_fence_before();
+  __syncthreads();
+  afd::cluster_sync_all();
+  afd::tcgen05_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int tiles = sh.first_tile[p.G];
+  volatile int* gave_up = &sh.gave_up;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loads
+    if (lane == 0) {
+      uint64_t keep, once;
+      asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+      asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+      const uint32_t lead_full = afd::map_to_rank(full, 0);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles; t += pairs) {
+        const Tile tile = find_tile(sh, p, t);
+        const int half = tile.cols >> 1;
+        const int row = tile.row + (int)rank * half;
+        const uint32_t bytes = 2 * (kHalfBytes + half * kBlockBytes);
+        // this weight tile is read again if the expert has more row tiles
+        const uint64_t w_policy = sh.first_tile[tile.group + 1] - sh.first_tile[tile.group] == p.m_tiles
+                                      ? once : keep;
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+          const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+          if (!(ok = afd::mbar_wait(empty + 8 * s, ph ^ 1, gave_up))) break;
+          if (rank == 0) afd::mbar_expect(full + 8 * s, bytes);
+          const uint32_t a = smem + s * kStageBytes, b = a + kHalfBytes, bar = lead_full + 8 * s;
+          const int k = kb * (FP8 ? 128 : 64);
+          if (GATED)
+            afd::tma_load_4d(a, &maps.w, bar, k, 0, tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2), tile.group, w_policy);
+          else
+            afd::tma_load_3d(a, &maps.w, bar, k, tile.m * kPairRows + (int)rank * kCtaRows, tile.group, w_policy);
+          int off = 0;
+#pragma unroll
+          for (int i = kRowMaps - 1; i >= 0; --i) {
+            const int box = 16 << i;
+            if (half & box) {
+              afd::tma_load_2d(b + off * kBlockBytes, &maps.x[i], bar, k, row + off, keep);
+              off += box;
+            }
+          }
+        }
+      }
+      // The pair's last products have read this CTA's operands.
+      for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
+        ok = afd::mbar_wait(empty + 8 * (i % kStages), (i / kStages) & 1, gave_up);
+      if (!ok && rank == 0) {
+        // Copies in flight count on this CTA's barriers: wait for the last ring of them.
+        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
+          const unsigned long long t0 = afd::global_timer_ns();
+          while (!afd::mbar_try(full + 8 * (i % kStages), (i / kStages) & 1) && afd::global_timer_ns() - t0 < 1000000) {
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- products
+    if (rank == 0 && lane == 0) {
+      uint32_t it = 0, unit = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles; t += pairs) {
+        const Tile tile = find_tile(sh, p, t);
+        const uint32_t idesc = afd::instr_desc(FP8, kPairRows, tile.cols);
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+          const bool opens = FP8 || kb == 0, closes = FP8 || kb == p.k_blocks - 1;
+          if (opens) {
+            if (!(ok = afd::mbar_wait(drain_empty + 8 * (unit & 1), ((unit >> 1) & 1) ^ 1, gave_up))) break;
+          }
+          const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+          if (!(ok = afd::mbar_wait(full + 8 * s, ph, gave_up))) break;
+          afd::tcgen05_fence_after();
+          const uint64_t a = afd::operand_desc(smem + s * kStageBytes);
+          const uint64_t b = afd::operand_desc(smem + s * kStageBytes + kHalfBytes);
+          const uint32_t d = tmem + (unit & 1) * (kColumns / 2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // 32 bytes of K each
+            afd::mma_pair<FP8>(d, a + 2 * i, b + 2 * i, idesc, !(opens && i == 0));
+          afd::mma_commit_pair(empty + 8 * s);
+          if (closes) afd::mma_commit_pair(drain_full + 8 * (unit++ & 1));
+        }
+      }
+      if (!ok) {
+        // let the products in flight finish before TMEM is freed
+        const unsigned long long t0 = afd::global_timer_ns();
+        while (afd::global_timer_ns() - t0 < 1000000) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ----------------------------------------------------------- accumulators
+    const int q = warp & 3, h = (warp - 4) >> 2;  // lanes 32 q .. of TMEM; every second 16 columns
+    const uint32_t lead_empty = afd::map_to_rank(drain_empty, 0);
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+    uint32_t unit = 0;
+    bool ok = true, stop = false;
+    for (int t = pair; !stop && t < tiles; t += pairs) {
+      const Tile tile = find_tile(sh, p, t);
+      const int n0 = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) + 16 * q
+                           : tile.m * kPairRows + (int)rank * kCtaRows + 32 * q;
+      if (!FP8) {
+        ok = __all_sync(0xffffffffu, afd::mbar_wait(drain_full + 8 * (unit & 1), (unit >> 1) & 1, gave_up));
+        if (!ok) break;
+        afd::tcgen05_fence_after();
+        const uint32_t acc = lanes + (unit & 1) * (kColumns / 2);
+        for (int c = 16 * h; c < tile.cols; c += 32) {
+          float v[16];
+          afd::tmem_load16(acc + c, v);
+          afd::tmem_wait_loads();
+          afd::tmem_loaded(v);
+          store16<GATED>(p, tile, c, n0, lane, v);
+        }
+        afd::tcgen05_fence_before();
+        __syncwarp();
+        if (lane == 0) afd::mbar_arrive_cluster(lead_empty + 8 * (unit & 1));
+        ++unit;
+      } else {
+        // This thread's share of the scales: received row `mine` of the tile,
+        // and the weight blocks of this CTA's rows (gate and up; equal if plain).
+        const int mine = threadIdx.x - 128;
+        const float* xs = p.x_scale + (int64_t)min(tile.row + mine, p.R - 1) * p.k_blocks;
+        const int64_t w_rows = (int64_t)(GATED ? 2 : 1) * p.N / 128;
+        const int f = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) : tile.m * kPairRows + (int)rank * kCtaRows;
+        const int fb = min(f, p.N - 1) / 128;
+        const float* wg = p.w_scale + (tile.group * w_rows + fb) * p.k_blocks;
+        const float* wu = GATED ? wg + (int64_t)(p.N / 128) * p.k_blocks : wg;
+        float sum[8][16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
+        float next_x = mine < tile.rows ? xs[0] : 0.f, next_g = wg[0], next_u = wu[0];
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++unit) {
+          float (&scale)[2][kScalePad] = sh.scale[unit & 1];
+          scale[0][mine] = next_x * next_g;
+          if (GATED) scale[1][mine] = next_x * next_u;
+          if (kb + 1 < p.k_blocks) {
+            next_x = mine < tile.rows ? xs[kb + 1] : 0.f;
+            next_g = wg[kb + 1];
+            next_u = wu[kb + 1];
+          }
+          // The barrier orders this block's scales before their use, and the
+          // use of the buffer's last ones (two blocks ago) before this write.
+          // If a wait of any of these warps gave up, all stop here.
+          if ((stop = any_of_drain_warps(!ok))) break;
+          ok = __all_sync(0xffffffffu, afd::mbar_wait(drain_full + 8 * (unit & 1), (unit >> 1) & 1, gave_up));
+          if (ok) {
+            afd::tcgen05_fence_after();
+            const uint32_t acc = lanes + (unit & 1) * (kColumns / 2);
+            const float* sc = scale[GATED ? lane & 1 : 0];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int c = 32 * i + 16 * h;
+              if (c < tile.cols) {
+                float v[16];
+                afd::tmem_load16(acc + c, v);
+                afd::tmem_wait_loads();
+                afd::tmem_loaded(v);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                  const float4 s4 = *reinterpret_cast<const float4*>(sc + c + j);
+                  sum[i][j] = fmaf(v[j], s4.x, sum[i][j]);
+                  sum[i][j + 1] = fmaf(v[j + 1], s4.y, sum[i][j + 1]);
+                  sum[i][j + 2] = fmaf(v[j + 2], s4.z, sum[i][j + 2]);
+                  sum[i][j + 3] = fmaf(v[j + 3], s4.w, sum[i][j + 3]);
+                }
+              }
+            }
+            afd::tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0) afd::mbar_arrive_cluster(lead_empty + 8 * (unit & 1));
+          }
+        }
+        if (ok && !stop) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (32 * i + 16 * h < tile.cols) store16<GATED>(p, tile, 32 * i + 16 * h, n0, lane, sum[i]);
+        }
+      }
+    }
+  }
+  // Neither CTA leaves while the other may signal it or read its operands.
+  __syncthreads();
+  if (threadIdx.x == 0 && *gave_up && p.error) *p.error = AFD_ERR_TIMEOUT;
+  afd::tcgen05_fence_before();
+  afd::cluster_sync_all();
+  afd::tcgen05_fence_after();
+  if (warp == 1) afd::tmem_free_pair(tmem, kColumns);
+}
+
+// ---------------------------------------------------------------------- host
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's encoder, looked up once (a library without a driver loads).
+EncodeTiled encoder() {
+  static std::atomic<EncodeTiled> cached{nullptr};
+  EncodeTiled f = cached.load(std::memory_order_acquire);
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  f = reinterpret_cast<EncodeTiled>(p);
+  cached.store(f, std::memory_order_release);
+  return f;
+}
+
+bool encode(EncodeTiled f, CUtensorMap* map, bool fp8, uint32_t rank, const void* base, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return f(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base),
+           dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP8, bool GATED>
+cudaError_t launch_grouped(const Maps& maps, const ExpertParams& p, int pairs, cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(grouped_linear_kernel<FP8, GATED>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, grouped_linear_kernel<FP8, GATED>, maps, p);
 }
 
 // Device memory of the current device (bulk copies read it).
@@ -122,14 +486,46 @@ extern "C" AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride
   if (!on_device(x, dev) || !on_device(weight, dev) || !on_device(ends, dev) || !on_device(out, dev) ||
       (fp8 && (!on_device(x_scale, dev) || !on_device(weight_scale, dev))) || (error && !on_device(error, dev)))
     return AFD_ERR_ARG;
-  ExpertParams p = {static_cast<const uint8_t*>(x), x_stride, x_scale, static_cast<const uint8_t*>(weight), weight_scale,
-                    ends, num_groups, expert_alignment, (int32_t)num_rows, K, N, gated,
-                    static_cast<uint16_t*>(out), out_stride, error};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((N + 63) / 64, num_groups, 4);
-  cfg.blockDim = dim3(256);
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = fp8 ? cudaLaunchKernelEx(&cfg, grouped_simple_kernel<true>, p)
-                            : cudaLaunchKernelEx(&cfg, grouped_simple_kernel<false>, p);
+  EncodeTiled enc = encoder();
+  int sms = 0;
+  if (!enc || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return AFD_ERR_CUDA;
+
+  const int W = gated ? 2 * N : N, block = kBlockBytes / elt;
+  Maps maps;
+  const cuuint64_t k_bytes = (cuuint64_t)K * elt;
+  bool ok;
+  if (gated) {
+    const cuuint64_t dims[4] = {(cuuint64_t)K, 2, (cuuint64_t)N, (cuuint64_t)num_groups};
+    const cuuint64_t strides[3] = {k_bytes * N, k_bytes, k_bytes * W};
+    const cuuint32_t box[4] = {(cuuint32_t)block, 2, kCtaRows / 2, 1};
+    ok = encode(enc, &maps.w, fp8, 4, weight, dims, strides, box);
+  } else {
+    const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)num_groups};
+    const cuuint64_t strides[2] = {k_bytes, k_bytes * N};
+    const cuuint32_t box[3] = {(cuuint32_t)block, kCtaRows, 1};
+    ok = encode(enc, &maps.w, fp8, 3, weight, dims, strides, box);
+  }
+  for (int i = 0; ok && i < kRowMaps; ++i) {
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)num_rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)x_stride * elt};
+    const cuuint32_t box[2] = {(cuuint32_t)block, 16u << i};
+    ok = encode(enc, &maps.x[i], fp8, 2, x, dims, strides, box);
+  }
+  if (!ok) return AFD_ERR_CUDA;
+
+  ExpertParams p = {};
+  p.x_scale = x_scale, p.w_scale = weight_scale, p.ends = ends;
+  p.G = num_groups, p.alpha = expert_alignment, p.R = (int32_t)num_rows, p.K = K, p.N = N;
+  p.m_tiles = (W + kPairRows - 1) / kPairRows;
+  p.k_blocks = (K + block - 1) / block;
+  p.out = static_cast<uint16_t*>(out), p.out_stride = out_stride, p.error = error;
+  p.vec = N % 2 == 0 && out_stride % 2 == 0 && afd::aligned_to(out, 4);
+  // no more pairs than there can be tiles
+  const int64_t row_tiles_max = (num_groups < num_rows ? num_groups : num_rows) + num_rows / kTileRows;
+  const int64_t most = row_tiles_max * p.m_tiles;
+  const int pairs = (int)(most < sms / 2 ? most : sms / 2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = fp8 ? (gated ? launch_grouped<true, true>(maps, p, pairs, s) : launch_grouped<true, false>(maps, p, pairs, s))
+                            : (gated ? launch_grouped<false, true>(maps, p, pairs, s) : launch_grouped<false, false>(maps, p, pairs, s));
   return e == cudaSuccess ? AFD_OK : AFD_ERR_CUDA;
 }
