@@ -49,7 +49,7 @@ constexpr int kDrainWarps = 8;
 constexpr int kThreads = 128 + 32 * kDrainWarps;
 constexpr int kColumns = 512;     // all of TMEM: two accumulators
 constexpr int kColStep = 32;      // received rows of a product come in multiples of this
-constexpr int kRowMaps = 4;       // boxes of 16, 32, 64 and 128 received rows
+constexpr int kRowMaps = 8;       // boxes of 16, 32, .. 128 received rows: one copy a stage, whatever the tile
 constexpr int kScalePad = kTileRows + 4;
 
 struct Maps {
@@ -222,58 +222,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
-    if (lane == 0) {
-      uint64_t keep, once;
-      asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
-      asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-      const uint32_t lead_full = afd::map_to_rank(full, 0);
-      uint32_t it = 0;
-      bool ok = true;
-      for (int t = pair; ok && t < tiles; t += pairs) {
-        const Tile tile = find_tile(sh, p, t);
-        const int half = tile.cols >> 1;
-        const int row = tile.row + (int)rank * half;
-        const uint32_t bytes = 2 * (kHalfBytes + half * kBlockBytes);
-        // this weight tile is read again if the expert has more row tiles
-        const uint64_t w_policy = sh.first_tile[tile.group + 1] - sh.first_tile[tile.group] == p.m_tiles
-                                      ? once : keep;
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-          const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-          if (!(ok = afd::mbar_wait(empty + 8 * s, ph ^ 1, gave_up))) break;
+    // The whole warp walks the loop and one elected lane issues: with a single
+    // lane in it the compiler cannot keep the operands in uniform registers,
+    // and an issue takes 100 clocks and more.
+    uint64_t keep, once;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+    const uint32_t lead_full = afd::map_to_rank(full, 0);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      const Tile tile = find_tile(sh, p, t);
+      const int half = tile.cols >> 1;
+      const int row = tile.row + (int)rank * half;
+      const uint32_t bytes = 2 * (kHalfBytes + half * kBlockBytes);
+      const CUtensorMap* x_map = &maps.x[half / 16 - 1];
+      // this weight tile is read again if the expert has more row tiles
+      const uint64_t w_policy = sh.first_tile[tile.group + 1] - sh.first_tile[tile.group] == p.m_tiles ? once : keep;
+      const int w_row = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) : tile.m * kPairRows + (int)rank * kCtaRows;
+      for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+        const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+        if (!(ok = __all_sync(0xffffffffu, afd::mbar_wait(empty + 8 * s, ph ^ 1, gave_up)))) break;
+        const uint32_t a = smem + s * kStageBytes, b = a + kHalfBytes, bar = lead_full + 8 * s;
+        const int k = kb * (FP8 ? 128 : 64);
+        if (afd::elect_one()) {
           if (rank == 0) afd::mbar_expect(full + 8 * s, bytes);
-          const uint32_t a = smem + s * kStageBytes, b = a + kHalfBytes, bar = lead_full + 8 * s;
-          const int k = kb * (FP8 ? 128 : 64);
           if (GATED)
-            afd::tma_load_4d(a, &maps.w, bar, k, 0, tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2), tile.group, w_policy);
+            afd::tma_load_4d(a, &maps.w, bar, k, 0, w_row, tile.group, w_policy);
           else
-            afd::tma_load_3d(a, &maps.w, bar, k, tile.m * kPairRows + (int)rank * kCtaRows, tile.group, w_policy);
-          int off = 0;
-#pragma unroll
-          for (int i = kRowMaps - 1; i >= 0; --i) {
-            const int box = 16 << i;
-            if (half & box) {
-              afd::tma_load_2d(b + off * kBlockBytes, &maps.x[i], bar, k, row + off, keep);
-              off += box;
-            }
-          }
+            afd::tma_load_3d(a, &maps.w, bar, k, w_row, tile.group, w_policy);
+          afd::tma_load_2d(b, x_map, bar, k, row, keep);
         }
+        __syncwarp();
       }
-      // The pair's last products have read this CTA's operands.
-      for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
-        ok = afd::mbar_wait(empty + 8 * (i % kStages), (i / kStages) & 1, gave_up);
-      if (!ok && rank == 0) {
-        // Copies in flight count on this CTA's barriers: wait for the last ring of them.
-        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
-          const unsigned long long t0 = afd::global_timer_ns();
-          while (!afd::mbar_try(full + 8 * (i % kStages), (i / kStages) & 1) && afd::global_timer_ns() - t0 < 1000000) {
-          }
+    }
+    // The pair's last products have read this CTA's operands.
+    for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
+      ok = __all_sync(0xffffffffu, afd::mbar_wait(empty + 8 * (i % kStages), (i / kStages) & 1, gave_up));
+    if (!ok && rank == 0) {
+      // Copies in flight count on this CTA's barriers: wait for the last ring of them.
+      for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
+        const long long t0 = clock64();
+        while (!afd::mbar_try(full + 8 * (i % kStages), (i / kStages) & 1) && clock64() - t0 < 2000000) {
         }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------- products
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       uint32_t it = 0, unit = 0;
       bool ok = true;
       for (int t = pair; ok && t < tiles; t += pairs) {
@@ -282,25 +279,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
           const bool opens = FP8 || kb == 0, closes = FP8 || kb == p.k_blocks - 1;
           if (opens) {
-            if (!(ok = afd::mbar_wait(drain_empty + 8 * (unit & 1), ((unit >> 1) & 1) ^ 1, gave_up))) break;
+            ok = __all_sync(0xffffffffu, afd::mbar_wait(drain_empty + 8 * (unit & 1), ((unit >> 1) & 1) ^ 1, gave_up));
+            if (!ok) break;
           }
           const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-          if (!(ok = afd::mbar_wait(full + 8 * s, ph, gave_up))) break;
+          if (!(ok = __all_sync(0xffffffffu, afd::mbar_wait(full + 8 * s, ph, gave_up)))) break;
           afd::tcgen05_fence_after();
           const uint64_t a = afd::operand_desc(smem + s * kStageBytes);
           const uint64_t b = afd::operand_desc(smem + s * kStageBytes + kHalfBytes);
           const uint32_t d = tmem + (unit & 1) * (kColumns / 2);
+          if (afd::elect_one()) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)  // 32 bytes of K each
-            afd::mma_pair<FP8>(d, a + 2 * i, b + 2 * i, idesc, !(opens && i == 0));
-          afd::mma_commit_pair(empty + 8 * s);
-          if (closes) afd::mma_commit_pair(drain_full + 8 * (unit++ & 1));
+            for (int i = 0; i < 4; ++i)  // 32 bytes of K each
+              afd::mma_pair<FP8>(d, a + 2 * i, b + 2 * i, idesc, !(opens && i == 0));
+            afd::mma_commit_pair(empty + 8 * s);
+            if (closes) afd::mma_commit_pair(drain_full + 8 * (unit & 1));
+          }
+          __syncwarp();
+          if (closes) ++unit;
         }
       }
       if (!ok) {
         // let the products in flight finish before TMEM is freed
-        const unsigned long long t0 = afd::global_timer_ns();
-        while (afd::global_timer_ns() - t0 < 1000000) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
         }
       }
     }
@@ -508,7 +510,7 @@ extern "C" AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride
   for (int i = 0; ok && i < kRowMaps; ++i) {
     const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)num_rows};
     const cuuint64_t strides[1] = {(cuuint64_t)x_stride * elt};
-    const cuuint32_t box[2] = {(cuuint32_t)block, 16u << i};
+    const cuuint32_t box[2] = {(cuuint32_t)block, 16u * (i + 1)};
     ok = encode(enc, &maps.x[i], fp8, 2, x, dims, strides, box);
   }
   if (!ok) return AFD_ERR_CUDA;

@@ -52,7 +52,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n.reg .pred p;\n"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       "selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
@@ -60,17 +60,18 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Waits for a barrier's phase, at most kWaitNs. False: it gave up, or
-// another wait of this CTA did (`gave_up`, in shared memory).
-constexpr unsigned long long kWaitNs = 2000000000ull;
+// Waits for a barrier's phase, at most kWaitCycles of this SM's clock (about
+// two seconds). False: it gave up, or another wait of this CTA did
+// (`gave_up`, in shared memory).
+constexpr long long kWaitCycles = 4000000000ll;
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
   if (mbar_try(bar, parity)) return true;
-  const unsigned long long t0 = global_timer_ns();
+  const long long t0 = clock64();
   for (;;) {
     for (int i = 0; i < 64; ++i)
       if (mbar_try(bar, parity)) return true;
     if (*gave_up) return false;
-    if (global_timer_ns() - t0 > kWaitNs) {
+    if (clock64() - t0 > kWaitCycles) {
       *gave_up = 1;
       return false;
     }
