@@ -21,7 +21,11 @@
 // lanes and one shuffle brings them together.
 //
 // FP8: each 128-wide K block has scales of its own, so it gets an accumulator
-// of its own; the draining warps add it, scaled, to FP32 sums in registers.
+// of its own; the draining warps add it, scaled, to FP32 sums in registers:
+// one multiply-add a value, with x_scale * weight_scale multiplied once per
+// row and block by warps 2 and 3, which keep a ring of them in shared memory.
+// 128 sums a thread need more than an even share of the registers, so the
+// other warps hand theirs over.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -45,12 +49,20 @@ constexpr int kBlockBytes = 128;  // bytes of K per stage and row
 constexpr int kStages = 6;
 constexpr int kHalfBytes = kCtaRows * kBlockBytes;  // one operand of a stage
 constexpr int kStageBytes = 2 * kHalfBytes;
-constexpr int kDrainWarps = 8;
+constexpr int kDrainWarps = 16;
+constexpr int kDrainParts = kDrainWarps / 4;  // warps that share 32 lanes of TMEM, 16 columns each in turn
+constexpr int kDrainSteps = kTileRows / (16 * kDrainParts);
 constexpr int kThreads = 128 + 32 * kDrainWarps;
 constexpr int kColumns = 512;     // all of TMEM: two accumulators
 constexpr int kColStep = 32;      // received rows of a product come in multiples of this
 constexpr int kRowMaps = 8;       // boxes of 16, 32, .. 128 received rows: one copy a stage, whatever the tile
-constexpr int kScalePad = kTileRows + 4;
+constexpr int kScaleStages = 8;   // ring of scales (FP8)
+constexpr int kScaleThreads = 64; // warps 2 and 3
+constexpr int kScaleRows = kTileRows / kScaleThreads;
+constexpr int kScaleAhead = 4;    // blocks whose scales are loaded together
+// Registers a thread after the hand-over (FP8): 128 x 64 + 512 x 104, at most
+// what the block is launched with (checked before the first launch).
+constexpr int kFrontRegs = 64, kDrainRegs = 104;
 
 struct Maps {
   CUtensorMap w;
@@ -70,13 +82,18 @@ struct ExpertParams {
   int32_t* error;
 };
 
+struct alignas(16) BlockScales {
+  float s[2][kTileRows + 4];  // [gate / up][received row]; plain uses the first
+};
+
 struct Shared {
   alignas(8) uint64_t full[kStages], empty[kStages], drain_full[2], drain_empty[2];
+  uint64_t scale_full[kScaleStages], scale_empty[kScaleStages];
   uint32_t tmem;
   int gave_up;
   int end[afd::kMaxExperts];
   int first_tile[afd::kMaxExperts + 1];
-  alignas(16) float scale[2][2][kScalePad];  // [block parity][gate / up][row]
+  BlockScales scale[kScaleStages];
 };
 
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + sizeof(Shared);
@@ -158,17 +175,6 @@ __device__ __forceinline__ void store16(const ExpertParams& p, const Tile& tile,
   }
 }
 
-// A barrier of the draining warps that also tells whether any thread says so.
-__device__ __forceinline__ bool any_of_drain_warps(bool mine) {
-  uint32_t any;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.or.pred p, 1, %2, q;\nselp.u32 %0, 1, 0, p;\n}"
-      : "=r"(any)
-      : "r"((uint32_t)mine), "n"(32 * kDrainWarps)
-      : "memory");
-  return any != 0;
-}
-
 template <bool FP8, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_linear_kernel(const __grid_constant__ Maps maps, const ExpertParams p) {
@@ -180,6 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const uint32_t full = afd::smem_u32(sh.full), empty = afd::smem_u32(sh.empty);
   const uint32_t drain_full = afd::smem_u32(sh.drain_full), drain_empty = afd::smem_u32(sh.drain_empty);
+  const uint32_t scale_full = afd::smem_u32(sh.scale_full), scale_empty = afd::smem_u32(sh.scale_empty);
 
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -189,6 +196,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       afd::mbar_init(drain_full + 8 * i, 1);
       afd::mbar_init(drain_empty + 8 * i, 2 * kDrainWarps);
+    }
+    for (int i = 0; FP8 && i < kScaleStages; ++i) {
+      afd::mbar_init(scale_full + 8 * i, kScaleThreads);
+      afd::mbar_init(scale_empty + 8 * i, kDrainWarps);
     }
     sh.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -220,6 +231,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int tiles = sh.first_tile[p.G];
   volatile int* gave_up = &sh.gave_up;
 
+  if (warp < 4) {
+  if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFrontRegs));
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
     // The whole warp walks the loop and one elected lane issues: with a single
@@ -307,14 +320,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else {
+    // --------------------------------------------------------------- scales
+    if (FP8) {
+      const int u = threadIdx.x - 64;
+      const int64_t w_rows = (int64_t)(GATED ? 2 : 1) * p.N / 128;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles; t += pairs) {
+        const Tile tile = find_tile(sh, p, t);
+        const float* xs = p.x_scale + (int64_t)(tile.row + u) * p.k_blocks;
+        // the weight block of this CTA's rows (the last one for rows past N, which are not stored)
+        const int f = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) : tile.m * kPairRows + (int)rank * kCtaRows;
+        const float* wg = p.w_scale + (tile.group * w_rows + min(f, p.N - 1) / 128) * p.k_blocks;
+        const float* wu = wg + (int64_t)(p.N / 128) * p.k_blocks;
+        // kScaleAhead blocks are loaded at a time; the ring is twice as long,
+        // so the loads of the next ones overlap the use of these
+        for (int kb0 = 0; ok && kb0 < p.k_blocks; kb0 += kScaleAhead) {
+          float x[kScaleAhead][kScaleRows], w[kScaleAhead][2];
+#pragma unroll
+          for (int j = 0; j < kScaleAhead; ++j) {
+            const int kb = min(kb0 + j, p.k_blocks - 1);
+            w[j][0] = wg[kb];
+            w[j][1] = GATED ? wu[kb] : 0.f;
+#pragma unroll
+            for (int i = 0; i < kScaleRows; ++i)
+              x[j][i] = u + kScaleThreads * i < tile.rows ? xs[(int64_t)kScaleThreads * i * p.k_blocks + kb] : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < kScaleAhead; ++j) {
+            if (ok && kb0 + j < p.k_blocks) {
+              const uint32_t s = it % kScaleStages, ph = (it / kScaleStages) & 1;
+              ok = __all_sync(0xffffffffu, afd::mbar_wait(scale_empty + 8 * s, ph ^ 1, gave_up));
+              if (ok) {
+                ++it;
+#pragma unroll
+                for (int i = 0; i < kScaleRows; ++i) {
+                  sh.scale[s].s[0][u + kScaleThreads * i] = x[j][i] * w[j][0];
+                  if (GATED) sh.scale[s].s[1][u + kScaleThreads * i] = x[j][i] * w[j][1];
+                }
+                afd::mbar_arrive(scale_full + 8 * s);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+  } else {
     // ----------------------------------------------------------- accumulators
-    const int q = warp & 3, h = (warp - 4) >> 2;  // lanes 32 q .. of TMEM; every second 16 columns
+    if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
+    const int q = warp & 3, h = (warp - 4) >> 2;  // lanes 32 q .. of TMEM; every fourth 16 columns
     const uint32_t lead_empty = afd::map_to_rank(drain_empty, 0);
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
     uint32_t unit = 0;
-    bool ok = true, stop = false;
-    for (int t = pair; !stop && t < tiles; t += pairs) {
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += pairs) {
       const Tile tile = find_tile(sh, p, t);
       const int n0 = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) + 16 * q
                            : tile.m * kPairRows + (int)rank * kCtaRows + 32 * q;
@@ -323,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) break;
         afd::tcgen05_fence_after();
         const uint32_t acc = lanes + (unit & 1) * (kColumns / 2);
-        for (int c = 16 * h; c < tile.cols; c += 32) {
+        for (int c = 16 * h; c < tile.cols; c += 16 * kDrainParts) {
           float v[16];
           afd::tmem_load16(acc + c, v);
           afd::tmem_wait_loads();
@@ -335,66 +396,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) afd::mbar_arrive_cluster(lead_empty + 8 * (unit & 1));
         ++unit;
       } else {
-        // This thread's share of the scales: received row `mine` of the tile,
-        // and the weight blocks of this CTA's rows (gate and up; equal if plain).
-        const int mine = threadIdx.x - 128;
-        const float* xs = p.x_scale + (int64_t)min(tile.row + mine, p.R - 1) * p.k_blocks;
-        const int64_t w_rows = (int64_t)(GATED ? 2 : 1) * p.N / 128;
-        const int f = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) : tile.m * kPairRows + (int)rank * kCtaRows;
-        const int fb = min(f, p.N - 1) / 128;
-        const float* wg = p.w_scale + (tile.group * w_rows + fb) * p.k_blocks;
-        const float* wu = GATED ? wg + (int64_t)(p.N / 128) * p.k_blocks : wg;
-        float sum[8][16];
+        float sum[kDrainSteps][16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < kDrainSteps; ++i)
 #pragma unroll
           for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
-        float next_x = mine < tile.rows ? xs[0] : 0.f, next_g = wg[0], next_u = wu[0];
         for (int kb = 0; kb < p.k_blocks; ++kb, ++unit) {
-          float (&scale)[2][kScalePad] = sh.scale[unit & 1];
-          scale[0][mine] = next_x * next_g;
-          if (GATED) scale[1][mine] = next_x * next_u;
-          if (kb + 1 < p.k_blocks) {
-            next_x = mine < tile.rows ? xs[kb + 1] : 0.f;
-            next_g = wg[kb + 1];
-            next_u = wu[kb + 1];
-          }
-          // The barrier orders this block's scales before their use, and the
-          // use of the buffer's last ones (two blocks ago) before this write.
-          // If a wait of any of these warps gave up, all stop here.
-          if ((stop = any_of_drain_warps(!ok))) break;
-          ok = __all_sync(0xffffffffu, afd::mbar_wait(drain_full + 8 * (unit & 1), (unit >> 1) & 1, gave_up));
-          if (ok) {
-            afd::tcgen05_fence_after();
-            const uint32_t acc = lanes + (unit & 1) * (kColumns / 2);
-            const float* sc = scale[GATED ? lane & 1 : 0];
+          const uint32_t s = unit % kScaleStages;
+          ok = __all_sync(0xffffffffu, afd::mbar_wait(scale_full + 8 * s, (unit / kScaleStages) & 1, gave_up) &&
+                                           afd::mbar_wait(drain_full + 8 * (unit & 1), (unit >> 1) & 1, gave_up));
+          if (!ok) break;
+          afd::tcgen05_fence_after();
+          const uint32_t acc = lanes + (unit & 1) * (kColumns / 2);
+          const float* sc = sh.scale[s].s[GATED ? lane & 1 : 0];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int c = 32 * i + 16 * h;
-              if (c < tile.cols) {
-                float v[16];
-                afd::tmem_load16(acc + c, v);
-                afd::tmem_wait_loads();
-                afd::tmem_loaded(v);
+          for (int i = 0; i < kDrainSteps; ++i) {
+            const int c = 16 * (kDrainParts * i + h);
+            if (c < tile.cols) {
+              float v[16];
+              afd::tmem_load16(acc + c, v);
+              afd::tmem_wait_loads();
+              afd::tmem_loaded(v);
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                  const float4 s4 = *reinterpret_cast<const float4*>(sc + c + j);
-                  sum[i][j] = fmaf(v[j], s4.x, sum[i][j]);
-                  sum[i][j + 1] = fmaf(v[j + 1], s4.y, sum[i][j + 1]);
-                  sum[i][j + 2] = fmaf(v[j + 2], s4.z, sum[i][j + 2]);
-                  sum[i][j + 3] = fmaf(v[j + 3], s4.w, sum[i][j + 3]);
-                }
+              for (int j = 0; j < 16; j += 4) {
+                const float4 s4 = *reinterpret_cast<const float4*>(sc + c + j);
+                afd::fma2(sum[i] + j, v + j, s4.x, s4.y);
+                afd::fma2(sum[i] + j + 2, v + j + 2, s4.z, s4.w);
               }
             }
-            afd::tcgen05_fence_before();
-            __syncwarp();
-            if (lane == 0) afd::mbar_arrive_cluster(lead_empty + 8 * (unit & 1));
+          }
+          afd::tcgen05_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            afd::mbar_arrive_cluster(lead_empty + 8 * (unit & 1));
+            afd::mbar_arrive(scale_empty + 8 * s);
           }
         }
-        if (ok && !stop) {
+        if (ok) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (32 * i + 16 * h < tile.cols) store16<GATED>(p, tile, 32 * i + 16 * h, n0, lane, sum[i]);
+          for (int i = 0; i < kDrainSteps; ++i) {
+            const int c = 16 * (kDrainParts * i + h);
+            if (c < tile.cols) store16<GATED>(p, tile, c, n0, lane, sum[i]);
+          }
         }
       }
     }
@@ -438,6 +481,15 @@ bool encode(EncodeTiled f, CUtensorMap* map, bool fp8, uint32_t rank, const void
 
 template <bool FP8, bool GATED>
 cudaError_t launch_grouped(const Maps& maps, const ExpertParams& p, int pairs, cudaStream_t stream) {
+  if (FP8) {
+    // the registers that the hand-over gives out must be there at launch
+    static const bool enough = [] {
+      cudaFuncAttributes a;
+      return cudaFuncGetAttributes(&a, grouped_linear_kernel<FP8, GATED>) == cudaSuccess &&
+             a.numRegs * kThreads >= kFrontRegs * 128 + kDrainRegs * 32 * kDrainWarps;
+    }();
+    if (!enough) return cudaErrorInvalidKernelImage;
+  }
   const cudaError_t e = cudaFuncSetAttribute(grouped_linear_kernel<FP8, GATED>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
