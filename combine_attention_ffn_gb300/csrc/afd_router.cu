@@ -10,9 +10,9 @@
 //
 // Softmax and sigmoid are monotone, so without a bias the logits themselves
 // are the keys, exactly. With a bias the keys score + bias are computed in
-// FP32 first; a token whose selected keys lie closer together than those
-// sums' error is selected again with 64-bit keys (rare: gaps are of the order
-// of 1e-2, the error of 1e-5).
+// FP32 first; where neighbouring keys lie closer together than those sums'
+// error, the experts in question are put in order by 64-bit keys, one a lane
+// (rare: gaps are of the order of 1e-2, the error of 1e-5).
 
 #include <cuda_runtime.h>
 #include <float.h>
@@ -69,7 +69,8 @@ __device__ __forceinline__ float key_slack(float pa, float pb, float ka, float k
   return 1.6e-5f * fmaxf(pa, pb) + 2.4e-7f * fmaxf(fabsf(ka), fabsf(kb));
 }
 
-// Selection with keys in 64 bits; every lane returns in `mine` the expert of
+// Selection with keys in 64 bits, for more than 32 keys that lie close
+// together; every lane returns in `mine` the expert of
 // slot `lane` (-1: none) and in `logit` its logit.
 template <int PER>
 __device__ __noinline__ void select_exact(const float (&l)[PER], const RouterParams& p, float top, int lane,
@@ -105,6 +106,39 @@ __device__ __noinline__ void select_exact(const float (&l)[PER], const RouterPar
     if ((at & 31) == lane) taken |= 1u << (at >> 5);
     if (lane == k) *mine = at, *logit = best_logit;
   }
+}
+
+// Puts the first `found` lanes' experts in the order of their 64-bit keys.
+template <int PER>
+__device__ __noinline__ void order_exact(const float (&l)[PER], const RouterParams& p, float top, int lane, int found,
+                                         int* mine, float* logit) {
+  double sum = 1.0;
+  if (!p.sigmoid) {
+    sum = 0.0;
+    for (int j = 0; j < PER; ++j)
+      if (l[j] != -INFINITY) sum += exp((double)l[j] - (double)top);
+    sum = warp_sum(sum);
+  }
+  double key = -INFINITY;
+  if (lane < found) {
+    const double v = *logit;
+    key = (p.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - (double)top) / sum) + (double)p.bias[*mine];
+  }
+  int rank = 0;
+  for (int j = 0; j < found; ++j) {
+    const double other = __shfl_sync(kFull, key, j);
+    const int id = __shfl_sync(kFull, *mine, j);
+    rank += other > key || (other == key && id < *mine);
+  }
+  int id = -1;
+  float v = 0.f;
+  for (int j = 0; j < found; ++j) {
+    const int r = __shfl_sync(kFull, rank, j), i = __shfl_sync(kFull, *mine, j);
+    const float x = __shfl_sync(kFull, *logit, j);
+    if (r == lane) id = i, v = x;
+  }
+  *mine = id;
+  *logit = v;
 }
 
 template <int PER, bool BF16>
@@ -158,11 +192,15 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_topk_kernel(const Rou
       const float k = p.bias ? score_of(l[j]) + p.bias[lane + 32 * j] : l[j];
       key[j] = order_image(k);
     }
-    const int rounds = p.bias ? min(p.K + 1, p.E) : p.K;
+    // Without a bias, K rounds. With one, the rounds go on while the last two
+    // keys are too close to tell: all experts that may belong to the first K
+    // are then in the lanes' slots.
     float last_key = 0.f, last_logit = 0.f, last_bias = 0.f, last_score = 0.f;
     bool close = false;
     float logit = 0.f;  // lane k: the logit of slot k
-    for (int k = 0; k < rounds; ++k) {
+    int found = 0;
+    for (;; ++found) {
+      if (!p.bias && found == p.K) break;
       uint32_t best = 0;
 #pragma unroll
       for (int j = 0; j < PER; ++j) best = max(best, key[j]);
@@ -180,14 +218,23 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_topk_kernel(const Rou
       v = __shfl_sync(kFull, v, at & 31);
       if (p.bias) {
         const float kv = from_image(best), b = p.bias[at], s = score_of(v);
-        if (k > 0 && !(v == last_logit && b == last_bias) &&
-            !(last_key - kv > key_slack(last_score, s, last_key, kv)))
-          close = true;
+        bool near = false;
+        if (found > 0)
+          near = !(v == last_logit && b == last_bias) && !(last_key - kv > key_slack(last_score, s, last_key, kv));
+        if (found >= p.K && !near) break;
+        close |= near;
+        if (found == 32) break;
         last_key = kv, last_logit = v, last_bias = b, last_score = s;
       }
-      if (lane == k && k < p.K) mine = (int)at, logit = v;
+      if (lane == found) mine = (int)at, logit = v;
     }
-    if (close) select_exact<PER>(l, p, top, lane, &mine, &logit);
+    if (close) {
+      if (found <= 31)
+        order_exact<PER>(l, p, top, lane, found, &mine, &logit);
+      else
+        select_exact<PER>(l, p, top, lane, &mine, &logit);
+    }
+    if (lane >= p.K) mine = -1;
     if (p.renormalize) {
       // A factor common to the selected scores cancels: exp(-top) of softmax,
       // and for sigmoid(v) = exp(min(v, 0)) / (1 + exp(-|v|)) that of the
