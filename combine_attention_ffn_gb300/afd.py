@@ -39,7 +39,7 @@ EXPORTS = ("afd_create", "afd_destroy", "afd_source_dispatch", "afd_source_dispa
            "afd_reset_exchange", "afd_status_string", "afd_error_detail", "afd_arena_rows",
            "afd_recv_rows_for_bucket", "afd_version", "afd_route_layout_noalloc",
            "afd_set_wait_limit", "afd_phase_stamps", "afd_l2_flush", "afd_route_topk",
-           "afd_grouped_linear", "afd_gated_rows", "afd_adapter_add")
+           "afd_grouped_linear", "afd_gated_rows", "afd_adapter_add", "afd_adapter_workspace_bytes")
 
 
 class AfdError(RuntimeError):
@@ -106,7 +106,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "afd_grouped_linear": (i32, [v, i64, v, v, v, v, i32, i32, i64, i32, i32, i32, i32, v, i64, v, v]),
         "afd_gated_rows": (i32, [v, i64, v, i32, i32, i64, i32, v, i64, v]),
         "afd_adapter_add": (i32, [v, i64, v, i64, v, v, v, v, v, v, i32, i32, i64, i32, i32, i32, i32,
-                                  i32, v, i64, v]),
+                                  i32, v, i64, v, i64, v]),
+        "afd_adapter_workspace_bytes": (i64, [i64, i32]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -600,7 +601,11 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
         out, out_stride = base, base_stride
     else:
         out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
-    _call("afd_adapter_add", base.device, stream, base.data_ptr(), base_stride, x.data_ptr(), x_stride,
+    workspace = torch.empty(R + S + 2, dtype=torch.int32, device=x.device)
+    if stream is not None:  # the allocator must not hand it on before that stream is done with it
+        workspace.record_stream(stream)
+    _call("afd_adapter_add", workspace.device, stream, base.data_ptr(), base_stride, x.data_ptr(), x_stride,
           down.data_ptr(), up.data_ptr(), token_slots.data_ptr(), scales.data_ptr(), _ptr(row_src),
-          _ptr(ends) if G else None, G, top_k, R, tokens, S, rank, K, N, out.data_ptr(), out_stride)
+          _ptr(ends) if G else None, G, top_k, R, tokens, S, rank, K, N, out.data_ptr(), out_stride,
+          workspace.data_ptr(), 4 * workspace.numel())
     return out
