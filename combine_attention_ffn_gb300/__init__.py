@@ -17,5 +17,6 @@ def __getattr__(name):
     if name in __all__:
         from . import afd
 
-        return getattr(afd, name)
+        globals()[name] = value = getattr(afd, name)
+        return value
     raise AttributeError(name)

@@ -432,33 +432,48 @@ def route_layout_noalloc(ids: torch.Tensor, num_experts: int, num_workers: int,
 
 
 # -- the experts' side of an exchange (afd.h: no context, no state) -----------
-def _call(name: str, device, stream, *args) -> None:
-    """Calls a context-free entry point on `device`'s stream, with that device
-    current (the library works on the current one)."""
-    lib = load_library()
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            st = getattr(lib, name)(*args, _stream_handle(stream, device))
+# A decode step's call is shorter on the GPU than on the host, so the binding
+# asks PyTorch for the raw stream and device number where it has them: the
+# public objects around them cost 1 us a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(name: str, on: torch.Tensor, stream, *args) -> None:
+    """Calls a context-free entry point on a stream of the device of `on`, with
+    that device current (the library works on the current one)."""
+    lib = _lib or load_library()
+    index, current = on.get_device(), _current_device()
+    if index < 0:  # page-locked host memory
+        index = current
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == current:
+        st = getattr(lib, name)(*args, handle)
     else:
-        st = getattr(lib, name)(*args, _stream_handle(stream, device))
+        with torch.cuda.device(index):
+            st = getattr(lib, name)(*args, handle)
     if st != OK:
         raise AfdError(st, f"{name}: {lib.afd_status_string(st).decode()}")
 
 
-def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> None:
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> int:
+    """Checks a dense tensor; returns its address."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise AfdError(ERR_ARG, f"{name} must be contiguous {dtype} {list(shape)}, "
                        f"got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
 
 
 def _want_rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> int:
     """Checks a [rows, columns] tensor whose rows may be strided; returns the
     row stride in elements."""
-    if t.dtype != dtype or t.shape != shape or (shape[1] > 1 and t.stride(1) != 1) \
-            or (shape[0] > 1 and t.stride(0) < shape[1]):
-        raise AfdError(ERR_ARG, f"{name} must be {dtype} {list(shape)} with dense rows, "
-                       f"got {t.dtype} {list(t.shape)}")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    if t.dtype is dtype and t.shape == shape:
+        row, col = t.stride()
+        if shape[0] <= 1:
+            row = shape[1]
+        if row >= shape[1] and (col == 1 or shape[1] <= 1):
+            return row
+    raise AfdError(ERR_ARG, f"{name} must be {dtype} {list(shape)} with dense rows, got {t.dtype} {list(t.shape)}")
 
 
 def route_topk(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
@@ -480,22 +495,17 @@ def route_topk(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
         raise AfdError(ERR_ARG, f"scoring must be one of {sorted(SCORINGS)}, got {scoring!r}")
     T, E = logits.shape
     stride = _want_rows(logits, "logits", logits.dtype, (T, E))
-    if bias is not None:
-        _want(bias, "bias", torch.float32, (E,))
-    if live_tokens is not None:
-        _want(live_tokens, "live_tokens", torch.int32, (1,))
+    bias_ptr = None if bias is None else _want(bias, "bias", torch.float32, (E,))
+    live_ptr = None if live_tokens is None else _want(live_tokens, "live_tokens", torch.int32, (1,))
+    shape = (T, top_k)
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int64, device=logits.device)
-    else:
-        _want(ids, "ids", torch.int64, (T, top_k))
+        ids = torch.empty(shape, dtype=torch.int64, device=logits.device)
+    ids_ptr = _want(ids, "ids", torch.int64, shape)
     if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
-    else:
-        _want(weights, "weights", torch.float32, (T, top_k))
-    _call("afd_route_topk", ids.device, stream, logits.data_ptr() if T else None,
-          FP32 if logits.dtype == torch.float32 else BF16, stride, _ptr(bias), _ptr(live_tokens), T, E, top_k,
-          SCORINGS[scoring], int(bool(renormalize)), scale, ids.data_ptr() if T else None,
-          weights.data_ptr() if T else None)
+        weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    weights_ptr = _want(weights, "weights", torch.float32, shape)
+    _call("afd_route_topk", ids, stream, logits.data_ptr(), FP32 if logits.dtype is torch.float32 else BF16, stride,
+          bias_ptr, live_ptr, T, E, top_k, SCORINGS[scoring], bool(renormalize), scale, ids_ptr, weights_ptr)
     return ids, weights
 
 
@@ -524,25 +534,23 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, ends: torch.Tensor, *,
         raise AfdError(ERR_ARG, f"a gated weight has an even number of rows, got {W}")
     N = W // 2 if gated else W
     x_stride = _want_rows(x, "x", x.dtype, (R, K))
-    _want(weight, "weight", x.dtype, (G, W, K))
-    _want(ends, "ends", torch.int32, (G,))
+    w_ptr = _want(weight, "weight", x.dtype, (G, W, K))
+    ends_ptr = _want(ends, "ends", torch.int32, (G,))
+    xs_ptr = ws_ptr = error_ptr = None
     if fp8:
         if x_scale is None or weight_scale is None or K % 128 or N % 128:
             raise AfdError(ERR_ARG, "float8_e4m3fn takes x_scale, weight_scale and K, N that are multiples of 128")
-        _want(x_scale, "x_scale", torch.float32, (R, K // 128))
-        _want(weight_scale, "weight_scale", torch.float32, (G, W // 128, K // 128))
+        xs_ptr = _want(x_scale, "x_scale", torch.float32, (R, K // 128))
+        ws_ptr = _want(weight_scale, "weight_scale", torch.float32, (G, W // 128, K // 128))
     elif x_scale is not None or weight_scale is not None:
         raise AfdError(ERR_ARG, "bfloat16 rows take no scales")
     if out is None:
         out = torch.empty((R, N), dtype=torch.bfloat16, device=x.device)
-        out_stride = N
-    else:
-        out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
+    out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
     if error is not None:
-        _want(error, "error", torch.int32, (1,))
-    _call("afd_grouped_linear", x.device, stream, x.data_ptr(), x_stride, _ptr(x_scale), weight.data_ptr(),
-          _ptr(weight_scale), ends.data_ptr(), G, expert_alignment, R, K, N, FP8_E4M3 if fp8 else BF16,
-          int(bool(gated)), out.data_ptr(), out_stride, _ptr(error))
+        error_ptr = _want(error, "error", torch.int32, (1,))
+    _call("afd_grouped_linear", x, stream, x.data_ptr(), x_stride, xs_ptr, w_ptr, ws_ptr, ends_ptr, G, expert_alignment,
+          R, K, N, FP8_E4M3 if fp8 else BF16, bool(gated), out.data_ptr(), out_stride, error_ptr)
     return out
 
 
@@ -556,14 +564,13 @@ def gated_rows(h: torch.Tensor, ends: torch.Tensor, *, expert_alignment: int = 1
         raise AfdError(ERR_ARG, "h must be bfloat16 [R, 2N]")
     R, N = h.shape[0], h.shape[1] // 2
     h_stride = _want_rows(h, "h", torch.bfloat16, (R, 2 * N))
-    if ends.dim() != 1:
-        raise AfdError(ERR_ARG, "ends must be int32 [G]")
-    _want(ends, "ends", torch.int32, (ends.shape[0],))
+    G = ends.numel()
+    ends_ptr = _want(ends, "ends", torch.int32, (G,))
     if out is None:
         out = torch.empty((R, N), dtype=torch.bfloat16, device=h.device)
     out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
-    _call("afd_gated_rows", ends.device, stream, h.data_ptr(), h_stride, ends.data_ptr(), ends.shape[0],
-          expert_alignment, R, N, out.data_ptr(), out_stride)
+    _call("afd_gated_rows", ends, stream, h.data_ptr(), h_stride, ends_ptr, G, expert_alignment, R, N, out.data_ptr(),
+          out_stride)
     return out
 
 
@@ -580,32 +587,32 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
     `base` (in place). See afd_adapter_add in include/afd.h."""
     if base.dim() != 2 or x.dim() != 2 or down.dim() != 3:
         raise AfdError(ERR_ARG, "base must be [R, N], x [R, K], down [S, rank, K] and up [S, N, rank]")
-    (R, N), K, (S, rank) = base.shape, x.shape[1], down.shape[:2]
+    (R, N), K, (S, rank, _) = base.shape, x.shape[1], down.shape
     base_stride = _want_rows(base, "base", torch.bfloat16, (R, N))
     x_stride = _want_rows(x, "x", torch.bfloat16, (R, K))
-    _want(down, "down", torch.bfloat16, (S, rank, K))
-    _want(up, "up", torch.bfloat16, (S, N, rank))
-    _want(scales, "scales", torch.float32, (S,))
+    down_ptr = _want(down, "down", torch.bfloat16, (S, rank, K))
+    up_ptr = _want(up, "up", torch.bfloat16, (S, N, rank))
+    scales_ptr = _want(scales, "scales", torch.float32, (S,))
     tokens = token_slots.numel()
-    _want(token_slots, "token_slots", torch.int32, (tokens,))
-    G = 0
+    slots_ptr = _want(token_slots, "token_slots", torch.int32, (tokens,))
+    G, src_ptr, ends_ptr = 0, None, None
     if row_src is not None:
-        if ends is None or ends.dim() != 1:
+        if ends is None:
             raise AfdError(ERR_ARG, "row_src needs the exchange's ends, int32 [G]")
-        G = ends.shape[0]
-        _want(row_src, "row_src", torch.int32, (R,))
-        _want(ends, "ends", torch.int32, (G,))
+        G = ends.numel()
+        src_ptr = _want(row_src, "row_src", torch.int32, (R,))
+        ends_ptr = _want(ends, "ends", torch.int32, (G,))
     elif tokens < R:
         raise AfdError(ERR_ARG, f"token_slots has {tokens} entries for {R} rows")
     if out is None:
         out, out_stride = base, base_stride
     else:
         out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
-    workspace = torch.empty(R + S + 2, dtype=torch.int32, device=x.device)
+    words = R + S + 2
+    workspace = torch.empty(words, dtype=torch.int32, device=x.device)
     if stream is not None:  # the allocator must not hand it on before that stream is done with it
         workspace.record_stream(stream)
-    _call("afd_adapter_add", workspace.device, stream, base.data_ptr(), base_stride, x.data_ptr(), x_stride,
-          down.data_ptr(), up.data_ptr(), token_slots.data_ptr(), scales.data_ptr(), _ptr(row_src),
-          _ptr(ends) if G else None, G, top_k, R, tokens, S, rank, K, N, out.data_ptr(), out_stride,
-          workspace.data_ptr(), 4 * workspace.numel())
+    _call("afd_adapter_add", workspace, stream, base.data_ptr(), base_stride, x.data_ptr(), x_stride, down_ptr, up_ptr,
+          slots_ptr, scales_ptr, src_ptr, ends_ptr, G, top_k, R, tokens, S, rank, K, N, out.data_ptr(), out_stride,
+          workspace.data_ptr(), 4 * words)
     return out

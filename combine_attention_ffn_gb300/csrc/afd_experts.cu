@@ -175,6 +175,56 @@ __device__ __forceinline__ void store16(const ExpertParams& p, const Tile& tile,
   }
 }
 
+struct Drain {
+  uint32_t acc, full, lead_empty, scale_full, scale_empty;
+  int h, n0, lane;
+};
+
+// One tile's FP8 blocks: every block's products, scaled, into FP32 sums in
+// registers, then the store. The number of steps is a constant: a sum that a
+// branch may or may not add to is moved twice a step.
+template <bool GATED, int STEPS>
+__device__ __forceinline__ bool drain_blocks(const ExpertParams& p, Shared& sh, const Tile& tile, const Drain& d,
+                                             uint32_t& unit) {
+  float sum[STEPS + 1][16];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
+  for (int kb = 0; kb < p.k_blocks; ++kb, ++unit) {
+    const uint32_t s = unit % kScaleStages;
+    if (!__all_sync(0xffffffffu, afd::mbar_wait(d.scale_full + 8 * s, (unit / kScaleStages) & 1, &sh.gave_up) &&
+                                     afd::mbar_wait(d.full + 8 * (unit & 1), (unit >> 1) & 1, &sh.gave_up)))
+      return false;
+    afd::tcgen05_fence_after();
+    const uint32_t acc = d.acc + (unit & 1) * (kColumns / 2);
+    const float* sc = sh.scale[s].s[GATED ? d.lane & 1 : 0] + 16 * d.h;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int c = 16 * kDrainParts * i;
+      float v[16];
+      afd::tmem_load16(acc + c, v);
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const float4 s4 = *reinterpret_cast<const float4*>(sc + c + j);
+        sum[i][j] = fmaf(v[j], s4.x, sum[i][j]);
+        sum[i][j + 1] = fmaf(v[j + 1], s4.y, sum[i][j + 1]);
+        sum[i][j + 2] = fmaf(v[j + 2], s4.z, sum[i][j + 2]);
+        sum[i][j + 3] = fmaf(v[j + 3], s4.w, sum[i][j + 3]);
+      }
+    }
+    afd::tcgen05_fence_before();
+    __syncwarp();
+    if (d.lane == 0) {
+      afd::mbar_arrive_cluster(d.lead_empty + 8 * (unit & 1));
+      afd::mbar_arrive(d.scale_empty + 8 * s);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) store16<GATED>(p, tile, 16 * (kDrainParts * i + d.h), d.n0, d.lane, sum[i]);
+  return true;
+}
+
 template <bool FP8, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_linear_kernel(const __grid_constant__ Maps maps, const ExpertParams p) {
@@ -387,8 +437,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int c = 16 * h; c < tile.cols; c += 16 * kDrainParts) {
           float v[16];
           afd::tmem_load16(acc + c, v);
-          afd::tmem_wait_loads();
-          afd::tmem_loaded(v);
           store16<GATED>(p, tile, c, n0, lane, v);
         }
         afd::tcgen05_fence_before();
@@ -396,49 +444,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) afd::mbar_arrive_cluster(lead_empty + 8 * (unit & 1));
         ++unit;
       } else {
-        float sum[kDrainSteps][16];
-#pragma unroll
-        for (int i = 0; i < kDrainSteps; ++i)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++unit) {
-          const uint32_t s = unit % kScaleStages;
-          ok = __all_sync(0xffffffffu, afd::mbar_wait(scale_full + 8 * s, (unit / kScaleStages) & 1, gave_up) &&
-                                           afd::mbar_wait(drain_full + 8 * (unit & 1), (unit >> 1) & 1, gave_up));
-          if (!ok) break;
-          afd::tcgen05_fence_after();
-          const uint32_t acc = lanes + (unit & 1) * (kColumns / 2);
-          const float* sc = sh.scale[s].s[GATED ? lane & 1 : 0];
-#pragma unroll
-          for (int i = 0; i < kDrainSteps; ++i) {
-            const int c = 16 * (kDrainParts * i + h);
-            if (c < tile.cols) {
-              float v[16];
-              afd::tmem_load16(acc + c, v);
-              afd::tmem_wait_loads();
-              afd::tmem_loaded(v);
-#pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const float4 s4 = *reinterpret_cast<const float4*>(sc + c + j);
-                afd::fma2(sum[i] + j, v + j, s4.x, s4.y);
-                afd::fma2(sum[i] + j + 2, v + j + 2, s4.z, s4.w);
-              }
-            }
-          }
-          afd::tcgen05_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            afd::mbar_arrive_cluster(lead_empty + 8 * (unit & 1));
-            afd::mbar_arrive(scale_empty + 8 * s);
-          }
-        }
-        if (ok) {
-#pragma unroll
-          for (int i = 0; i < kDrainSteps; ++i) {
-            const int c = 16 * (kDrainParts * i + h);
-            if (c < tile.cols) store16<GATED>(p, tile, c, n0, lane, sum[i]);
-          }
-        }
+        // this warp's 16-column steps of the tile
+        const int steps = max(0, (tile.cols - 16 * h + 16 * kDrainParts - 1) / (16 * kDrainParts));
+        const Drain d = {lanes + 16 * h, drain_full, lead_empty, scale_full, scale_empty, h, n0, lane};
+        if (steps == 4) ok = drain_blocks<GATED, 4>(p, sh, tile, d, unit);
+        else if (steps == 3) ok = drain_blocks<GATED, 3>(p, sh, tile, d, unit);
+        else if (steps == 2) ok = drain_blocks<GATED, 2>(p, sh, tile, d, unit);
+        else if (steps == 1) ok = drain_blocks<GATED, 1>(p, sh, tile, d, unit);
+        else ok = drain_blocks<GATED, 0>(p, sh, tile, d, unit);
       }
     }
   }

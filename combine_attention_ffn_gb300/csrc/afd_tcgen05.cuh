@@ -82,15 +82,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// sum[0..1] += v[0..1] * (a, b), two FP32 multiply-adds an instruction.
-__device__ __forceinline__ void fma2(float* sum, const float* v, float a, float b) {
-  asm("{\n.reg .b64 s, x, k;\n"
-      "mov.b64 s, {%0, %1};\nmov.b64 x, {%2, %3};\nmov.b64 k, {%4, %5};\n"
-      "fma.rn.f32x2 s, x, k, s;\nmov.b64 {%0, %1}, s;\n}"
-      : "+f"(sum[0]), "+f"(sum[1])
-      : "f"(v[0]), "f"(v[1]), "f"(a), "f"(b));
-}
-
 // Tiled bulk loads of one CTA of a pair into its own shared memory, counted on
 // a barrier of either CTA (a map_to_rank address).
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
@@ -163,37 +154,26 @@ __device__ __forceinline__ void tmem_free_pair(uint32_t base, uint32_t columns) 
 __device__ __forceinline__ void tcgen05_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tcgen05_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 16 (or 32) columns of this warp's 32 lanes; the values may be used after
-// tmem_wait_loads() and tmem_loaded().
+// 16 columns of this warp's 32 lanes. Load and wait are one statement: apart,
+// the values would have to pass through a second one to keep their uses behind
+// the wait, which cost three moves a value.
 __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
-  uint32_t* u = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
-        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
-      : "r"(addr));
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(addr)
+      : "memory");
 }
 
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
-  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+__device__ __forceinline__ void tmem_load8(uint32_t addr, float (&v)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
-        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
-        "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]),
-        "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
-      : "r"(addr));
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+      : "r"(addr)
+      : "memory");
 }
-
-// Keeps the compiler from moving uses of v ahead of the wait.
-template <int N>
-__device__ __forceinline__ void tmem_loaded(float (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 8)
-    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
-                      "+f"(v[i + 6]), "+f"(v[i + 7]));
-}
-
-__device__ __forceinline__ void tmem_wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 }  // namespace afd

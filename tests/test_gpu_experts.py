@@ -575,7 +575,7 @@ def test_row_operators_take_pinned_host_buffers():
     ids, w = lib.route_topk(logits, 3)
     pids, pw = (torch.zeros(5, 3, dtype=d).pin_memory() for d in (torch.int64, torch.float32))
     host = pin(logits)
-    afd._call("afd_route_topk", logits.device, None, host.data_ptr(), afd.FP32, 16, None, None, 5, 16, 3, 0, 1, 1.0,
+    afd._call("afd_route_topk", logits, None, host.data_ptr(), afd.FP32, 16, None, None, 5, 16, 3, 0, 1, 1.0,
               pids.data_ptr(), pw.data_ptr())
     torch.cuda.synchronize()
     assert torch.equal(pids, ids.cpu()) and torch.equal(pw, w.cpu())
