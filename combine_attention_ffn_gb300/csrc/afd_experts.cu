@@ -12,9 +12,14 @@
 //
 // Persistent pairs walk the tiles (expert, weight tile, row tile) with these
 // roles per CTA: warp 0 loads by tiled bulk copies (K blocks of 128 bytes, a
-// ring of stages), warp 1 of the even CTA issues the products, eight warps
-// drain the accumulators, which are double-buffered in TMEM (2 x 256 columns):
-// the next tile's products run while the last one's are stored.
+// ring of stages), warp 1 of the even CTA issues the products, sixteen warps
+// drain the accumulators, which take turns in TMEM (two of 256 columns, or more
+// and narrower ones where the widest tile is narrower): the next tile's
+// products run while the last one's are stored.
+//
+// Tiles are dealt out once, widest experts first and back and forth over the
+// pairs: on a prefill bucket the pair with the most work has 1.04 times the
+// mean, dealt in the experts' order 1.09 to 1.14 times.
 //
 // Gated: a bulk copy with dimensions (k, half, row) interleaves gate and up
 // rows in shared memory, so the two sums of an output sit in neighbouring
@@ -51,9 +56,11 @@ constexpr int kHalfBytes = kCtaRows * kBlockBytes;  // one operand of a stage
 constexpr int kStageBytes = 2 * kHalfBytes;
 constexpr int kDrainWarps = 16;
 constexpr int kDrainParts = kDrainWarps / 4;  // warps that share 32 lanes of TMEM, 16 columns each in turn
-constexpr int kDrainSteps = kTileRows / (16 * kDrainParts);
 constexpr int kThreads = 128 + 32 * kDrainWarps;
-constexpr int kColumns = 512;     // all of TMEM: two accumulators
+constexpr int kColumns = 512;     // all of TMEM
+constexpr int kMaxBufs = 8;       // accumulators in it, at most
+constexpr int kClasses = kTileRows / 32;  // tile widths
+constexpr int kListed = 64;       // tiles of a pair that are looked up before the roles start
 constexpr int kColStep = 32;      // received rows of a product come in multiples of this
 constexpr int kRowMaps = 8;       // boxes of 16, 32, .. 128 received rows: one copy a stage, whatever the tile
 constexpr int kScaleStages = 8;   // ring of scales (FP8)
@@ -86,24 +93,47 @@ struct alignas(16) BlockScales {
   float s[2][kTileRows + 4];  // [gate / up][received row]; plain uses the first
 };
 
+struct alignas(16) Tile {
+  int group, m, row, rows;
+  __device__ __forceinline__ int cols() const { return (rows + kColStep - 1) & -kColStep; }
+};
+
 struct Shared {
-  alignas(8) uint64_t full[kStages], empty[kStages], drain_full[2], drain_empty[2];
+  alignas(8) uint64_t full[kStages], empty[kStages];
+  uint64_t drain_full[kMaxBufs];  // an accumulator's products are complete
+  uint64_t drained[kMaxBufs];     // this CTA's warps have read it
+  uint64_t peer_drained[kMaxBufs];  // ... and the other CTA's (used in the even one)
   uint64_t scale_full[kScaleStages], scale_empty[kScaleStages];
   uint32_t tmem;
   int gave_up;
+  int widest, mixed;               // widest tile, and whether there are others
   int end[afd::kMaxExperts];
-  int first_tile[afd::kMaxExperts + 1];
+  int first_tile[afd::kMaxExperts + 1];  // by position in `order`
+  uint16_t order[afd::kMaxExperts];      // the groups, widest tiles first
+  uint16_t class_count[afd::kMaxExperts / 32][kClasses + 1];
+  Tile list[kListed];                    // this pair's first tiles
   BlockScales scale[kScaleStages];
 };
 
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + sizeof(Shared);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
-struct Tile {
-  int group, m, row, rows, cols;  // cols: rows rounded up to kColStep
-};
-
 __device__ __forceinline__ int row_tiles(int count) { return (count + kTileRows - 1) / kTileRows; }
+
+// Width of a group's tiles: its rows in equal parts, whole column steps.
+__device__ __forceinline__ int tile_width(int count) {
+  const int n = row_tiles(count);
+  return n ? ((count + n - 1) / n + kColStep - 1) & -kColStep : 0;
+}
+
+__device__ __forceinline__ int group_count(const Shared& sh, const ExpertParams& p, int g) {
+  return max(sh.end[g] - (g ? afd::group_start(sh.end[g - 1], p.alpha, p.R) : 0), 0);
+}
+
+// Tile `t` of this pair's turn: every second turn goes back over the pairs.
+__device__ __forceinline__ int dealt(int turn, int pair, int pairs) {
+  return turn * pairs + (turn & 1 ? pairs - 1 - pair : pair);
+}
 
 __device__ __forceinline__ Tile find_tile(const Shared& sh, const ExpertParams& p, int t) {
   int lo = 0, hi = p.G - 1;  // the last group whose first tile is at or before t, skipping empty ones
@@ -111,94 +141,129 @@ __device__ __forceinline__ Tile find_tile(const Shared& sh, const ExpertParams& 
     const int mid = (lo + hi + 1) >> 1;
     if (sh.first_tile[mid] <= t) lo = mid; else hi = mid - 1;
   }
-  const int start = lo ? afd::group_start(sh.end[lo - 1], p.alpha, p.R) : 0;
-  const int count = sh.end[lo] - start, n = row_tiles(count);
-  const int i = t - sh.first_tile[lo];
-  const int width = ((count + n - 1) / n + kColStep - 1) & -kColStep;
   Tile tile;
-  tile.group = lo;
+  tile.group = sh.mixed ? sh.order[lo] : lo;
+  const int start = tile.group ? afd::group_start(sh.end[tile.group - 1], p.alpha, p.R) : 0;
+  const int count = sh.end[tile.group] - start, n = row_tiles(count), width = tile_width(count);
+  const int i = t - sh.first_tile[lo];
   tile.m = i / n;
   const int off = (i - tile.m * n) * width;
   tile.row = start + off;
   tile.rows = min(width, count - off);  // at least 1: (n - 1) * width < count
-  tile.cols = (tile.rows + kColStep - 1) & -kColStep;
   return tile;
 }
 
-// Stores 16 received rows x 32 lanes of sums: lane = weight row, v[i] = row i.
-// Pairs of rows are exchanged between neighbouring lanes, so that each lane
-// stores two columns of one row (plain), or completes one output (gated).
+// The tile of this pair's turn; false: it has none.
+__device__ __forceinline__ bool next_tile(const Shared& sh, const ExpertParams& p, int turn, int pair, int pairs, int tiles,
+                                          Tile* tile) {
+  const int t = dealt(turn, pair, pairs);
+  if (t >= tiles) return false;
+  *tile = turn < kListed ? sh.list[turn] : find_tile(sh, p, t);
+  return true;
+}
+
+// Where a lane stores: two neighbouring columns of every second (plain) or
+// fourth (gated) row, or with other strides one column.
+struct Out {
+  uint16_t* at;      // the lane's column in its first row of the tile
+  int64_t step;      // elements from one of its rows to the next
+  int row;           // its first row in a chunk
+  bool in;           // its columns exist
+  uint32_t select;   // which halves of two lanes' pairs it stores
+};
+
 template <bool GATED>
-__device__ __forceinline__ void store16(const ExpertParams& p, const Tile& tile, int c0, int n0, int lane,
+__device__ __forceinline__ Out lane_out(const ExpertParams& p, const Tile& tile, int n0, int lane) {
+  Out o;
+  const int odd = lane & 1, upper = lane >> 1 & 1;
+  const int n = n0 + (GATED ? lane >> 1 : lane);
+  const int side = GATED ? upper : odd;
+  o.row = GATED ? (p.vec ? 2 * upper + odd : odd) : (p.vec ? odd : 0);
+  o.step = p.out_stride * (GATED ? (p.vec ? 4 : 2) : (p.vec ? 2 : 1));
+  o.in = n < p.N;
+  o.select = side ? 0x3276 : 0x5410;
+  o.at = p.out + (int64_t)(tile.row + o.row) * p.out_stride + (p.vec ? n & ~1 : n);
+  return o;
+}
+
+// Stores 16 received rows x 32 lanes of sums: lane = weight row, v[i] = row i.
+// Rows are exchanged between neighbouring lanes in pairs, so that each lane
+// completes one output of two (gated), then stores two columns at a time.
+template <bool GATED>
+__device__ __forceinline__ void store16(const ExpertParams& p, const Tile& tile, const Out& o, int c0, int lane,
                                         const float (&v)[16]) {
-  const int odd = lane & 1;
-  const int left = tile.rows - c0;
-  uint16_t* out = p.out + (int64_t)(tile.row + c0) * p.out_stride;
+  const int left = o.in ? tile.rows - c0 - o.row : 0;
+  uint16_t* at = o.at + c0 * p.out_stride;
   if (GATED) {
-    const int f = n0 + (lane >> 1);
+    const bool odd = lane & 1;
     float a[8];  // outputs of row 2 i + odd
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      const float mine = odd ? v[2 * i + 1] : v[2 * i];
       const float other = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
-      a[i] = odd ? afd::silu_mul(other, v[2 * i + 1]) : afd::silu_mul(v[2 * i], other);
+      a[i] = afd::silu_mul(odd ? other : mine, odd ? mine : other);
     }
     if (p.vec) {
-      const int upper = (lane >> 1) & 1;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float other = __shfl_xor_sync(0xffffffffu, upper ? a[2 * i] : a[2 * i + 1], 2);
-        const int r = 4 * i + 2 * upper + odd;
-        const uint32_t two = upper ? afd::pack_bf16(other, a[2 * i + 1]) : afd::pack_bf16(a[2 * i], other);
-        if (r < left && f < p.N) *reinterpret_cast<uint32_t*>(out + r * p.out_stride + (f & ~1)) = two;
+        const uint32_t two = afd::pack_bf16(a[2 * i], a[2 * i + 1]);
+        const uint32_t out = __byte_perm(two, __shfl_xor_sync(0xffffffffu, two, 2), o.select);
+        if (4 * i < left) *reinterpret_cast<uint32_t*>(at) = out;
+        at += o.step;
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (2 * i + odd < left && f < p.N)
-          out[(2 * i + odd) * p.out_stride + f] = (uint16_t)afd::pack_bf16(a[i], 0.f);
-    }
-  } else {
-    const int n = n0 + lane;
-    if (p.vec) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float other = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
-        const uint32_t two = odd ? afd::pack_bf16(other, v[2 * i + 1]) : afd::pack_bf16(v[2 * i], other);
-        if (2 * i + odd < left && n < p.N)
-          *reinterpret_cast<uint32_t*>(out + (2 * i + odd) * p.out_stride + (n & ~1)) = two;
+        if (2 * i < left) *at = (uint16_t)afd::pack_bf16(a[i], 0.f);
+        at += o.step;
       }
-    } else {
+    }
+  } else if (p.vec) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < left && n < p.N) out[i * p.out_stride + n] = (uint16_t)afd::pack_bf16(v[i], 0.f);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t two = afd::pack_bf16(v[2 * i], v[2 * i + 1]);
+      const uint32_t out = __byte_perm(two, __shfl_xor_sync(0xffffffffu, two, 1), o.select);
+      if (2 * i < left) *reinterpret_cast<uint32_t*>(at) = out;
+      at += o.step;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i < left) *at = (uint16_t)afd::pack_bf16(v[i], 0.f);
+      at += o.step;
     }
   }
 }
 
-struct Drain {
-  uint32_t acc, full, lead_empty, scale_full, scale_empty;
-  int h, n0, lane;
+// The accumulators' turns: unit u uses buffer u & (bufs - 1).
+struct Turns {
+  uint32_t tmem, full, drained;  // addresses of buffer 0
+  int shift;                     // log2 bufs
+  int cols;                      // columns of a buffer
+  __device__ __forceinline__ uint32_t buf(uint32_t unit) const { return unit & ((1u << shift) - 1); }
+  __device__ __forceinline__ uint32_t phase(uint32_t unit) const { return unit >> shift & 1; }
 };
 
 // One tile's FP8 blocks: every block's products, scaled, into FP32 sums in
 // registers, then the store. The number of steps is a constant: a sum that a
 // branch may or may not add to is moved twice a step.
 template <bool GATED, int STEPS>
-__device__ __forceinline__ bool drain_blocks(const ExpertParams& p, Shared& sh, const Tile& tile, const Drain& d,
-                                             uint32_t& unit) {
+__device__ __forceinline__ bool drain_blocks(const ExpertParams& p, Shared& sh, const Tile& tile, const Turns& turns,
+                                             const Out& out, int h, int lane, uint32_t& unit) {
+  const uint32_t scale_full = afd::smem_u32(sh.scale_full), scale_empty = afd::smem_u32(sh.scale_empty);
   float sum[STEPS + 1][16];
 #pragma unroll
   for (int i = 0; i < STEPS; ++i)
 #pragma unroll
     for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
   for (int kb = 0; kb < p.k_blocks; ++kb, ++unit) {
-    const uint32_t s = unit % kScaleStages;
-    if (!__all_sync(0xffffffffu, afd::mbar_wait(d.scale_full + 8 * s, (unit / kScaleStages) & 1, &sh.gave_up) &&
-                                     afd::mbar_wait(d.full + 8 * (unit & 1), (unit >> 1) & 1, &sh.gave_up)))
+    const uint32_t s = unit % kScaleStages, b = turns.buf(unit);
+    if (!__all_sync(0xffffffffu, afd::mbar_wait(scale_full + 8 * s, (unit / kScaleStages) & 1, &sh.gave_up) &&
+                                     afd::mbar_wait(turns.full + 8 * b, turns.phase(unit), &sh.gave_up)))
       return false;
     afd::tcgen05_fence_after();
-    const uint32_t acc = d.acc + (unit & 1) * (kColumns / 2);
-    const float* sc = sh.scale[s].s[GATED ? d.lane & 1 : 0] + 16 * d.h;
+    const uint32_t acc = turns.tmem + b * turns.cols + 16 * h;
+    const float* sc = sh.scale[s].s[GATED ? lane & 1 : 0] + 16 * h;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
       const int c = 16 * kDrainParts * i;
@@ -215,13 +280,13 @@ __device__ __forceinline__ bool drain_blocks(const ExpertParams& p, Shared& sh, 
     }
     afd::tcgen05_fence_before();
     __syncwarp();
-    if (d.lane == 0) {
-      afd::mbar_arrive_cluster(d.lead_empty + 8 * (unit & 1));
-      afd::mbar_arrive(d.scale_empty + 8 * s);
+    if (lane == 0) {
+      afd::mbar_arrive(turns.drained + 8 * b);
+      afd::mbar_arrive(scale_empty + 8 * s);
     }
   }
 #pragma unroll
-  for (int i = 0; i < STEPS; ++i) store16<GATED>(p, tile, 16 * (kDrainParts * i + d.h), d.n0, d.lane, sum[i]);
+  for (int i = 0; i < STEPS; ++i) store16<GATED>(p, tile, out, 16 * (kDrainParts * i + h), lane, sum[i]);
   return true;
 }
 
@@ -235,7 +300,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = afd::cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const uint32_t full = afd::smem_u32(sh.full), empty = afd::smem_u32(sh.empty);
-  const uint32_t drain_full = afd::smem_u32(sh.drain_full), drain_empty = afd::smem_u32(sh.drain_empty);
+  const uint32_t drain_full = afd::smem_u32(sh.drain_full), drained = afd::smem_u32(sh.drained);
+  const uint32_t peer_drained = afd::smem_u32(sh.peer_drained);
   const uint32_t scale_full = afd::smem_u32(sh.scale_full), scale_empty = afd::smem_u32(sh.scale_empty);
 
   if (warp == 0 && lane == 0) {
@@ -243,9 +309,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       afd::mbar_init(full + 8 * i, 1);
       afd::mbar_init(empty + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kMaxBufs; ++i) {
       afd::mbar_init(drain_full + 8 * i, 1);
-      afd::mbar_init(drain_empty + 8 * i, 2 * kDrainWarps);
+      afd::mbar_init(drained + 8 * i, kDrainWarps);
+      afd::mbar_init(peer_drained + 8 * i, 1);
     }
     for (int i = 0; FP8 && i < kScaleStages; ++i) {
       afd::mbar_init(scale_full + 8 * i, kScaleThreads);
@@ -259,27 +326,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   for (int g = threadIdx.x; g < p.G; g += kThreads) sh.end[g] = afd::group_end(p.ends[g], p.R);
   __syncthreads();
   if (warp == 2) {
-    int carry = 0;
+    int widest = 0, narrowest = kTileRows, carry = 0;
     for (int g0 = 0; g0 < p.G; g0 += 32) {
-      const int g = g0 + lane;
-      int tiles = 0;
-      if (g < p.G) {
-        const int start = g ? afd::group_start(sh.end[g - 1], p.alpha, p.R) : 0;
-        tiles = row_tiles(max(sh.end[g] - start, 0)) * p.m_tiles;
-      }
-      const int incl = afd::warp_inclusive_scan(tiles);
-      if (g < p.G) sh.first_tile[g] = carry + incl - tiles;
+      const int g = g0 + lane, count = g < p.G ? group_count(sh, p, g) : 0;
+      const int w = tile_width(count), n = row_tiles(count) * p.m_tiles;
+      widest = max(widest, w);
+      if (w) narrowest = min(narrowest, w);
+      const int incl = afd::warp_inclusive_scan(n);
+      if (g < p.G) sh.first_tile[g] = carry + incl - n;
       carry += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) sh.first_tile[p.G] = carry;
+    widest = __reduce_max_sync(0xffffffffu, widest);
+    narrowest = __reduce_min_sync(0xffffffffu, narrowest);
+    if (lane == 0) {
+      sh.widest = max(widest, kColStep);
+      sh.mixed = narrowest < widest;
+      sh.first_tile[p.G] = carry;
+    }
+  }
+  __syncthreads();
+  if (sh.mixed) {
+    // A stable counting sort of the groups by width: counts of 32 groups and
+    // class, their prefix with the widest class first, then the places.
+    for (int c = warp; c * 32 < p.G; c += kThreads / 32) {
+      const int g = c * 32 + lane;
+      const int k = g < p.G ? kClasses - tile_width(group_count(sh, p, g)) / kColStep : -1;  // 0: widest
+      int place = 0;
+      for (int i = 0; i <= kClasses; ++i) {
+        const unsigned m = __ballot_sync(0xffffffffu, k == i);
+        if (k == i) place = __popc(m & ((1u << lane) - 1));
+        if (lane == i) sh.class_count[c][i] = (uint16_t)__popc(m);
+      }
+      if (g < p.G) sh.first_tile[g] = k << 16 | place;  // kept until the places are known
+    }
+    __syncthreads();
+    if (warp == 2) {
+      int carry = 0;
+      for (int i = 0; i <= kClasses; ++i) {
+        const int n = lane * 32 < p.G ? sh.class_count[lane][i] : 0;
+        const int incl = afd::warp_inclusive_scan(n);
+        if (lane * 32 < p.G) sh.class_count[lane][i] = (uint16_t)(carry + incl - n);
+        carry += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    __syncthreads();
+    for (int g = threadIdx.x; g < p.G; g += kThreads) {
+      const int v = sh.first_tile[g];
+      sh.order[sh.class_count[g >> 5][v >> 16] + (v & 0xffff)] = (uint16_t)g;
+    }
+    __syncthreads();
+    if (warp == 2) {
+      int carry = 0;
+      for (int i0 = 0; i0 < p.G; i0 += 32) {
+        const int i = i0 + lane;
+        const int n = i < p.G ? row_tiles(group_count(sh, p, sh.order[i])) * p.m_tiles : 0;
+        const int incl = afd::warp_inclusive_scan(n);
+        if (i < p.G) sh.first_tile[i] = carry + incl - n;
+        carry += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    __syncthreads();
+  }
+  const int tiles = sh.first_tile[p.G];
+  if (threadIdx.x < kListed) {
+    const int t = dealt(threadIdx.x, pair, pairs);
+    if (t < tiles) sh.list[threadIdx.x] = find_tile(sh, p, t);
   }
   afd::tcgen05_fence_before();
   __syncthreads();
   afd::cluster_sync_all();
   afd::tcgen05_fence_after();
   const uint32_t tmem = sh.tmem;
-  const int tiles = sh.first_tile[p.G];
   volatile int* gave_up = &sh.gave_up;
+  // as many accumulators of the widest tile's columns (a power of two) as fit
+  const int wide = 32 - __clz(sh.widest - 1);
+  const int buf_shift = min(wide < 6 ? 3 : 9 - wide, 3);
+  const Turns turns = {tmem, drain_full, drained, buf_shift, kColumns >> buf_shift};
 
   if (warp < 4) {
   if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFrontRegs));
@@ -294,14 +416,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t lead_full = afd::map_to_rank(full, 0);
     uint32_t it = 0;
     bool ok = true;
-    for (int t = pair; ok && t < tiles; t += pairs) {
-      const Tile tile = find_tile(sh, p, t);
-      const int half = tile.cols >> 1;
+    Tile tile;
+    for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
+      const int half = tile.cols() >> 1;
       const int row = tile.row + (int)rank * half;
       const uint32_t bytes = 2 * (kHalfBytes + half * kBlockBytes);
       const CUtensorMap* x_map = &maps.x[half / 16 - 1];
       // this weight tile is read again if the expert has more row tiles
-      const uint64_t w_policy = sh.first_tile[tile.group + 1] - sh.first_tile[tile.group] == p.m_tiles ? once : keep;
+      const uint64_t w_policy = tile.rows == group_count(sh, p, tile.group) ? once : keep;
       const int w_row = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) : tile.m * kPairRows + (int)rank * kCtaRows;
       for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
         const uint32_t s = it % kStages, ph = (it / kStages) & 1;
@@ -336,13 +458,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       uint32_t it = 0, unit = 0;
       bool ok = true;
-      for (int t = pair; ok && t < tiles; t += pairs) {
-        const Tile tile = find_tile(sh, p, t);
-        const uint32_t idesc = afd::instr_desc(FP8, kPairRows, tile.cols);
+      Tile tile;
+      for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
+        const uint32_t idesc = afd::instr_desc(FP8, kPairRows, tile.cols());
         for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
           const bool opens = FP8 || kb == 0, closes = FP8 || kb == p.k_blocks - 1;
           if (opens) {
-            ok = __all_sync(0xffffffffu, afd::mbar_wait(drain_empty + 8 * (unit & 1), ((unit >> 1) & 1) ^ 1, gave_up));
+            const uint32_t buf = turns.buf(unit), ph = turns.phase(unit) ^ 1;
+            ok = __all_sync(0xffffffffu, afd::mbar_wait(drained + 8 * buf, ph, gave_up) &&
+                                             afd::mbar_wait(peer_drained + 8 * buf, ph, gave_up));
             if (!ok) break;
           }
           const uint32_t s = it % kStages, ph = (it / kStages) & 1;
@@ -350,13 +474,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           afd::tcgen05_fence_after();
           const uint64_t a = afd::operand_desc(smem + s * kStageBytes);
           const uint64_t b = afd::operand_desc(smem + s * kStageBytes + kHalfBytes);
-          const uint32_t d = tmem + (unit & 1) * (kColumns / 2);
+          const uint32_t d = tmem + turns.buf(unit) * turns.cols;
           if (afd::elect_one()) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)  // 32 bytes of K each
               afd::mma_pair<FP8>(d, a + 2 * i, b + 2 * i, idesc, !(opens && i == 0));
             afd::mma_commit_pair(empty + 8 * s);
-            if (closes) afd::mma_commit_pair(drain_full + 8 * (unit & 1));
+            if (closes) afd::mma_commit_pair(drain_full + 8 * turns.buf(unit));
           }
           __syncwarp();
           if (closes) ++unit;
@@ -368,6 +492,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (clock64() - t0 < 2000000) {
         }
       }
+    } else {
+      // The odd CTA's warp passes on that its accumulators are read: one
+      // arrival across the pair instead of one for every draining warp.
+      const uint32_t lead = afd::map_to_rank(peer_drained, 0);
+      uint32_t unit = 0;
+      bool ok = true;
+      for (int turn = 0; ok && dealt(turn, pair, pairs) < tiles; ++turn) {
+        for (int kb = 0; kb < (FP8 ? p.k_blocks : 1); ++kb, ++unit) {
+          const uint32_t buf = turns.buf(unit);
+          if (!(ok = __all_sync(0xffffffffu, afd::mbar_wait(drained + 8 * buf, turns.phase(unit), gave_up)))) break;
+          if (lane == 0) afd::mbar_arrive_cluster(lead + 8 * buf);
+        }
+      }
     }
     __syncwarp();
   } else {
@@ -377,8 +514,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int64_t w_rows = (int64_t)(GATED ? 2 : 1) * p.N / 128;
       uint32_t it = 0;
       bool ok = true;
-      for (int t = pair; ok && t < tiles; t += pairs) {
-        const Tile tile = find_tile(sh, p, t);
+      Tile tile;
+      for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
         const float* xs = p.x_scale + (int64_t)(tile.row + u) * p.k_blocks;
         // the weight block of this CTA's rows (the last one for rows past N, which are not stored)
         const int f = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) : tile.m * kPairRows + (int)rank * kCtaRows;
@@ -421,37 +558,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------------- accumulators
     if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
     const int q = warp & 3, h = (warp - 4) >> 2;  // lanes 32 q .. of TMEM; every fourth 16 columns
-    const uint32_t lead_empty = afd::map_to_rank(drain_empty, 0);
-    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+    Turns mine = turns;
+    mine.tmem += (uint32_t)(32 * q) << 16;
     uint32_t unit = 0;
     bool ok = true;
-    for (int t = pair; ok && t < tiles; t += pairs) {
-      const Tile tile = find_tile(sh, p, t);
+    Tile tile;
+    for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
       const int n0 = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) + 16 * q
                            : tile.m * kPairRows + (int)rank * kCtaRows + 32 * q;
+      const Out out = lane_out<GATED>(p, tile, n0, lane);
       if (!FP8) {
-        ok = __all_sync(0xffffffffu, afd::mbar_wait(drain_full + 8 * (unit & 1), (unit >> 1) & 1, gave_up));
+        const uint32_t b = turns.buf(unit);
+        ok = __all_sync(0xffffffffu, afd::mbar_wait(drain_full + 8 * b, turns.phase(unit), gave_up));
         if (!ok) break;
         afd::tcgen05_fence_after();
-        const uint32_t acc = lanes + (unit & 1) * (kColumns / 2);
-        for (int c = 16 * h; c < tile.cols; c += 16 * kDrainParts) {
+        for (int c = 16 * h; c < tile.cols(); c += 16 * kDrainParts) {
           float v[16];
-          afd::tmem_load16(acc + c, v);
-          store16<GATED>(p, tile, c, n0, lane, v);
+          afd::tmem_load16(mine.tmem + b * turns.cols + c, v);
+          store16<GATED>(p, tile, out, c, lane, v);
         }
         afd::tcgen05_fence_before();
         __syncwarp();
-        if (lane == 0) afd::mbar_arrive_cluster(lead_empty + 8 * (unit & 1));
+        if (lane == 0) afd::mbar_arrive(drained + 8 * b);
         ++unit;
       } else {
         // this warp's 16-column steps of the tile
-        const int steps = max(0, (tile.cols - 16 * h + 16 * kDrainParts - 1) / (16 * kDrainParts));
-        const Drain d = {lanes + 16 * h, drain_full, lead_empty, scale_full, scale_empty, h, n0, lane};
-        if (steps == 4) ok = drain_blocks<GATED, 4>(p, sh, tile, d, unit);
-        else if (steps == 3) ok = drain_blocks<GATED, 3>(p, sh, tile, d, unit);
-        else if (steps == 2) ok = drain_blocks<GATED, 2>(p, sh, tile, d, unit);
-        else if (steps == 1) ok = drain_blocks<GATED, 1>(p, sh, tile, d, unit);
-        else ok = drain_blocks<GATED, 0>(p, sh, tile, d, unit);
+        const int steps = max(0, (tile.cols() - 16 * h + 16 * kDrainParts - 1) / (16 * kDrainParts));
+        if (steps == 4) ok = drain_blocks<GATED, 4>(p, sh, tile, mine, out, h, lane, unit);
+        else if (steps == 3) ok = drain_blocks<GATED, 3>(p, sh, tile, mine, out, h, lane, unit);
+        else if (steps == 2) ok = drain_blocks<GATED, 2>(p, sh, tile, mine, out, h, lane, unit);
+        else if (steps == 1) ok = drain_blocks<GATED, 1>(p, sh, tile, mine, out, h, lane, unit);
+        else ok = drain_blocks<GATED, 0>(p, sh, tile, mine, out, h, lane, unit);
       }
     }
   }
