@@ -107,7 +107,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "afd_gated_rows": (i32, [v, i64, v, i32, i32, i64, i32, v, i64, v]),
         "afd_adapter_add": (i32, [v, i64, v, i64, v, v, v, v, v, v, i32, i32, i64, i32, i32, i32, i32,
                                   i32, v, i64, v, i64, v]),
-        "afd_adapter_workspace_bytes": (i64, [i64, i32]),
+        "afd_adapter_workspace_bytes": (i64, [i64, i32, i32]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -608,11 +608,11 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
         out, out_stride = base, base_stride
     else:
         out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
-    words = R + S + 2
-    workspace = torch.empty(words, dtype=torch.int32, device=x.device)
+    size = (_lib or load_library()).afd_adapter_workspace_bytes(R, S, rank)
+    workspace = torch.empty(max(size, 0), dtype=torch.uint8, device=x.device)
     if stream is not None:  # the allocator must not hand it on before that stream is done with it
         workspace.record_stream(stream)
     _call("afd_adapter_add", workspace, stream, base.data_ptr(), base_stride, x.data_ptr(), x_stride, down_ptr, up_ptr,
           slots_ptr, scales_ptr, src_ptr, ends_ptr, G, top_k, R, tokens, S, rank, K, N, out.data_ptr(), out_stride,
-          workspace.data_ptr(), 4 * words)
+          workspace.data_ptr(), size)
     return out

@@ -79,34 +79,37 @@ struct AdapterParams {
   int64_t out_stride;
   int32_t* first;  // workspace: where each adapter's rows start in `order`, [S + 2]
   int32_t* order;  // workspace: the live rows by adapter, [R]
+  uint16_t *t_hi, *t_lo;  // workspace: scale * down[a] x of each of them, [R][rank]
 };
 
-// Low-rank adapters, in two launches. The first groups the rows by adapter
-// (a request's rows are spread over every expert's range, so rows that follow
-// one another mostly differ in theirs): a permutation of the live rows, sorted
-// by adapter, and where each adapter starts. In the second a cluster of four
-// CTAs takes up to 64 rows of one adapter at a time:
-//   down: t = down[a] x, K split over the cluster's CTAs and four warps in
-//         each, the parts joined through distributed shared memory in a fixed
-//         order;
-//   up:   out = base + (scale t) up[a], the columns split the same way.
-// The operands go from global memory straight into registers: the order of K
-// (and of the output's columns) inside a fragment is free as long as both
-// sides agree, so a thread takes eight neighbouring values, 16 bytes at a time.
+// Low-rank adapters, in three launches that follow each other by programmatic
+// dependent launch.
+//   group: the live rows sorted by adapter (a request's rows are spread over
+//          every expert's range, so rows that follow one another mostly differ
+//          in theirs), and where each adapter starts.
+//   down:  t = scale * down[a] x for 16 rows of one adapter a block, K split
+//          over its eight warps and joined in a fixed order.
+//   up:    out = base + up[a] t for 16 rows and some of the columns a warp, 32
+//          columns at a time with the next ones' operands on their way; rows
+//          without an adapter are copied.
 // What bounds it is the traffic of x, base and out (about 6 bytes a column and
-// row against 2 rank flops): mma.sync's rate is enough, and its register
-// operands spare the copies through shared memory and TMEM. A product's rows
-// do not mix, so neither the order of the rows inside a group nor what another
-// request's adapter holds reaches a result.
-// t is FP32; for the up product it is split into two BF16 (16 bits and more).
+// row against 2 rank flops), which down and up stream with many small blocks
+// in flight. mma.sync's rate is enough, and its register operands spare TMEM
+// and the layout it wants: the order of K (and of the output's columns) inside
+// a fragment is free as long as both sides agree, so a thread takes eight
+// neighbouring values, 16 bytes at a time. A product's rows do not mix, so
+// neither the order of the rows inside a group nor what another request's
+// adapter holds reaches a result.
+// t is FP32; between the two it is kept as two BF16 (16 bits and more).
 constexpr int kMaxSlots = 1024;
 constexpr int kGroupCtas = 8;
 constexpr int kGroupThreads = 1024;
-constexpr int kAdRows = 64;
-constexpr int kAdCtas = 4;      // a cluster's CTAs
-constexpr int kAdParts = 4;     // warps of a CTA that share 32 rows
-constexpr int kAdSplit = kAdCtas * kAdParts;
-constexpr int kAdThreads = 256;
+constexpr int kGroupKeep = 4;      // rows of a thread whose group it remembers
+constexpr int kDownRows = 16;      // rows of a block
+constexpr int kDownWarps = 8;      // ... whose warps share K
+constexpr int kUpRows = 64;        // rows of a tile: 16 for each of four warps
+constexpr int kUpThreads = 256;
+constexpr int kUpStages = 4;       // column groups whose operands are in flight
 
 // The group of a row: its adapter, S for none, -1 for what is not a row.
 __device__ __forceinline__ int row_group(const AdapterParams& p, int r) {
@@ -146,11 +149,21 @@ __global__ void __cluster_dims__(kGroupCtas, 1, 1) __launch_bounds__(kGroupThrea
   const int64_t lo = (int64_t)cta * share, hi = lo + share < limit ? lo + share : limit;
   for (int g = threadIdx.x; g < groups; g += kGroupThreads) count[g] = 0;
   __syncthreads();
-  for (int64_t r0 = lo + 32 * warp; r0 < hi; r0 += kGroupThreads) {
-    const int g = r0 + lane < hi ? row_group(p, (int)r0 + lane) : -1;
+  // The first rows' groups stay in registers, all their loads in flight at once.
+  int keep[kGroupKeep];
+#pragma unroll
+  for (int i = 0; i < kGroupKeep; ++i) {
+    const int64_t r = lo + i * kGroupThreads + threadIdx.x;
+    keep[i] = r < hi ? row_group(p, (int)r) : -1;
+  }
+  auto tally = [&](int g) {
     const unsigned same = __match_any_sync(0xffffffffu, g);
     if (g >= 0 && lane == __ffs(same) - 1) atomicAdd(&count[g], __popc(same));
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kGroupKeep; ++i) tally(keep[i]);
+  const int64_t rest = lo + kGroupKeep * kGroupThreads + 32 * warp;
+  for (int64_t r0 = rest; r0 < hi; r0 += kGroupThreads) tally(r0 + lane < hi ? row_group(p, (int)r0 + lane) : -1);
   cluster_sync();
   // a thread takes `each` neighbouring groups of the prefix sum
   const int each = (groups + kGroupThreads - 1) / kGroupThreads;
@@ -184,14 +197,16 @@ __global__ void __cluster_dims__(kGroupCtas, 1, 1) __launch_bounds__(kGroupThrea
     if (cta == 0 && g == groups - 1) p.first[groups] = run;
   }
   __syncthreads();
-  for (int64_t r0 = lo + 32 * warp; r0 < hi; r0 += kGroupThreads) {
-    const int g = r0 + lane < hi ? row_group(p, (int)r0 + lane) : -1;
+  auto place = [&](int g, int64_t r) {
     const unsigned same = __match_any_sync(0xffffffffu, g);
     int at = 0;
     if (g >= 0 && lane == __ffs(same) - 1) at = atomicAdd(&cursor[g], __popc(same));
     at = __shfl_sync(0xffffffffu, at, __ffs(same) - 1) + __popc(same & ((1u << lane) - 1));
-    if (g >= 0) p.order[at] = (int)r0 + lane;
-  }
+    if (g >= 0) p.order[at] = (int)r;
+  };
+#pragma unroll
+  for (int i = 0; i < kGroupKeep; ++i) place(keep[i], lo + i * kGroupThreads + threadIdx.x);
+  for (int64_t r0 = rest; r0 < hi; r0 += kGroupThreads) place(r0 + lane < hi ? row_group(p, (int)r0 + lane) : -1, r0 + lane);
   cluster_sync();  // nobody leaves while its counts may be read
 }
 
@@ -202,244 +217,303 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int RANK>
-struct AdapterShared {
-  static constexpr int kPad = RANK + 4;    // FP32 row
-  static constexpr int kPadH = RANK + 8;   // BF16 row
-  alignas(16) float part[kAdParts][kAdRows][kPad];
-  alignas(16) uint16_t hi[kAdRows][kPadH], lo[kAdRows][kPadH];
-  int first[kMaxSlots + 2];       // of the order: where each group starts
+// Where the groups start, in rows and in tiles of ROWS rows (of the first
+// `groups` groups).
+struct GroupTable {
+  int first[kMaxSlots + 2];
   int first_tile[kMaxSlots + 2];
 };
 
+template <int ROWS>
+__device__ __forceinline__ int load_groups(const AdapterParams& p, GroupTable& sh, int groups) {
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i <= groups; i += blockDim.x) sh.first[i] = p.first[i];
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int carry = 0;
+    for (int i0 = 0; i0 < groups; i0 += 32) {
+      const int i = i0 + lane;
+      const int t = i < groups ? (sh.first[i + 1] - sh.first[i] + ROWS - 1) / ROWS : 0;
+      const int incl = afd::warp_inclusive_scan(t);
+      if (i < groups) sh.first_tile[i] = carry + incl - t;
+      carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) sh.first_tile[groups] = carry;
+  }
+  __syncthreads();
+  return sh.first_tile[groups];
+}
+
+// The group of tile t: the last one that starts at or before it.
+__device__ __forceinline__ int tile_group(const GroupTable& sh, int groups, int t) {
+  int a = 0;
+  for (int hi = groups - 1; a < hi;) {
+    const int mid = (a + hi + 1) >> 1;
+    if (sh.first_tile[mid] <= t) a = mid; else hi = mid - 1;
+  }
+  return a;
+}
+
 template <int RANK>
-__global__ void __cluster_dims__(kAdCtas, 1, 1) __launch_bounds__(kAdThreads, RANK <= 32 ? 2 : 1)
-    adapter_kernel(const AdapterParams p) {
-  using Sh = AdapterShared<RANK>;
+struct DownShared {
+  static constexpr int kPad = RANK + 4;
+  alignas(16) float part[kDownWarps][kDownRows][kPad];
+  GroupTable groups;
+};
+
+template <int RANK>
+__global__ void __launch_bounds__(kDownWarps * 32, 4) adapter_down_kernel(const AdapterParams p) {
+  __shared__ DownShared<RANK> sh;
+  constexpr int NT = RANK / 8;             // 8-column tiles of the product
+  constexpr int U = RANK <= 32 ? 4 : 2;    // K chunks of 32 loaded together
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, tig = lane & 3;
+  const int chunks = (p.K + 31) >> 5;
+  afd::pdl_launch_dependents();
+  afd::pdl_wait();
+  const int tiles = load_groups<kDownRows>(p, sh.groups, p.S);
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int a = tile_group(sh.groups, p.S, t);
+    const int at = sh.groups.first[a] + (t - sh.groups.first_tile[a]) * kDownRows, end = sh.groups.first[a + 1];
+    const uint16_t* x[2];  // this thread's rows: g / g + 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = at + 8 * h + g;
+      x[h] = i < end ? p.x + p.order[i] * p.x_stride : nullptr;
+    }
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    const uint16_t* down = p.down + ((int64_t)a * RANK + g) * p.K;
+    for (int c0 = warp; c0 < chunks; c0 += U * kDownWarps) {
+      uint4 xv[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = (c0 + u * kDownWarps) * 32 + tig * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          xv[u][h] = k < p.K && x[h] ? afd::ld_once(reinterpret_cast<const uint4*>(x[h] + k)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = (c0 + u * kDownWarps) * 32 + tig * 8;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint4 b = k < p.K ? __ldg(reinterpret_cast<const uint4*>(down + (int64_t)n * 8 * p.K + k)) : make_uint4(0, 0, 0, 0);
+          mma_16816(acc[n], xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y, b.x, b.y);
+          mma_16816(acc[n], xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w, b.z, b.w);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(&sh.part[warp][8 * h + g][8 * n + 2 * tig]) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+    __syncthreads();
+    const float scale = p.scales[a];
+    for (int i = threadIdx.x; i < kDownRows * RANK / 2; i += kDownWarps * 32) {
+      const int r = i / (RANK / 2), c = i % (RANK / 2) * 2;
+      if (at + r >= end) continue;
+      float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kDownWarps; ++w) {
+        const float2 o = *reinterpret_cast<const float2*>(&sh.part[w][r][c]);
+        v.x += o.x, v.y += o.y;
+      }
+      v.x *= scale, v.y *= scale;
+      const uint32_t hi = afd::pack_bf16(v.x, v.y);
+      // (an infinite product leaves no rest)
+      const uint32_t lo = afd::pack_bf16(isinf(v.x) ? 0.f : v.x - __uint_as_float(hi << 16),
+                                         isinf(v.y) ? 0.f : v.y - __uint_as_float(hi & 0xffff0000u));
+      const int64_t o = (int64_t)(at + r) * RANK + c;
+      *reinterpret_cast<uint32_t*>(p.t_hi + o) = hi;
+      *reinterpret_cast<uint32_t*>(p.t_lo + o) = lo;
+    }
+    __syncthreads();
+  }
+}
+
+// EL rank values (EL / 2 words) of a thread.
+template <int EL>
+__device__ __forceinline__ void load_rank(const uint16_t* q, bool in, uint32_t (&v)[EL / 2]) {
+  if (EL == 8) {
+    const uint4 w = in ? *reinterpret_cast<const uint4*>(q) : make_uint4(0, 0, 0, 0);
+    v[0] = w.x, v[1 % (EL / 2)] = w.y, v[2 % (EL / 2)] = w.z, v[3 % (EL / 2)] = w.w;
+  } else if (EL == 4) {
+    const uint2 w = in ? *reinterpret_cast<const uint2*>(q) : make_uint2(0, 0);
+    v[0] = w.x, v[1 % (EL / 2)] = w.y;
+  } else {
+    v[0] = in ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+  }
+}
+
+// Asynchronous copies of BYTES (4, 8 or 16) into shared memory; nothing is
+// read where `in` is false, and zeros are written.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool in) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  const int n = in ? BYTES : 0;
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+
+// Operands of one 32-column group on their way: every thread copies exactly
+// what it uses itself, so no other thread has to be waited for.
+template <int RANK>
+struct UpStage {
+  static constexpr int EL = RANK >= 32 ? 8 : RANK / 4;  // rank values a thread takes at a time
+  static constexpr int CH = RANK >= 32 ? RANK / 32 : 1;  // ... and how often
+  uint4 base[2][32];                                    // rows g / g + 8
+  struct alignas(EL * 2) { uint32_t v[EL / 2]; } up[4][CH][32];
+};
+
+template <int RANK>
+struct UpShared {
+  alignas(16) UpStage<RANK> stage[kUpThreads / 32][kUpStages];
+  GroupTable groups;
+};
+
+template <int RANK>
+__global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_kernel(const AdapterParams p) {
   extern __shared__ __align__(16) uint8_t ad_smem[];
-  Sh& sh = *reinterpret_cast<Sh*>(ad_smem);
-  constexpr int NT = RANK / 8;                        // 8-column tiles of the down product
-  constexpr int U = RANK <= 32 ? 4 : 2;               // K chunks of 32 loaded together
-  constexpr int EL = RANK >= 32 ? 8 : RANK / 4;       // rank values a thread takes at a time
-  constexpr int CH = RANK >= 32 ? RANK / 32 : 1;      // ... and how often
+  UpShared<RANK>& sh = *reinterpret_cast<UpShared<RANK>*>(ad_smem);
+  constexpr int EL = UpStage<RANK>::EL, CH = UpStage<RANK>::CH;
   constexpr int STEPS = EL == 8 ? 2 : 1;              // products per chunk
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tig = lane & 3;
-  const int wr = warp & 1, wk = warp >> 1;            // half of the rows; part of K and of the columns
-  const int cta = blockIdx.x % kAdCtas, cluster = blockIdx.x / kAdCtas, clusters = gridDim.x / kAdCtas;
-  const int part = cta * kAdParts + wk;
-  const int chunks = (p.K + 31) >> 5, col_groups = (p.N + 31) >> 5;
-  bool open = false;  // this CTA has told the cluster that it has read its parts, and not waited yet
-
-  afd::pdl_wait();  // the grouping
-  for (int i = threadIdx.x; i < p.S + 2; i += kAdThreads) sh.first[i] = p.first[i];
-  __syncthreads();
-  if (warp == 0) {
-    int carry = 0;
-    for (int i0 = 0; i0 <= p.S; i0 += 32) {
-      const int i = i0 + lane;
-      const int t = i <= p.S ? (sh.first[i + 1] - sh.first[i] + kAdRows - 1) / kAdRows : 0;
-      const int incl = afd::warp_inclusive_scan(t);
-      if (i <= p.S) sh.first_tile[i] = carry + incl - t;
-      carry += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) sh.first_tile[p.S + 1] = carry;
-  }
-  __syncthreads();
-  const int tiles = sh.first_tile[p.S + 1];
-
-  for (int t = cluster; t < tiles; t += clusters) {
-    int a = 0;  // the last group that starts at or before this tile
-    for (int hi = p.S; a < hi;) {
-      const int mid = (a + hi + 1) >> 1;
-      if (sh.first_tile[mid] <= t) a = mid; else hi = mid - 1;
-    }
-    const int at = sh.first[a] + (t - sh.first_tile[a]) * kAdRows, end = sh.first[a + 1];
-    int64_t row[2][2];  // of this thread: [16-row tile][g / g + 8]; -1: none
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = at + 32 * wr + 16 * s + 8 * h + g;
-        row[s][h] = i < end ? p.order[i] : -1;
-      }
+  const int col_groups = (p.N + 31) >> 5, slots = gridDim.x * (kUpThreads / 32);
+  UpStage<RANK>* stage = sh.stage[warp];
+  afd::pdl_wait();
+  const int tiles = load_groups<kUpRows>(p, sh.groups, p.S + 1);
+  // The columns are split so far that every warp has something to do.
+  const int want = max(1, min(col_groups, slots / max(4 * tiles, 1)));
+  const int each = (col_groups + want - 1) / want, parts = (col_groups + each - 1) / each;
+  const int64_t items = (int64_t)tiles * parts * 4;
+  for (int64_t item = (int64_t)blockIdx.x * (kUpThreads / 32) + warp; item < items; item += slots) {
+    const int quarter = (int)(item & 3);
+    const int t = (int)((item >> 2) / parts), part = (int)((item >> 2) % parts);
+    const int a = tile_group(sh.groups, p.S + 1, t);
+    const int at = sh.groups.first[a] + (t - sh.groups.first_tile[a]) * kUpRows + 16 * quarter, end = sh.groups.first[a + 1];
+    if (at >= end) continue;
+    const int g0 = part * each, g1 = min(g0 + each, col_groups);
     const bool adapt = a < p.S;  // the last group has no adapter: its rows are copied
-
-    if (adapt) {
-      // ---------------------------------------------------------------- down
-      float acc[2][NT][4];
+    const uint16_t* base[2];     // this thread's rows at its first column: g / g + 8
+    uint16_t* out[2];
+    uint32_t th[2][CH][EL / 2], tl[2][CH][EL / 2];
+    bool live[2];
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+    for (int h = 0; h < 2; ++h) {
+      const int i = at + 8 * h + g;
+      live[h] = i < end;
+      const int64_t r = live[h] ? p.order[i] : 0;
+      base[h] = p.base + r * p.base_stride + tig * 8;
+      out[h] = p.out + r * p.out_stride + tig * 8;
+    }
+    // column tile i holds columns 8 j + 2 i and 8 j + 2 i + 1, so that a thread
+    // ends with eight neighbouring ones
+    const int col = (g >> 1) * 8 + (g & 1);
+    const uint16_t* up = p.up + ((int64_t)(adapt ? a : 0) * p.N + col) * RANK + tig * EL;
+    auto fetch = [&](int gi) {
+      if (gi < g1) {
+        UpStage<RANK>& st = stage[gi % kUpStages];
+        const int n0 = gi * 32;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[s][n][i] = 0.f;
-      const uint16_t* down = p.down + ((int64_t)a * RANK + g) * p.K;
-      for (int c0 = part; c0 < chunks; c0 += U * kAdSplit) {
-        uint4 xv[U][2][2];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int k = (c0 + u * kAdSplit) * 32 + tig * 8;
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              xv[u][s][h] = k < p.K && row[s][h] >= 0
-                                ? afd::ld_once(reinterpret_cast<const uint4*>(p.x + row[s][h] * p.x_stride + k))
-                                : make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < 2; ++h) {
+          const bool in = live[h] && n0 + tig * 8 < p.N;
+          copy_async<16>(&st.base[h][lane], in ? base[h] + n0 : p.base, in);
         }
+        if (adapt) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int k = (c0 + u * kAdSplit) * 32 + tig * 8;
+          for (int i = 0; i < 4; ++i) {
+            const bool in = n0 + col + 2 * i < p.N;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint4 b = k < p.K ? __ldg(reinterpret_cast<const uint4*>(down + (int64_t)n * 8 * p.K + k)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const uint4 &x0 = xv[u][s][0], &x1 = xv[u][s][1];
-              mma_16816(acc[s][n], x0.x, x1.x, x0.y, x1.y, b.x, b.y);
-              mma_16816(acc[s][n], x0.z, x1.z, x0.w, x1.w, b.z, b.w);
-            }
+            for (int q = 0; q < CH; ++q)
+              copy_async<2 * EL>(&st.up[i][q][lane], in ? up + (int64_t)(n0 + 2 * i) * RANK + q * 32 : p.up, in);
           }
         }
       }
-      if (open) {  // the others have read the last tile's parts
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        open = false;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kUpStages - 1; ++i) fetch(g0 + i);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < CH; ++q) {
+        const int64_t o = (int64_t)(at + 8 * h + g) * RANK + q * 32 + tig * EL;
+        load_rank<EL>(p.t_hi + o, live[h] && adapt, th[h][q]);
+        load_rank<EL>(p.t_lo + o, live[h] && adapt, tl[h][q]);
       }
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float2*>(&sh.part[wk][32 * wr + 16 * s + 8 * h + g][8 * n + 2 * tig]) =
-                make_float2(acc[s][n][2 * h], acc[s][n][2 * h + 1]);
-      __syncthreads();
-      for (int i = threadIdx.x; i < kAdRows * RANK / 2; i += kAdThreads) {
-        const int r = i / (RANK / 2), c = i % (RANK / 2) * 2;
-        float2 v = *reinterpret_cast<const float2*>(&sh.part[0][r][c]);
-#pragma unroll
-        for (int w = 1; w < kAdParts; ++w) {
-          const float2 o = *reinterpret_cast<const float2*>(&sh.part[w][r][c]);
-          v.x += o.x, v.y += o.y;
-        }
-        *reinterpret_cast<float2*>(&sh.part[0][r][c]) = v;
-      }
-      cluster_sync();
-      const float scale = p.scales[a];
-      for (int i = threadIdx.x; i < kAdRows * RANK / 2; i += kAdThreads) {
-        const int r = i / (RANK / 2), c = i % (RANK / 2) * 2;
-        float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kAdCtas; ++w) {
-          float2 o;
-          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(o.x), "=f"(o.y) : "r"(remote(&sh.part[0][r][c], w)) : "memory");
-          v.x += o.x, v.y += o.y;
-        }
-        v.x *= scale, v.y *= scale;
-        const uint32_t hi = afd::pack_bf16(v.x, v.y);
-        *reinterpret_cast<uint32_t*>(&sh.hi[r][c]) = hi;
-        // (an infinite product leaves no rest)
-        *reinterpret_cast<uint32_t*>(&sh.lo[r][c]) =
-            afd::pack_bf16(isinf(v.x) ? 0.f : v.x - __uint_as_float(hi << 16),
-                           isinf(v.y) ? 0.f : v.y - __uint_as_float(hi & 0xffff0000u));
-      }
-      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-      open = true;
-      __syncthreads();
-    }
-
-    // -------------------------------------------------------------------- up
-    uint32_t th[2][2][CH][EL / 2], tl[2][2][CH][EL / 2];  // [tile][g / g + 8]
-    if (adapt) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int q = 0; q < CH; ++q)
-#pragma unroll
-            for (int e = 0; e < EL / 2; ++e) {
-              const int r = 32 * wr + 16 * s + 8 * h + g, c = q * 32 + tig * EL + 2 * e;
-              th[s][h][q][e] = *reinterpret_cast<const uint32_t*>(&sh.hi[r][c]);
-              tl[s][h][q][e] = *reinterpret_cast<const uint32_t*>(&sh.lo[r][c]);
-            }
-    }
-    for (int gi = part; gi < col_groups; gi += kAdSplit) {
+    for (int gi = g0; gi < g1; ++gi) {
+      fetch(gi + kUpStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kUpStages - 1) : "memory");
+      const UpStage<RANK>& st = stage[gi % kUpStages];
       const int n0 = gi * 32;
-      const bool in = n0 + tig * 8 < p.N;  // this thread's eight output columns
-      uint4 bv[2][2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (in && row[s][h] >= 0) bv[s][h] = *reinterpret_cast<const uint4*>(p.base + row[s][h] * p.base_stride + n0 + tig * 8);
+      uint4 bv[2] = {st.base[0][lane], st.base[1][lane]};
       if (adapt) {
-        float acc[2][4][4];  // [row tile][column tile]
+        float acc[4][4];  // [column tile]
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // column tile i holds columns 8 j + 2 i and 8 j + 2 i + 1, so that a
-          // thread ends with eight neighbouring ones
-          const int n = n0 + (g >> 1) * 8 + 2 * i + (g & 1);
-          const uint16_t* up = p.up + ((int64_t)a * p.N + n) * RANK + tig * EL;
 #pragma unroll
-          for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[s][i][e] = 0.f;
+          for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 #pragma unroll
           for (int q = 0; q < CH; ++q) {
-            uint32_t b[EL / 2];
-            if (EL == 8) {
-              const uint4 v = n < p.N ? __ldg(reinterpret_cast<const uint4*>(up + q * 32)) : make_uint4(0, 0, 0, 0);
-              b[0] = v.x, b[1 % (EL / 2)] = v.y, b[2 % (EL / 2)] = v.z, b[3 % (EL / 2)] = v.w;
-            } else if (EL == 4) {
-              const uint2 v = n < p.N ? __ldg(reinterpret_cast<const uint2*>(up)) : make_uint2(0, 0);
-              b[0] = v.x, b[1 % (EL / 2)] = v.y;
-            } else {
-              b[0] = n < p.N ? __ldg(reinterpret_cast<const uint32_t*>(up)) : 0u;
+            const auto b = st.up[i][q][lane];
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+              const int e0 = 2 * s, e1 = EL == 2 ? 0 : 2 * s + 1;
+              const bool two = EL != 2;  // rank 8 fills half of a product's K
+              mma_16816(acc[i], th[0][q][e0], th[1][q][e0], two ? th[0][q][e1] : 0u, two ? th[1][q][e1] : 0u, b.v[e0],
+                        two ? b.v[e1] : 0u);
+              mma_16816(acc[i], tl[0][q][e0], tl[1][q][e0], two ? tl[0][q][e1] : 0u, two ? tl[1][q][e1] : 0u, b.v[e0],
+                        two ? b.v[e1] : 0u);
             }
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-              for (int st = 0; st < STEPS; ++st) {
-                const int e0 = 2 * st, e1 = EL == 2 ? 0 : 2 * st + 1;
-                const bool two = EL != 2;  // rank 8 fills half of a product's K
-                mma_16816(acc[s][i], th[s][0][q][e0], th[s][1][q][e0], two ? th[s][0][q][e1] : 0u, two ? th[s][1][q][e1] : 0u,
-                          b[e0], two ? b[e1] : 0u);
-                mma_16816(acc[s][i], tl[s][0][q][e0], tl[s][1][q][e0], two ? tl[s][0][q][e1] : 0u, two ? tl[s][1][q][e1] : 0u,
-                          b[e0], two ? b[e1] : 0u);
-              }
           }
         }
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int h = 0; h < 2; ++h) {
+          float f[8];
+          afd::bf16x8_to_float(bv[h], f);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float f[8];
-            afd::bf16x8_to_float(bv[s][h], f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              f[2 * i] += acc[s][i][2 * h];
-              f[2 * i + 1] += acc[s][i][2 * h + 1];
-            }
-            bv[s][h] = afd::float_to_bf16x8(f);
+          for (int i = 0; i < 4; ++i) {
+            f[2 * i] += acc[i][2 * h];
+            f[2 * i + 1] += acc[i][2 * h + 1];
           }
+          bv[h] = afd::float_to_bf16x8(f);
+        }
       }
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (in && row[s][h] >= 0) *reinterpret_cast<uint4*>(p.out + row[s][h] * p.out_stride + n0 + tig * 8) = bv[s][h];
+      for (int h = 0; h < 2; ++h)
+        if (live[h] && n0 + tig * 8 < p.N) *reinterpret_cast<uint4*>(out[h] + n0) = bv[h];
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
-  if (open) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <typename K>
+cudaError_t launch_after(K kernel, int grid, int block, size_t smem, const AdapterParams& p, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <int RANK>
 cudaError_t launch_adapters(const AdapterParams& p, int sms, cudaStream_t stream) {
-  constexpr int kSmem = sizeof(AdapterShared<RANK>);
-  cudaError_t e = cudaFuncSetAttribute(adapter_kernel<RANK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  constexpr int kUpSmem = sizeof(UpShared<RANK>);
+  cudaError_t e = cudaFuncSetAttribute(adapter_up_kernel<RANK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUpSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kGroupCtas);
@@ -447,19 +521,18 @@ cudaError_t launch_adapters(const AdapterParams& p, int sms, cudaStream_t stream
   cfg.stream = stream;
   e = cudaLaunchKernelEx(&cfg, adapter_group_kernel, p);
   if (e != cudaSuccess) return e;
-  // a tile holds rows of one adapter: at most one tile more than full ones per group
-  const int64_t tiles = (int64_t)p.R / kAdRows + (p.S + 1 < p.R ? p.S + 1 : p.R);
-  const int64_t most = sms * (RANK <= 32 ? 2 : 1) / kAdCtas;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * kAdCtas));
-  cfg.blockDim = dim3(kAdThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, adapter_kernel<RANK>, p);
+  // A tile holds rows of one group: at most one partial tile for each. Blocks
+  // beyond what fits at once would only queue, so each takes several tiles.
+  const int64_t down = p.R / kDownRows + (p.S < p.R ? p.S : p.R);
+  const int64_t up = (p.R / kUpRows + (p.S + 1 < p.R ? p.S + 1 : p.R)) * (((int64_t)p.N + 31) / 32);
+  const int64_t down_most = (int64_t)sms * 4, up_most = (int64_t)sms * (RANK <= 32 ? 2 : 1);
+  e = launch_after(adapter_down_kernel<RANK>, (int)(down < down_most ? down : down_most), kDownWarps * 32, 0, p, stream);
+  if (e != cudaSuccess) return e;
+  return launch_after(adapter_up_kernel<RANK>, (int)(up < up_most ? up : up_most), kUpThreads, kUpSmem, p, stream);
 }
+
+// Bytes of the groups' starts and the order, up to a 16-byte boundary.
+int64_t adapter_table_bytes(int64_t rows, int32_t slots) { return (rows + slots + 2 + 3) / 4 * 16; }
 
 int sm_count() {
   int dev = 0, n = 0;
@@ -499,8 +572,9 @@ AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t
   return e == cudaSuccess ? AFD_OK : AFD_ERR_CUDA;
 }
 
-AFD_API int64_t afd_adapter_workspace_bytes(int64_t num_rows, int32_t num_slots) {
-  return num_rows < 0 || num_slots < 1 ? -1 : (num_rows + num_slots + 2) * (int64_t)sizeof(int32_t);
+AFD_API int64_t afd_adapter_workspace_bytes(int64_t num_rows, int32_t num_slots, int32_t rank) {
+  if (num_rows < 0 || num_slots < 1 || rank < 1) return -1;
+  return adapter_table_bytes(num_rows, num_slots) + 2 * num_rows * rank * (int64_t)sizeof(uint16_t);
 }
 
 AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const void* x, int64_t x_stride,
@@ -515,11 +589,11 @@ AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const 
   if (row_src ? (!ends || num_groups < 1 || top_k < 1) : num_tokens < num_rows) return AFD_ERR_ARG;
   if (rank != 8 && rank != 16 && rank != 32 && rank != 64) return AFD_ERR_UNSUPPORTED;
   if (in_features % 16 || out_features % 8 || base_stride % 8 || out_stride % 8 || x_stride % 8 ||
-      num_rows > INT32_MAX - kAdRows || num_slots > kMaxSlots)
+      num_rows > INT32_MAX - 64 || num_slots > kMaxSlots)
     return AFD_ERR_UNSUPPORTED;
   if (num_rows == 0) return AFD_OK;
   if (!base || !x || !down || !up || !token_slots || !scales || !out || !workspace) return AFD_ERR_ARG;
-  if (workspace_bytes < afd_adapter_workspace_bytes(num_rows, num_slots)) return AFD_ERR_ARG;
+  if (workspace_bytes < afd_adapter_workspace_bytes(num_rows, num_slots, rank)) return AFD_ERR_ARG;
   AdapterParams p = {};
   p.base_stride = base_stride, p.x_stride = x_stride, p.out_stride = out_stride;
   p.G = num_groups, p.top_k = top_k, p.R = (int32_t)num_rows, p.tokens = num_tokens, p.S = num_slots, p.rank = rank;
@@ -533,7 +607,9 @@ AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const 
       (row_src && (!afd::device_view(row_src, &p.row_src) || !afd::device_view(ends, &p.ends))))
     return AFD_ERR_ARG;
   p.order = p.first + num_slots + 2;
-  if (!afd::aligned_to(p.first, 4) || !afd::aligned_to(p.token_slots, 4) || !afd::aligned_to(p.scales, 4) || !afd::aligned_to(p.row_src, 4) ||
+  p.t_hi = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(p.first) + adapter_table_bytes(num_rows, num_slots));
+  p.t_lo = p.t_hi + num_rows * rank;
+  if (!afd::aligned_to(p.first, 16) || !afd::aligned_to(p.token_slots, 4) || !afd::aligned_to(p.scales, 4) || !afd::aligned_to(p.row_src, 4) ||
       !afd::aligned_to(p.ends, 4))
     return AFD_ERR_ARG;
   if (!afd::aligned_to(p.base, 16) || !afd::aligned_to(p.x, 16) || !afd::aligned_to(p.down, 16) ||

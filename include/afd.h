@@ -504,7 +504,7 @@ AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t
  *   row_src      device int32 [num_rows] with ends, or NULL (then num_tokens
  *                >= num_rows, and ends may be NULL)
  *   workspace    device, at least afd_adapter_workspace_bytes(num_rows,
- *                num_slots) bytes, 4-byte aligned; its contents need not be set
+ *                num_slots, rank) bytes, 16-byte aligned; its contents need not be set
  *                and mean nothing afterwards. Calls that may run at the same
  *                time (other streams, other captured graphs) need one each.
  * Limits: num_slots <= 1024; rank 8, 16, 32 or 64; in_features a multiple of
@@ -521,7 +521,7 @@ AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const 
                                    void* workspace, int64_t workspace_bytes, afd_stream stream);
 
 /* Bytes of workspace for afd_adapter_add with these sizes (-1 for sizes it refuses). */
-AFD_API int64_t afd_adapter_workspace_bytes(int64_t num_rows, int32_t num_slots);
+AFD_API int64_t afd_adapter_workspace_bytes(int64_t num_rows, int32_t num_slots, int32_t rank);
 
 /* Library version, (major << 16) | minor. */
 AFD_API int32_t afd_version(void);

@@ -77,7 +77,7 @@ def test_gated_rows(lib, over, status):
 
 def _adapter(lib, **over):
     a = dict(base=P, base_stride=64, x=P, x_stride=128, down=P, up=P, slots=P, scales=P, row_src=None, ends=None, G=0,
-             top_k=1, R=8, tokens=8, S=2, rank=16, K=128, N=64, out=P, out_stride=64, ws=P, ws_bytes=48)
+             top_k=1, R=8, tokens=8, S=2, rank=16, K=128, N=64, out=P, out_stride=64, ws=P, ws_bytes=48 + 2 * 8 * 16 * 2)
     a.update(over)
     return lib.afd_adapter_add(*a.values(), None)
 
@@ -91,7 +91,7 @@ def _adapter(lib, **over):
     (dict(scales=None), afd.ERR_ARG), (dict(out=None), afd.ERR_ARG), (dict(rank=24), afd.ERR_UNSUPPORTED),
     (dict(rank=128), afd.ERR_UNSUPPORTED), (dict(K=120), afd.ERR_UNSUPPORTED),
     (dict(N=60, base_stride=60, out_stride=60), afd.ERR_UNSUPPORTED), (dict(base_stride=68), afd.ERR_UNSUPPORTED),
-    (dict(S=1025, ws_bytes=1 << 20), afd.ERR_UNSUPPORTED), (dict(ws=None), afd.ERR_ARG), (dict(ws_bytes=47), afd.ERR_ARG),
+    (dict(S=1025, ws_bytes=1 << 20), afd.ERR_UNSUPPORTED), (dict(ws=None), afd.ERR_ARG), (dict(ws_bytes=48 + 511), afd.ERR_ARG),
     (dict(R=0, base=None, x=None, out=None, ws=None, ws_bytes=0), afd.OK)])
 def test_adapters(lib, over, status):
     assert _adapter(lib, **over) == status
