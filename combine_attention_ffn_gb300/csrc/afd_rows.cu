@@ -47,13 +47,25 @@ __global__ void __launch_bounds__(256) gated_rows_kernel(const GatedParams p) {
     const uint16_t* up = gate + p.N;
     uint16_t* out = p.out + r * p.out_stride;
     if (VEC) {
-      for (int c = lane * 8; c < p.N; c += 256) {
-        float g[8], u[8];
-        afd::bf16x8_to_float(*reinterpret_cast<const uint4*>(gate + c), g);
-        afd::bf16x8_to_float(*reinterpret_cast<const uint4*>(up + c), u);
+      // four column groups' loads in flight at a time
+      for (int c0 = lane * 8; c0 < p.N; c0 += 4 * 256) {
+        uint4 gv[4], uv[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = afd::silu_mul(g[i], u[i]);
-        *reinterpret_cast<uint4*>(out + c) = afd::float_to_bf16x8(g);
+        for (int i = 0; i < 4; ++i)
+          if (c0 + 256 * i < p.N) {
+            gv[i] = afd::ld_once(reinterpret_cast<const uint4*>(gate + c0 + 256 * i));
+            uv[i] = afd::ld_once(reinterpret_cast<const uint4*>(up + c0 + 256 * i));
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c0 + 256 * i < p.N) {
+            float g[8], u[8];
+            afd::bf16x8_to_float(gv[i], g);
+            afd::bf16x8_to_float(uv[i], u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = afd::silu_mul(g[j], u[j]);
+            *reinterpret_cast<uint4*>(out + c0 + 256 * i) = afd::float_to_bf16x8(g);
+          }
       }
     } else {
       for (int c = lane; c < p.N; c += 32)
@@ -124,10 +136,11 @@ __device__ __forceinline__ int row_group(const AdapterParams& p, int r) {
   return a >= 0 && a < p.S ? a : p.S;
 }
 
-__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
-  uint32_t a = (uint32_t)__cvta_generic_to_shared(p);
-  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(rank));
-  return a;
+// The generic address of this shared address in another CTA of the cluster.
+__device__ __forceinline__ const int* remote(const int* p, uint32_t rank) {
+  uint64_t a;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(p), "r"(rank));
+  return reinterpret_cast<const int*>(a);
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -173,8 +186,7 @@ __global__ void __cluster_dims__(kGroupCtas, 1, 1) __launch_bounds__(kGroupThrea
     if (g >= groups) break;
 #pragma unroll
     for (uint32_t c = 0; c < kGroupCtas; ++c) {
-      int v;
-      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote(&count[g], c)) : "memory");
+      const int v = *remote(&count[g], c);
       total[i] += v;
       if (c < cta) before[i] += v;
     }

@@ -167,13 +167,4 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_load8(uint32_t addr, float (&v)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-      : "r"(addr)
-      : "memory");
-}
-
 }  // namespace afd
