@@ -119,6 +119,7 @@ constexpr int kGroupThreads = 1024;
 constexpr int kGroupKeep = 4;      // rows of a thread whose group it remembers
 constexpr int kDownRows = 16;      // rows of a block
 constexpr int kDownWarps = 8;      // ... whose warps share K
+constexpr int kDownStages = 3;     // K chunks of a warp in flight
 constexpr int kUpRows = 64;        // rows of a tile: 16 for each of four warps
 constexpr int kUpThreads = 256;
 constexpr int kUpStages = 4;       // column groups whose operands are in flight
@@ -232,12 +233,19 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 // Where the groups start, in rows and in tiles of ROWS rows (of the first
 // `groups` groups).
 struct GroupTable {
-  int first[kMaxSlots + 2];
-  int first_tile[kMaxSlots + 2];
+  int* first;
+  int* first_tile;
 };
 
+// In dynamic shared memory, behind what a block needs besides.
+constexpr size_t table_bytes(int slots) { return 2 * sizeof(int) * (slots + 2); }
+__device__ __forceinline__ GroupTable table_at(void* p, int slots) {
+  int* first = static_cast<int*>(p);
+  return {first, first + slots + 2};
+}
+
 template <int ROWS>
-__device__ __forceinline__ int load_groups(const AdapterParams& p, GroupTable& sh, int groups) {
+__device__ __forceinline__ int load_groups(const AdapterParams& p, const GroupTable& sh, int groups) {
   const int lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i <= groups; i += blockDim.x) sh.first[i] = p.first[i];
   __syncthreads();
@@ -266,59 +274,92 @@ __device__ __forceinline__ int tile_group(const GroupTable& sh, int groups, int 
   return a;
 }
 
+// Asynchronous copies of BYTES (4, 8 or 16) into shared memory; nothing is
+// read where `in` is false, and zeros are written.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool in) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  const int n = in ? BYTES : 0;
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+
+// Operands of one 32-wide K chunk on their way: every thread copies exactly
+// what it uses itself, so no other thread has to be waited for.
 template <int RANK>
-struct DownShared {
-  static constexpr int kPad = RANK + 4;
-  alignas(16) float part[kDownWarps][kDownRows][kPad];
-  GroupTable groups;
+struct DownStage {
+  uint4 x[2][32];            // rows g / g + 8
+  uint4 down[RANK / 8][32];  // rank rows 8 n + g
 };
 
 template <int RANK>
-__global__ void __launch_bounds__(kDownWarps * 32, 4) adapter_down_kernel(const AdapterParams p) {
-  __shared__ DownShared<RANK> sh;
+struct DownShared {
+  static constexpr int kPad = RANK + 4;
+  union {
+    DownStage<RANK> stage[kDownWarps][kDownStages];
+    float part[kDownWarps][kDownRows][kPad];  // once the products are done
+  };
+};
+
+template <int RANK>
+__global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const AdapterParams p) {
+  extern __shared__ __align__(16) uint8_t ad_smem[];
+  DownShared<RANK>& sh = *reinterpret_cast<DownShared<RANK>*>(ad_smem);
   constexpr int NT = RANK / 8;             // 8-column tiles of the product
-  constexpr int U = RANK <= 32 ? 4 : 2;    // K chunks of 32 loaded together
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tig = lane & 3;
   const int chunks = (p.K + 31) >> 5;
+  DownStage<RANK>* stage = sh.stage[warp];
+  const GroupTable groups = table_at(&sh + 1, p.S);
   afd::pdl_launch_dependents();
   afd::pdl_wait();
-  const int tiles = load_groups<kDownRows>(p, sh.groups, p.S);
+  const int tiles = load_groups<kDownRows>(p, groups, p.S);
   for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int a = tile_group(sh.groups, p.S, t);
-    const int at = sh.groups.first[a] + (t - sh.groups.first_tile[a]) * kDownRows, end = sh.groups.first[a + 1];
+    const int a = tile_group(groups, p.S, t);
+    const int at = groups.first[a] + (t - groups.first_tile[a]) * kDownRows, end = groups.first[a + 1];
     const uint16_t* x[2];  // this thread's rows: g / g + 8
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int i = at + 8 * h + g;
       x[h] = i < end ? p.x + p.order[i] * p.x_stride : nullptr;
     }
+    const uint16_t* down = p.down + ((int64_t)a * RANK + g) * p.K;
+    auto fetch = [&](int i) {  // this warp's i-th chunk
+      const int c = warp + i * kDownWarps;
+      if (c < chunks) {
+        DownStage<RANK>& st = stage[i % kDownStages];
+        const int k = c * 32 + tig * 8;
+        const bool in = k < p.K;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) copy_async<16>(&st.down[n][lane], in ? down + (int64_t)n * 8 * p.K + k : p.down, in);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) copy_async<16>(&st.x[h][lane], in && x[h] ? x[h] + k : p.x, in && x[h]);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kDownStages - 1; ++i) fetch(i);
     float acc[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    const uint16_t* down = p.down + ((int64_t)a * RANK + g) * p.K;
-    for (int c0 = warp; c0 < chunks; c0 += U * kDownWarps) {
-      uint4 xv[U][2];
+    for (int i = 0; warp + i * kDownWarps < chunks; ++i) {
+      fetch(i + kDownStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDownStages - 1) : "memory");
+      const DownStage<RANK>& st = stage[i % kDownStages];
+      const uint4 x0 = st.x[0][lane], x1 = st.x[1][lane];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = (c0 + u * kDownWarps) * 32 + tig * 8;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          xv[u][h] = k < p.K && x[h] ? afd::ld_once(reinterpret_cast<const uint4*>(x[h] + k)) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = (c0 + u * kDownWarps) * 32 + tig * 8;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 b = k < p.K ? __ldg(reinterpret_cast<const uint4*>(down + (int64_t)n * 8 * p.K + k)) : make_uint4(0, 0, 0, 0);
-          mma_16816(acc[n], xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y, b.x, b.y);
-          mma_16816(acc[n], xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w, b.z, b.w);
-        }
+      for (int n = 0; n < NT; ++n) {
+        const uint4 b = st.down[n][lane];
+        mma_16816(acc[n], x0.x, x1.x, x0.y, x1.y, b.x, b.y);
+        mma_16816(acc[n], x0.z, x1.z, x0.w, x1.w, b.z, b.w);
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -362,18 +403,6 @@ __device__ __forceinline__ void load_rank(const uint16_t* q, bool in, uint32_t (
   }
 }
 
-// Asynchronous copies of BYTES (4, 8 or 16) into shared memory; nothing is
-// read where `in` is false, and zeros are written.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* dst, const void* src, bool in) {
-  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-  const int n = in ? BYTES : 0;
-  if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES), "r"(n) : "memory");
-}
-
 // Operands of one 32-column group on their way: every thread copies exactly
 // what it uses itself, so no other thread has to be waited for.
 template <int RANK>
@@ -387,7 +416,6 @@ struct UpStage {
 template <int RANK>
 struct UpShared {
   alignas(16) UpStage<RANK> stage[kUpThreads / 32][kUpStages];
-  GroupTable groups;
 };
 
 template <int RANK>
@@ -400,8 +428,9 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
   const int g = lane >> 2, tig = lane & 3;
   const int col_groups = (p.N + 31) >> 5, slots = gridDim.x * (kUpThreads / 32);
   UpStage<RANK>* stage = sh.stage[warp];
+  const GroupTable groups = table_at(&sh + 1, p.S);
   afd::pdl_wait();
-  const int tiles = load_groups<kUpRows>(p, sh.groups, p.S + 1);
+  const int tiles = load_groups<kUpRows>(p, groups, p.S + 1);
   // The columns are split so far that every warp has something to do.
   const int want = max(1, min(col_groups, slots / max(4 * tiles, 1)));
   const int each = (col_groups + want - 1) / want, parts = (col_groups + each - 1) / each;
@@ -409,8 +438,8 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
   for (int64_t item = (int64_t)blockIdx.x * (kUpThreads / 32) + warp; item < items; item += slots) {
     const int quarter = (int)(item & 3);
     const int t = (int)((item >> 2) / parts), part = (int)((item >> 2) % parts);
-    const int a = tile_group(sh.groups, p.S + 1, t);
-    const int at = sh.groups.first[a] + (t - sh.groups.first_tile[a]) * kUpRows + 16 * quarter, end = sh.groups.first[a + 1];
+    const int a = tile_group(groups, p.S + 1, t);
+    const int at = groups.first[a] + (t - groups.first_tile[a]) * kUpRows + 16 * quarter, end = groups.first[a + 1];
     if (at >= end) continue;
     const int g0 = part * each, g1 = min(g0 + each, col_groups);
     const bool adapt = a < p.S;  // the last group has no adapter: its rows are copied
@@ -524,9 +553,17 @@ cudaError_t launch_after(K kernel, int grid, int block, size_t smem, const Adapt
 
 template <int RANK>
 cudaError_t launch_adapters(const AdapterParams& p, int sms, cudaStream_t stream) {
-  constexpr int kUpSmem = sizeof(UpShared<RANK>);
-  cudaError_t e = cudaFuncSetAttribute(adapter_up_kernel<RANK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUpSmem);
+  // the attribute is set to the most any call asks for: calls on other threads
+  // may set it at the same time
+  constexpr int kDownBase = sizeof(DownShared<RANK>), kUpBase = sizeof(UpShared<RANK>);
+  cudaError_t e = cudaFuncSetAttribute(adapter_up_kernel<RANK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kUpBase + (int)table_bytes(kMaxSlots));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(adapter_down_kernel<RANK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kDownBase + (int)table_bytes(kMaxSlots));
   if (e != cudaSuccess) return e;
+  const int down_smem = kDownBase + (int)table_bytes(p.S), up_smem = kUpBase + (int)table_bytes(p.S);
+  const int down_fit = 227 * 1024 / (down_smem + 1024), up_fit = 227 * 1024 / (up_smem + 1024);  // blocks of an SM
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kGroupCtas);
   cfg.blockDim = dim3(kGroupThreads);
@@ -537,10 +574,10 @@ cudaError_t launch_adapters(const AdapterParams& p, int sms, cudaStream_t stream
   // beyond what fits at once would only queue, so each takes several tiles.
   const int64_t down = p.R / kDownRows + (p.S < p.R ? p.S : p.R);
   const int64_t up = (p.R / kUpRows + (p.S + 1 < p.R ? p.S + 1 : p.R)) * (((int64_t)p.N + 31) / 32);
-  const int64_t down_most = (int64_t)sms * 4, up_most = (int64_t)sms * (RANK <= 32 ? 2 : 1);
-  e = launch_after(adapter_down_kernel<RANK>, (int)(down < down_most ? down : down_most), kDownWarps * 32, 0, p, stream);
+  const int64_t down_most = (int64_t)sms * (down_fit < 4 ? down_fit : 4), up_most = (int64_t)sms * (up_fit < 2 ? up_fit : 2);
+  e = launch_after(adapter_down_kernel<RANK>, (int)(down < down_most ? down : down_most), kDownWarps * 32, down_smem, p, stream);
   if (e != cudaSuccess) return e;
-  return launch_after(adapter_up_kernel<RANK>, (int)(up < up_most ? up : up_most), kUpThreads, kUpSmem, p, stream);
+  return launch_after(adapter_up_kernel<RANK>, (int)(up < up_most ? up : up_most), kUpThreads, up_smem, p, stream);
 }
 
 // Bytes of the groups' starts and the order, up to a 16-byte boundary.
