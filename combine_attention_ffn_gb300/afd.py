@@ -500,12 +500,14 @@ def route_topk(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
     shape = (T, top_k)
     if ids is None:
         ids = torch.empty(shape, dtype=torch.int64, device=logits.device)
-    ids_ptr = _want(ids, "ids", torch.int64, shape)
+    else:
+        _want(ids, "ids", torch.int64, shape)
     if weights is None:
         weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
-    weights_ptr = _want(weights, "weights", torch.float32, shape)
+    else:
+        _want(weights, "weights", torch.float32, shape)
     _call("afd_route_topk", ids, stream, logits.data_ptr(), FP32 if logits.dtype is torch.float32 else BF16, stride,
-          bias_ptr, live_ptr, T, E, top_k, SCORINGS[scoring], bool(renormalize), scale, ids_ptr, weights_ptr)
+          bias_ptr, live_ptr, T, E, top_k, SCORINGS[scoring], bool(renormalize), scale, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -608,8 +610,8 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
         out, out_stride = base, base_stride
     else:
         out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
-    size = (_lib or load_library()).afd_adapter_workspace_bytes(R, S, rank)
-    workspace = torch.empty(max(size, 0), dtype=torch.uint8, device=x.device)
+    size = (R + S + 5) // 4 * 16 + 4 * R * rank  # afd_adapter_workspace_bytes
+    workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
     if stream is not None:  # the allocator must not hand it on before that stream is done with it
         workspace.record_stream(stream)
     _call("afd_adapter_add", workspace, stream, base.data_ptr(), base_stride, x.data_ptr(), x_stride, down_ptr, up_ptr,

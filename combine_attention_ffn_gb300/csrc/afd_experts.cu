@@ -322,6 +322,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) afd::tmem_alloc_pair(afd::smem_u32(&sh.tmem), kColumns);
+  // Up to here nothing of another kernel's has been touched.
+  afd::pdl_wait();
+  afd::pdl_launch_dependents();
   // every group's end, then the prefix sums of the groups' tiles
   for (int g = threadIdx.x; g < p.G; g += kThreads) sh.end[g] = afd::group_end(p.ends[g], p.R);
   __syncthreads();
@@ -630,7 +633,7 @@ bool encode(EncodeTiled f, CUtensorMap* map, bool fp8, uint32_t rank, const void
 }
 
 template <bool FP8, bool GATED>
-cudaError_t launch_grouped(const Maps& maps, const ExpertParams& p, int pairs, cudaStream_t stream) {
+cudaError_t launch_grouped(const Maps& maps, const ExpertParams& p, int device, int pairs, cudaStream_t stream) {
   if (FP8) {
     // the registers that the hand-over gives out must be there at launch
     static const bool enough = [] {
@@ -640,15 +643,10 @@ cudaError_t launch_grouped(const Maps& maps, const ExpertParams& p, int pairs, c
     }();
     if (!enough) return cudaErrorInvalidKernelImage;
   }
-  const cudaError_t e = cudaFuncSetAttribute(grouped_linear_kernel<FP8, GATED>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t e = afd::allow_shared(grouped_linear_kernel<FP8, GATED>, (int)kSmem, device, set);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * pairs);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, grouped_linear_kernel<FP8, GATED>, maps, p);
+  return afd::launch_dependent(grouped_linear_kernel<FP8, GATED>, 2 * pairs, kThreads, kSmem, stream, maps, p);
 }
 
 // Device memory of the current device (bulk copies read it).
@@ -729,7 +727,7 @@ extern "C" AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride
   const int64_t most = row_tiles_max * p.m_tiles;
   const int pairs = (int)(most < sms / 2 ? most : sms / 2);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = fp8 ? (gated ? launch_grouped<true, true>(maps, p, pairs, s) : launch_grouped<true, false>(maps, p, pairs, s))
-                            : (gated ? launch_grouped<false, true>(maps, p, pairs, s) : launch_grouped<false, false>(maps, p, pairs, s));
+  const cudaError_t e = fp8 ? (gated ? launch_grouped<true, true>(maps, p, dev, pairs, s) : launch_grouped<true, false>(maps, p, dev, pairs, s))
+                            : (gated ? launch_grouped<false, true>(maps, p, dev, pairs, s) : launch_grouped<false, false>(maps, p, dev, pairs, s));
   return e == cudaSuccess ? AFD_OK : AFD_ERR_CUDA;
 }

@@ -1,10 +1,24 @@
-// Host checks of caller buffers, shared by the calls that take no context.
+// Host helpers of the calls that take no context: checks of caller buffers,
+// launches.
 #pragma once
 
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace afd {
+
+// Sets a kernel's dynamic shared memory limit once per device (`done`: one
+// bit for each, static to the caller's kernel).
+template <typename K>
+inline cudaError_t allow_shared(K kernel, int bytes, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // The address a kernel on the current device uses for a caller buffer: the
 // buffer itself in that device's memory or in managed memory, the mapped
@@ -30,7 +44,26 @@ inline bool device_view(T* p, T** out) {
   return false;
 }
 
-// Whether [p, p + bytes) starts on an `align`-byte boundary.
+// Launches a kernel as a programmatic dependent of the work before it on the
+// stream: its blocks may start while that work still runs, and the kernel
+// waits (pdl_wait) before it touches memory.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_dependent(void (*kernel)(Params...), int64_t grid, int block, size_t smem, cudaStream_t stream,
+                                    Args&&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+}
+
+// Whether p is on an `align`-byte boundary.
 inline bool aligned_to(const void* p, uintptr_t align) { return (reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0; }
 
 }  // namespace afd

@@ -143,6 +143,8 @@ __device__ __noinline__ void order_exact(const float (&l)[PER], const RouterPara
 
 template <int PER, bool BF16>
 __global__ void __launch_bounds__(kRouterWarps * 32) route_topk_kernel(const RouterParams p) {
+  afd::pdl_wait();
+  afd::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kRouterWarps + (threadIdx.x >> 5);
   if (t >= p.T) return;
@@ -258,12 +260,9 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_topk_kernel(const Rou
 
 template <int PER>
 cudaError_t launch_router(const RouterParams& p, bool bf16, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.T + kRouterWarps - 1) / kRouterWarps);
-  cfg.blockDim = dim3(kRouterWarps * 32);
-  cfg.stream = stream;
-  return bf16 ? cudaLaunchKernelEx(&cfg, route_topk_kernel<PER, true>, p)
-              : cudaLaunchKernelEx(&cfg, route_topk_kernel<PER, false>, p);
+  const int grid = (p.T + kRouterWarps - 1) / kRouterWarps;
+  return bf16 ? afd::launch_dependent(route_topk_kernel<PER, true>, grid, kRouterWarps * 32, 0, stream, p)
+              : afd::launch_dependent(route_topk_kernel<PER, false>, grid, kRouterWarps * 32, 0, stream, p);
 }
 
 }  // namespace

@@ -30,6 +30,8 @@ __device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_f
 template <bool VEC>
 __global__ void __launch_bounds__(256) gated_rows_kernel(const GatedParams p) {
   __shared__ int sh_end[afd::kMaxExperts];
+  afd::pdl_wait();
+  afd::pdl_launch_dependents();
   for (int g = threadIdx.x; g < p.G; g += blockDim.x) sh_end[g] = afd::group_end(p.ends[g], p.R);
   __syncthreads();
   const int lane = threadIdx.x & 31;
@@ -154,6 +156,7 @@ __device__ __forceinline__ void cluster_sync() {
 __global__ void __cluster_dims__(kGroupCtas, 1, 1) __launch_bounds__(kGroupThreads) adapter_group_kernel(const AdapterParams p) {
   __shared__ int count[kMaxSlots + 1], cursor[kMaxSlots + 1];
   __shared__ int warp_total[kGroupThreads / 32];
+  afd::pdl_wait();
   afd::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t cta = blockIdx.x;
@@ -313,8 +316,8 @@ __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const Ada
   const int chunks = (p.K + 31) >> 5;
   DownStage<RANK>* stage = sh.stage[warp];
   const GroupTable groups = table_at(&sh + 1, p.S);
-  afd::pdl_launch_dependents();
   afd::pdl_wait();
+  afd::pdl_launch_dependents();
   const int tiles = load_groups<kDownRows>(p, groups, p.S);
   for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int a = tile_group(groups, p.S, t);
@@ -430,6 +433,7 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
   UpStage<RANK>* stage = sh.stage[warp];
   const GroupTable groups = table_at(&sh + 1, p.S);
   afd::pdl_wait();
+  afd::pdl_launch_dependents();
   const int tiles = load_groups<kUpRows>(p, groups, p.S + 1);
   // The columns are split so far that every warp has something to do.
   const int want = max(1, min(col_groups, slots / max(4 * tiles, 1)));
@@ -536,58 +540,34 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
   }
 }
 
-template <typename K>
-cudaError_t launch_after(K kernel, int grid, int block, size_t smem, const AdapterParams& p, cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 template <int RANK>
-cudaError_t launch_adapters(const AdapterParams& p, int sms, cudaStream_t stream) {
-  // the attribute is set to the most any call asks for: calls on other threads
-  // may set it at the same time
+cudaError_t launch_adapters(const AdapterParams& p, int device, int sms, cudaStream_t stream) {
   constexpr int kDownBase = sizeof(DownShared<RANK>), kUpBase = sizeof(UpShared<RANK>);
-  cudaError_t e = cudaFuncSetAttribute(adapter_up_kernel<RANK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kUpBase + (int)table_bytes(kMaxSlots));
+  static std::atomic<uint64_t> down_set{0}, up_set{0};
+  cudaError_t e = afd::allow_shared(adapter_up_kernel<RANK>, kUpBase + (int)table_bytes(kMaxSlots), device, up_set);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(adapter_down_kernel<RANK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kDownBase + (int)table_bytes(kMaxSlots));
+    e = afd::allow_shared(adapter_down_kernel<RANK>, kDownBase + (int)table_bytes(kMaxSlots), device, down_set);
   if (e != cudaSuccess) return e;
   const int down_smem = kDownBase + (int)table_bytes(p.S), up_smem = kUpBase + (int)table_bytes(p.S);
   const int down_fit = 227 * 1024 / (down_smem + 1024), up_fit = 227 * 1024 / (up_smem + 1024);  // blocks of an SM
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kGroupCtas);
-  cfg.blockDim = dim3(kGroupThreads);
-  cfg.stream = stream;
-  e = cudaLaunchKernelEx(&cfg, adapter_group_kernel, p);
+  e = afd::launch_dependent(adapter_group_kernel, kGroupCtas, kGroupThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
   // A tile holds rows of one group: at most one partial tile for each. Blocks
   // beyond what fits at once would only queue, so each takes several tiles.
   const int64_t down = p.R / kDownRows + (p.S < p.R ? p.S : p.R);
   const int64_t up = (p.R / kUpRows + (p.S + 1 < p.R ? p.S + 1 : p.R)) * (((int64_t)p.N + 31) / 32);
   const int64_t down_most = (int64_t)sms * (down_fit < 4 ? down_fit : 4), up_most = (int64_t)sms * (up_fit < 2 ? up_fit : 2);
-  e = launch_after(adapter_down_kernel<RANK>, (int)(down < down_most ? down : down_most), kDownWarps * 32, down_smem, p, stream);
+  e = afd::launch_dependent(adapter_down_kernel<RANK>, down < down_most ? down : down_most, kDownWarps * 32, down_smem, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_after(adapter_up_kernel<RANK>, (int)(up < up_most ? up : up_most), kUpThreads, up_smem, p, stream);
+  return afd::launch_dependent(adapter_up_kernel<RANK>, up < up_most ? up : up_most, kUpThreads, up_smem, stream, p);
 }
 
 // Bytes of the groups' starts and the order, up to a 16-byte boundary.
 int64_t adapter_table_bytes(int64_t rows, int32_t slots) { return (rows + slots + 2 + 3) / 4 * 16; }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return n;
+int sm_count(int device) {
+  int n = 0;
+  return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) == cudaSuccess ? n : 0;
 }
 
 }  // namespace
@@ -607,17 +587,16 @@ AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t
       !afd::device_view(static_cast<uint16_t*>(out), &p.out))
     return AFD_ERR_ARG;
   if (!afd::aligned_to(p.h, 2) || !afd::aligned_to(p.out, 2) || !afd::aligned_to(p.ends, 4)) return AFD_ERR_ARG;
-  const int sms = sm_count();
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return AFD_ERR_CUDA;
+  const int sms = sm_count(dev);
   if (sms < 1) return AFD_ERR_CUDA;
   const bool vec = features % 8 == 0 && h_stride % 8 == 0 && out_stride % 8 == 0 && afd::aligned_to(p.h, 16) &&
                    afd::aligned_to(p.out, 16);
-  cudaLaunchConfig_t cfg = {};
-  const int64_t blocks = (num_rows + 7) / 8;
-  cfg.gridDim = dim3((unsigned)(blocks < sms * 8 ? blocks : sms * 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = vec ? cudaLaunchKernelEx(&cfg, gated_rows_kernel<true>, p)
-                            : cudaLaunchKernelEx(&cfg, gated_rows_kernel<false>, p);
+  const int64_t blocks = (num_rows + 7) / 8, grid = blocks < sms * 8 ? blocks : sms * 8;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = vec ? afd::launch_dependent(gated_rows_kernel<true>, grid, 256, 0, st, p)
+                            : afd::launch_dependent(gated_rows_kernel<false>, grid, 256, 0, st, p);
   return e == cudaSuccess ? AFD_OK : AFD_ERR_CUDA;
 }
 
@@ -664,13 +643,15 @@ AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const 
   if (!afd::aligned_to(p.base, 16) || !afd::aligned_to(p.x, 16) || !afd::aligned_to(p.down, 16) ||
       !afd::aligned_to(p.up, 16) || !afd::aligned_to(p.out, 16))
     return AFD_ERR_UNSUPPORTED;
-  const int sms = sm_count();
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return AFD_ERR_CUDA;
+  const int sms = sm_count(dev);
   if (sms < 1) return AFD_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = rank == 8    ? launch_adapters<8>(p, sms, st)
-                        : rank == 16 ? launch_adapters<16>(p, sms, st)
-                        : rank == 32 ? launch_adapters<32>(p, sms, st)
-                                     : launch_adapters<64>(p, sms, st);
+  const cudaError_t e = rank == 8    ? launch_adapters<8>(p, dev, sms, st)
+                        : rank == 16 ? launch_adapters<16>(p, dev, sms, st)
+                        : rank == 32 ? launch_adapters<32>(p, dev, sms, st)
+                                     : launch_adapters<64>(p, dev, sms, st);
   return e == cudaSuccess ? AFD_OK : AFD_ERR_CUDA;
 }
 

@@ -97,6 +97,12 @@ def test_adapters(lib, over, status):
     assert _adapter(lib, **over) == status
 
 
+def test_adapter_workspace(lib):
+    for R, S, rank in ((0, 1, 8), (1, 1, 8), (2, 1, 16), (7, 3, 32), (100_000, 1024, 64), (1 << 28, 5, 64)):
+        assert lib.afd_adapter_workspace_bytes(R, S, rank) == (R + S + 2 + 3) // 4 * 16 + 4 * R * rank
+    assert lib.afd_adapter_workspace_bytes(-1, 1, 8) == lib.afd_adapter_workspace_bytes(1, 0, 8) == -1
+
+
 def test_binding_refuses_wrong_types_and_shapes(lib):
     bf = torch.bfloat16
     z = lambda *s, dtype=bf: torch.zeros(*s, dtype=dtype)
