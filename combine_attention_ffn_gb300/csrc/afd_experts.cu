@@ -51,9 +51,9 @@ constexpr int kPairRows = 256;    // weight rows of a tile (two CTAs)
 constexpr int kCtaRows = 128;
 constexpr int kTileRows = 256;    // received rows of a tile, at most
 constexpr int kBlockBytes = 128;  // bytes of K per stage and row
-constexpr int kStages = 6;
-constexpr int kHalfBytes = kCtaRows * kBlockBytes;  // one operand of a stage
-constexpr int kStageBytes = 2 * kHalfBytes;
+constexpr int kHalfBytes = kCtaRows * kBlockBytes;  // a stage's weight rows
+constexpr int kRingBytes = 6 * 2 * kHalfBytes;      // six stages of the widest tiles, or more of narrower ones
+constexpr int kMaxStages = 10;
 constexpr int kDrainWarps = 16;
 constexpr int kDrainParts = kDrainWarps / 4;  // warps that share 32 lanes of TMEM, 16 columns each in turn
 constexpr int kThreads = 128 + 32 * kDrainWarps;
@@ -99,7 +99,7 @@ struct alignas(16) Tile {
 };
 
 struct Shared {
-  alignas(8) uint64_t full[kStages], empty[kStages];
+  alignas(8) uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t drain_full[kMaxBufs];  // an accumulator's products are complete
   uint64_t drained[kMaxBufs];     // this CTA's warps have read it
   uint64_t peer_drained[kMaxBufs];  // ... and the other CTA's (used in the even one)
@@ -115,7 +115,7 @@ struct Shared {
   BlockScales scale[kScaleStages];
 };
 
-constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + sizeof(Shared);
+constexpr size_t kSmem = 1024 + kRingBytes + sizeof(Shared);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
 __device__ __forceinline__ int row_tiles(int count) { return (count + kTileRows - 1) / kTileRows; }
@@ -235,6 +235,26 @@ __device__ __forceinline__ void store16(const ExpertParams& p, const Tile& tile,
   }
 }
 
+// The ring of stages. Narrow tiles leave room for more of them: with six a
+// decode step of 128 skewed tokens took 3% longer than with eight.
+struct Ring {
+  int stages, bytes;         // of a stage: weight rows, then half the widest tile's received rows
+  uint32_t count = 0;        // stages passed so far
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ explicit Ring(int widest)
+      : stages(min(kMaxStages, kRingBytes / (kHalfBytes + widest / 2 * kBlockBytes))), bytes(kHalfBytes + widest / 2 * kBlockBytes) {}
+  __device__ __forceinline__ void advance() {
+    ++count;
+    if (++slot == stages) slot = 0, phase ^= 1;
+  }
+  // Calls wait(slot, parity) for the last stages passed, oldest first.
+  template <typename F>
+  __device__ __forceinline__ void last(F wait) const {
+    for (uint32_t i = count > (uint32_t)stages ? count - stages : 0; i < count; ++i) wait(i % stages, i / stages & 1);
+  }
+};
+
 // The accumulators' turns: unit u uses buffer u & (bufs - 1).
 struct Turns {
   uint32_t tmem, full, drained;  // addresses of buffer 0
@@ -258,8 +278,8 @@ __device__ __forceinline__ bool drain_blocks(const ExpertParams& p, Shared& sh, 
     for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
   for (int kb = 0; kb < p.k_blocks; ++kb, ++unit) {
     const uint32_t s = unit % kScaleStages, b = turns.buf(unit);
-    if (!__all_sync(0xffffffffu, afd::mbar_wait(scale_full + 8 * s, (unit / kScaleStages) & 1, &sh.gave_up) &&
-                                     afd::mbar_wait(turns.full + 8 * b, turns.phase(unit), &sh.gave_up)))
+    if (!afd::mbar_wait(scale_full + 8 * s, (unit / kScaleStages) & 1, &sh.gave_up) ||
+        !afd::mbar_wait(turns.full + 8 * b, turns.phase(unit), &sh.gave_up))
       return false;
     afd::tcgen05_fence_after();
     const uint32_t acc = turns.tmem + b * turns.cols + 16 * h;
@@ -295,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_linear_kernel(const __grid_constant__ Maps maps, const ExpertParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem = (afd::smem_u32(smem_raw) + 1023) & ~1023u;
-  Shared& sh = *reinterpret_cast<Shared*>(smem_raw + (smem - afd::smem_u32(smem_raw)) + kStages * kStageBytes);
+  Shared& sh = *reinterpret_cast<Shared*>(smem_raw + (smem - afd::smem_u32(smem_raw)) + kRingBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = afd::cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -305,7 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t scale_full = afd::smem_u32(sh.scale_full), scale_empty = afd::smem_u32(sh.scale_empty);
 
   if (warp == 0 && lane == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       afd::mbar_init(full + 8 * i, 1);
       afd::mbar_init(empty + 8 * i, 1);
     }
@@ -417,7 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
     asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
     const uint32_t lead_full = afd::map_to_rank(full, 0);
-    uint32_t it = 0;
+    Ring ring(sh.widest);
     bool ok = true;
     Tile tile;
     for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
@@ -428,10 +448,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // this weight tile is read again if the expert has more row tiles
       const uint64_t w_policy = tile.rows == group_count(sh, p, tile.group) ? once : keep;
       const int w_row = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) : tile.m * kPairRows + (int)rank * kCtaRows;
-      for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-        const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-        if (!(ok = __all_sync(0xffffffffu, afd::mbar_wait(empty + 8 * s, ph ^ 1, gave_up)))) break;
-        const uint32_t a = smem + s * kStageBytes, b = a + kHalfBytes, bar = lead_full + 8 * s;
+      for (int kb = 0; kb < p.k_blocks; ++kb, ring.advance()) {
+        const int s = ring.slot;
+        if (!(ok = afd::mbar_wait(empty + 8 * s, ring.phase ^ 1, gave_up))) break;
+        const uint32_t a = smem + s * ring.bytes, b = a + kHalfBytes, bar = lead_full + 8 * s;
         const int k = kb * (FP8 ? 128 : 64);
         if (afd::elect_one()) {
           if (rank == 0) afd::mbar_expect(full + 8 * s, bytes);
@@ -445,38 +465,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     // The pair's last products have read this CTA's operands.
-    for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
-      ok = __all_sync(0xffffffffu, afd::mbar_wait(empty + 8 * (i % kStages), (i / kStages) & 1, gave_up));
+    ring.last([&](int slot, uint32_t parity) { ok = ok && afd::mbar_wait(empty + 8 * slot, parity, gave_up); });
     if (!ok && rank == 0) {
       // Copies in flight count on this CTA's barriers: wait for the last ring of them.
-      for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
+      ring.last([&](int slot, uint32_t parity) {
         const long long t0 = clock64();
-        while (!afd::mbar_try(full + 8 * (i % kStages), (i / kStages) & 1) && clock64() - t0 < 2000000) {
+        while (!afd::mbar_try(full + 8 * slot, parity) && clock64() - t0 < 2000000) {
         }
-      }
+      });
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------- products
     if (rank == 0) {
-      uint32_t it = 0, unit = 0;
+      Ring ring(sh.widest);
+      uint32_t unit = 0;
       bool ok = true;
       Tile tile;
       for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
         const uint32_t idesc = afd::instr_desc(FP8, kPairRows, tile.cols());
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+        for (int kb = 0; kb < p.k_blocks; ++kb, ring.advance()) {
           const bool opens = FP8 || kb == 0, closes = FP8 || kb == p.k_blocks - 1;
           if (opens) {
             const uint32_t buf = turns.buf(unit), ph = turns.phase(unit) ^ 1;
-            ok = __all_sync(0xffffffffu, afd::mbar_wait(drained + 8 * buf, ph, gave_up) &&
-                                             afd::mbar_wait(peer_drained + 8 * buf, ph, gave_up));
+            ok = afd::mbar_wait(drained + 8 * buf, ph, gave_up) && afd::mbar_wait(peer_drained + 8 * buf, ph, gave_up);
             if (!ok) break;
           }
-          const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-          if (!(ok = __all_sync(0xffffffffu, afd::mbar_wait(full + 8 * s, ph, gave_up)))) break;
+          const int s = ring.slot;
+          if (!(ok = afd::mbar_wait(full + 8 * s, ring.phase, gave_up))) break;
           afd::tcgen05_fence_after();
-          const uint64_t a = afd::operand_desc(smem + s * kStageBytes);
-          const uint64_t b = afd::operand_desc(smem + s * kStageBytes + kHalfBytes);
+          const uint64_t a = afd::operand_desc(smem + s * ring.bytes);
+          const uint64_t b = afd::operand_desc(smem + s * ring.bytes + kHalfBytes);
           const uint32_t d = tmem + turns.buf(unit) * turns.cols;
           if (afd::elect_one()) {
 #pragma unroll
@@ -504,7 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int turn = 0; ok && dealt(turn, pair, pairs) < tiles; ++turn) {
         for (int kb = 0; kb < (FP8 ? p.k_blocks : 1); ++kb, ++unit) {
           const uint32_t buf = turns.buf(unit);
-          if (!(ok = __all_sync(0xffffffffu, afd::mbar_wait(drained + 8 * buf, turns.phase(unit), gave_up)))) break;
+          if (!(ok = afd::mbar_wait(drained + 8 * buf, turns.phase(unit), gave_up))) break;
           if (lane == 0) afd::mbar_arrive_cluster(lead + 8 * buf);
         }
       }
@@ -541,7 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 0; j < kScaleAhead; ++j) {
             if (ok && kb0 + j < p.k_blocks) {
               const uint32_t s = it % kScaleStages, ph = (it / kScaleStages) & 1;
-              ok = __all_sync(0xffffffffu, afd::mbar_wait(scale_empty + 8 * s, ph ^ 1, gave_up));
+              ok = afd::mbar_wait(scale_empty + 8 * s, ph ^ 1, gave_up);
               if (ok) {
                 ++it;
 #pragma unroll
@@ -572,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Out out = lane_out<GATED>(p, tile, n0, lane);
       if (!FP8) {
         const uint32_t b = turns.buf(unit);
-        ok = __all_sync(0xffffffffu, afd::mbar_wait(drain_full + 8 * b, turns.phase(unit), gave_up));
+        ok = afd::mbar_wait(drain_full + 8 * b, turns.phase(unit), gave_up);
         if (!ok) break;
         afd::tcgen05_fence_after();
         for (int c = 16 * h; c < tile.cols(); c += 16 * kDrainParts) {
