@@ -456,6 +456,15 @@ def _call(name: str, on: torch.Tensor, stream, *args) -> None:
         raise AfdError(st, f"{name}: {lib.afd_status_string(st).decode()}")
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """A new tensor from the pool of the stream that will use it (what the
+    allocator hands out on another one may still be in use there)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> int:
     """Checks a dense tensor; returns its address."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
@@ -499,11 +508,11 @@ def route_topk(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
     live_ptr = None if live_tokens is None else _want(live_tokens, "live_tokens", torch.int32, (1,))
     shape = (T, top_k)
     if ids is None:
-        ids = torch.empty(shape, dtype=torch.int64, device=logits.device)
+        ids = _empty(shape, torch.int64, logits.device, stream)
     else:
         _want(ids, "ids", torch.int64, shape)
     if weights is None:
-        weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+        weights = _empty(shape, torch.float32, logits.device, stream)
     else:
         _want(weights, "weights", torch.float32, shape)
     _call("afd_route_topk", ids, stream, logits.data_ptr(), FP32 if logits.dtype is torch.float32 else BF16, stride,
@@ -547,7 +556,7 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, ends: torch.Tensor, *,
     elif x_scale is not None or weight_scale is not None:
         raise AfdError(ERR_ARG, "bfloat16 rows take no scales")
     if out is None:
-        out = torch.empty((R, N), dtype=torch.bfloat16, device=x.device)
+        out = _empty((R, N), torch.bfloat16, x.device, stream)
     out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
     if error is not None:
         error_ptr = _want(error, "error", torch.int32, (1,))
@@ -569,7 +578,7 @@ def gated_rows(h: torch.Tensor, ends: torch.Tensor, *, expert_alignment: int = 1
     G = ends.numel()
     ends_ptr = _want(ends, "ends", torch.int32, (G,))
     if out is None:
-        out = torch.empty((R, N), dtype=torch.bfloat16, device=h.device)
+        out = _empty((R, N), torch.bfloat16, h.device, stream)
     out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
     _call("afd_gated_rows", ends, stream, h.data_ptr(), h_stride, ends_ptr, G, expert_alignment, R, N, out.data_ptr(),
           out_stride)
@@ -611,9 +620,8 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
     else:
         out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
     size = (R + S + 5) // 4 * 16 + 4 * R * rank  # afd_adapter_workspace_bytes
-    workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
-    if stream is not None:  # the allocator must not hand it on before that stream is done with it
-        workspace.record_stream(stream)
+    on = x.device if x.is_cuda else torch.device("cuda", _current_device())
+    workspace = _empty(size, torch.uint8, on, stream)
     _call("afd_adapter_add", workspace, stream, base.data_ptr(), base_stride, x.data_ptr(), x_stride, down_ptr, up_ptr,
           slots_ptr, scales_ptr, src_ptr, ends_ptr, G, top_k, R, tokens, S, rank, K, N, out.data_ptr(), out_stride,
           workspace.data_ptr(), size)

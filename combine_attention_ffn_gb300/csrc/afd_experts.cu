@@ -697,6 +697,10 @@ extern "C" AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride
   if (num_groups > afd::kMaxExperts || num_rows > INT32_MAX - (int64_t)expert_alignment || N > (1 << 24) || K > (1 << 24))
     return AFD_ERR_UNSUPPORTED;
   if (K * elt % 16 || x_stride * elt % 16 || (fp8 && (K % 128 || N % 128))) return AFD_ERR_UNSUPPORTED;
+  // the most tiles there can be, counted in 32 bits by the kernel
+  const int m_tiles = ((gated ? 2 * N : N) + kPairRows - 1) / kPairRows;
+  const int64_t most = ((num_groups < num_rows ? num_groups : num_rows) + num_rows / kTileRows) * m_tiles;
+  if (most > (1 << 30)) return AFD_ERR_UNSUPPORTED;
   if (num_rows == 0) return AFD_OK;
   if (!afd::aligned_to(x, 16) || !afd::aligned_to(weight, 16)) return AFD_ERR_UNSUPPORTED;
   if (!afd::aligned_to(x_scale, 4) || !afd::aligned_to(weight_scale, 4) || !afd::aligned_to(ends, 4) ||
@@ -737,14 +741,11 @@ extern "C" AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride
   ExpertParams p = {};
   p.x_scale = x_scale, p.w_scale = weight_scale, p.ends = ends;
   p.G = num_groups, p.alpha = expert_alignment, p.R = (int32_t)num_rows, p.K = K, p.N = N;
-  p.m_tiles = (W + kPairRows - 1) / kPairRows;
+  p.m_tiles = m_tiles;
   p.k_blocks = (K + block - 1) / block;
   p.out = static_cast<uint16_t*>(out), p.out_stride = out_stride, p.error = error;
   p.vec = N % 2 == 0 && out_stride % 2 == 0 && afd::aligned_to(out, 4);
-  // no more pairs than there can be tiles
-  const int64_t row_tiles_max = (num_groups < num_rows ? num_groups : num_rows) + num_rows / kTileRows;
-  const int64_t most = row_tiles_max * p.m_tiles;
-  const int pairs = (int)(most < sms / 2 ? most : sms / 2);
+  const int pairs = (int)(most < sms / 2 ? most : sms / 2);  // no more than there can be tiles
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = fp8 ? (gated ? launch_grouped<true, true>(maps, p, dev, pairs, s) : launch_grouped<true, false>(maps, p, dev, pairs, s))
                             : (gated ? launch_grouped<false, true>(maps, p, dev, pairs, s) : launch_grouped<false, false>(maps, p, dev, pairs, s));

@@ -458,7 +458,8 @@ AFD_API afd_status afd_route_topk(const void* logits, int32_t logits_dtype, int6
  * Buffers are device memory of the current device (the rows and weights move
  * by bulk copies). x, weight, x_stride and the rows of weight are multiples
  * of 16 bytes; FP8 takes in_features and out_features that are multiples of
- * 128. num_groups <= 1024.
+ * 128. num_groups <= 1024, in_features and out_features <= 2^24, and at most
+ * 2^30 tiles of 256 weight rows by 256 rows.
  * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (sizes or alignments above),
  * AFD_ERR_CUDA. */
 AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride, const float* x_scale,

@@ -53,6 +53,7 @@ def _grouped(lib, **over):
     (dict(x_stride=260), afd.ERR_UNSUPPORTED),
     (dict(dtype=afd.FP8_E4M3, x_scale=P, w_scale=P, K=192), afd.ERR_UNSUPPORTED),
     (dict(dtype=afd.FP8_E4M3, x_scale=P, w_scale=P, N=64), afd.ERR_UNSUPPORTED),
+    (dict(N=1 << 24, out_stride=1 << 24, R=1 << 30), afd.ERR_UNSUPPORTED), (dict(N=(1 << 24) + 1, out_stride=1 << 25), afd.ERR_UNSUPPORTED),
     (dict(x=ctypes.c_void_p(4104)), afd.ERR_UNSUPPORTED), (dict(w=ctypes.c_void_p(4104)), afd.ERR_UNSUPPORTED),
     (dict(ends=ctypes.c_void_p(4098)), afd.ERR_ARG), (dict(out=ctypes.c_void_p(4097)), afd.ERR_ARG),
     (dict(R=0, x=None, out=None), afd.OK)])

@@ -2,6 +2,9 @@
 afd_adapter_add) against float64 values from their definitions, at the sizes
 and masks where they can go wrong, and their refusals that need a GPU."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -11,6 +14,7 @@ import expert_harness as eh
 from combine_attention_ffn_gb300 import afd
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BF16, FP8 = torch.bfloat16, torch.float8_e4m3fn
 
 
@@ -107,6 +111,13 @@ def test_grouped_fp8_sizes(K, N, gated):
 def test_grouped_most_experts():
     counts = [(i * 5) % 4 for i in range(1024)]
     _grouped_check(*_grouped_case(counts, 1, 64, 64, False, False, 3), 1, False)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_grouped_more_tiles_than_are_listed(gated):
+    """Over 100 tiles for every pair of CTAs, of several widths."""
+    counts = [(i * 7) % 5 + (90 if i % 50 == 0 else 0) for i in range(1024)]
+    _grouped_check(*_grouped_case(counts, 1, 64, 2048 // (1 + gated), gated, False, 4), 1, gated)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -347,6 +358,52 @@ def test_adapters_strided_and_captured():
     eh.check_bf16(out, want, err, torch.ones(R, dtype=torch.bool, device="cuda"))
 
 
+def test_adapters_many_rows():
+    """More rows than the grouping keeps in registers, and uneven groups."""
+    R, K, N, rank, S = 40_000, 32, 24, 8, 300
+    x, base, down, up, scales, slots = _adapter_case(R, K, N, rank, S, 7, R)
+    slots[: R // 2] = 3
+    out = lib.adapter_add(base, x, down, up, slots, scales, out=torch.empty_like(base))
+    s = slots.long()
+    ok = (s >= 0) & (s < S)
+    d, u = down.double()[s.clamp(0, S - 1)], up.double()[s.clamp(0, S - 1)]
+    t = torch.einsum("rk,rjk->rj", x.double(), d)
+    sc = torch.where(ok, scales.double()[s.clamp(0, S - 1)], 0.0)[:, None]
+    want = base.double() + sc * torch.einsum("rj,rnj->rn", t, u)
+    et = K * eh.FP32_STEP * torch.einsum("rk,rjk->rj", x.double().abs(), d.abs()) + 2.0 ** -16 * t.abs()
+    err = sc * torch.einsum("rj,rnj->rn", et, u.abs()) + (2 * rank + 4) * eh.FP32_STEP * (want.abs() + base.double().abs() + sc * (
+        t.abs()[:, None, :] * u.abs()).sum(-1))
+    eh.check_bf16(out, want, err, torch.ones(R, dtype=torch.bool, device="cuda"))
+
+
+def test_adapters_keep_requests_apart():
+    """An adapter full of infinities and NaN reaches its own rows only; so do rows of NaN."""
+    R, K, N, rank, S = 70, 64, 40, 16, 4
+    x, base, down, up, scales, _ = _adapter_case(R, K, N, rank, S, 8, R)
+    slots = (torch.arange(R, device="cuda") % 4).int()
+    clean = lib.adapter_add(base, x, down, up, slots, scales, out=torch.empty_like(base))
+    down[2], up[1] = float("inf"), float("nan")
+    x[3] = float("nan")
+    out = lib.adapter_add(base, x, down, up, slots, scales, out=torch.empty_like(base))
+    own = (slots == 1) | (slots == 2)
+    own[3] = True
+    assert torch.equal(out[~own], clean[~own])
+    assert not torch.isfinite(out[own]).any()
+
+
+def test_adapters_two_streams_at_once():
+    R, K, N, rank, S = 500, 512, 256, 32, 6
+    a, b = (_adapter_case(R, K, N, rank, S, seed, R) for seed in (1, 2))
+    call = lambda c, **kw: lib.adapter_add(c[1], c[0], c[2], c[3], c[5], c[4], out=torch.empty_like(c[1]), **kw)
+    want = [call(a), call(b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[call(c, stream=s) for _ in range(20)] for c, s in zip((a, b), streams)]
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        assert all(torch.equal(w, o) for o in outs)
+
+
 # ------------------------------------------------------------------ router
 def _route_check(logits, top_k, **kw):
     ids, w = lib.route_topk(logits, top_k, **kw)
@@ -538,6 +595,51 @@ def test_whole_expert_path(fp8, T):
         buf.close()
 
 
+def test_calls_on_a_given_stream():
+    """stream=: the operators run there, and so do the tensors they make."""
+    side = torch.cuda.Stream()
+    ends = torch.tensor([3, 9], dtype=torch.int32, device="cuda")
+    x = torch.randn(9, 128, generator=_gen(1), device="cuda").to(BF16)
+    w = torch.randn(2, 256, 128, generator=_gen(2), device="cuda").to(BF16)
+    logits = torch.randn(9, 16, generator=_gen(3), device="cuda")
+    want = (*lib.route_topk(logits, 2), lib.grouped_linear(x, w, ends, gated=True), lib.gated_rows(x, ends))
+    torch.cuda.synchronize()
+    got = (*lib.route_topk(logits, 2, stream=side), lib.grouped_linear(x, w, ends, gated=True, stream=side),
+           lib.gated_rows(x, ends, stream=side))
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first call of every operator is captured (nothing has to be set up eagerly)."""
+    code = """
+import torch, combine_attention_ffn_gb300 as lib
+d = "cuda"
+ends = torch.tensor([3, 9], dtype=torch.int32, device=d)
+x = torch.randn(9, 128, device=d).bfloat16(); w = torch.randn(2, 256, 128, device=d).bfloat16()
+q = x.to(torch.float8_e4m3fn); qw = w.to(torch.float8_e4m3fn)
+xs, ws = torch.ones(9, 1, device=d), torch.ones(2, 2, 1, device=d)
+logits = torch.randn(9, 16, device=d)
+down, up = torch.randn(2, 16, 128, device=d).bfloat16(), torch.randn(2, 256, 16, device=d).bfloat16()
+slots, scales = torch.tensor([0, 1, -1] * 3, dtype=torch.int32, device=d), torch.ones(2, device=d)
+def step():
+    h = lib.grouped_linear(x, w, ends)
+    return [*lib.route_topk(logits, 2), lib.adapter_add(h, x, down, up, slots, scales), lib.gated_rows(h, ends),
+            lib.grouped_linear(x, w, ends, gated=True), lib.grouped_linear(q, qw, ends, x_scale=xs, weight_scale=ws)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+g.replay(); torch.cuda.synchronize()
+for a, b in zip(got, step()):
+    assert torch.equal(a, b)
+print("captured first: ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=120)
+    assert r.returncode == 0 and "captured first: ok" in r.stdout, r.stderr[-2000:]
+
+
 # ---------------------------------------------------------------- refusals
 def test_refusals_of_unreachable_and_unaligned_buffers():
     """Host memory, misaligned bases and bad shapes raise before anything runs."""
@@ -574,8 +676,17 @@ def test_row_operators_take_pinned_host_buffers():
     logits = torch.randn(5, 16, generator=_gen(1), device="cuda")
     ids, w = lib.route_topk(logits, 3)
     pids, pw = (torch.zeros(5, 3, dtype=d).pin_memory() for d in (torch.int64, torch.float32))
-    host = pin(logits)
-    afd._call("afd_route_topk", logits, None, host.data_ptr(), afd.FP32, 16, None, None, 5, 16, 3, 0, 1, 1.0,
-              pids.data_ptr(), pw.data_ptr())
+    lib.route_topk(pin(logits), 3, ids=pids, weights=pw)
+    ends = torch.tensor([4, 5], dtype=torch.int32, device="cuda")
+    h = torch.randn(5, 64, generator=_gen(2), device="cuda").to(BF16)
+    act, pact = lib.gated_rows(h, ends), torch.zeros(5, 32, dtype=BF16).pin_memory()
+    lib.gated_rows(pin(h), pin(ends), out=pact)
+    case = _adapter_case(20, 64, 40, 16, 3, 3, 20)
+    x, base, down, up, scales, slots = case
+    want = lib.adapter_add(base, x, down, up, slots, scales, out=torch.empty_like(base))
+    px, pbase, pdown, pup, pscales, pslots = (pin(t) for t in case)
+    lib.adapter_add(pbase, px, pdown, pup, pslots, pscales)
     torch.cuda.synchronize()
     assert torch.equal(pids, ids.cpu()) and torch.equal(pw, w.cpu())
+    assert torch.equal(pact, act.cpu())
+    assert torch.equal(pbase, want.cpu())
