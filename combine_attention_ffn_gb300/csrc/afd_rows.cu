@@ -100,12 +100,13 @@ struct AdapterParams {
 // dependent launch.
 //   group: the live rows sorted by adapter (a request's rows are spread over
 //          every expert's range, so rows that follow one another mostly differ
-//          in theirs), and where each adapter starts.
+//          in theirs), and where each adapter starts; rows without one last.
 //   down:  t = scale * down[a] x for 16 rows of one adapter a block, K split
-//          over its eight warps and joined in a fixed order.
+//          over its eight warps and joined in a fixed order. Then the blocks
+//          copy the rows without an adapter (not in place): few blocks have a
+//          tile more than the others, and the copies fill the rest.
 //   up:    out = base + up[a] t for 16 rows and some of the columns a warp, 32
-//          columns at a time with the next ones' operands on their way; rows
-//          without an adapter are copied.
+//          columns at a time with the next ones' operands on their way.
 // What bounds it is the traffic of x, base and out (about 6 bytes a column and
 // row against 2 rank flops), which down and up stream with many small blocks
 // in flight. mma.sync's rate is enough, and its register operands spare TMEM
@@ -115,7 +116,7 @@ struct AdapterParams {
 // neither the order of the rows inside a group nor what another request's
 // adapter holds reaches a result.
 // t is FP32; between the two it is kept as two BF16 (16 bits and more).
-constexpr int kMaxSlots = 1024;
+constexpr int kMaxSlots = 1023;    // and the rows without one: a thread of the grouping each
 constexpr int kGroupCtas = 8;
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupKeep = 4;      // rows of a thread whose group it remembers
@@ -150,9 +151,8 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// One cluster: counts per adapter and CTA, their prefix, then every row's
-// place. Inside a group the order is that of the atomics; no result depends
-// on it.
+// One cluster: counts per group and CTA, their prefix, then every row's place.
+// Inside a group the order is that of the atomics; no result depends on it.
 __global__ void __cluster_dims__(kGroupCtas, 1, 1) __launch_bounds__(kGroupThreads) adapter_group_kernel(const AdapterParams p) {
   __shared__ int count[kMaxSlots + 1], cursor[kMaxSlots + 1];
   __shared__ int warp_total[kGroupThreads / 32];
@@ -160,7 +160,7 @@ __global__ void __cluster_dims__(kGroupCtas, 1, 1) __launch_bounds__(kGroupThrea
   afd::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t cta = blockIdx.x;
-  const int groups = p.S + 1;
+  const int groups = p.S + 1;  // at most kGroupThreads
   const int limit = p.row_src ? afd::group_end(p.ends[p.G - 1], p.R) : p.R;
   const int share = ((limit + kGroupCtas - 1) / kGroupCtas + 31) & ~31;
   const int64_t lo = (int64_t)cta * share, hi = lo + share < limit ? lo + share : limit;
@@ -182,20 +182,18 @@ __global__ void __cluster_dims__(kGroupCtas, 1, 1) __launch_bounds__(kGroupThrea
   const int64_t rest = lo + kGroupKeep * kGroupThreads + 32 * warp;
   for (int64_t r0 = rest; r0 < hi; r0 += kGroupThreads) tally(r0 + lane < hi ? row_group(p, (int)r0 + lane) : -1);
   cluster_sync();
-  // a thread takes `each` neighbouring groups of the prefix sum
-  const int each = (groups + kGroupThreads - 1) / kGroupThreads;
-  int total[2] = {0, 0}, before[2] = {0, 0};  // each <= 2
-  for (int i = 0; i < each; ++i) {
-    const int g = threadIdx.x * each + i;
-    if (g >= groups) break;
+  // a thread per group of the prefix sum
+  const int g = threadIdx.x;
+  int total = 0, before = 0;
+  if (g < groups) {
 #pragma unroll
     for (uint32_t c = 0; c < kGroupCtas; ++c) {
       const int v = *remote(&count[g], c);
-      total[i] += v;
-      if (c < cta) before[i] += v;
+      total += v;
+      if (c < cta) before += v;
     }
   }
-  int run = afd::warp_inclusive_scan(total[0] + total[1]);
+  int run = afd::warp_inclusive_scan(total);
   if (lane == 31) warp_total[warp] = run;
   __syncthreads();
   if (warp == 0) {
@@ -203,14 +201,13 @@ __global__ void __cluster_dims__(kGroupCtas, 1, 1) __launch_bounds__(kGroupThrea
     warp_total[lane] = afd::warp_inclusive_scan(t) - t;
   }
   __syncthreads();
-  run += warp_total[warp] - total[0] - total[1];
-  for (int i = 0; i < each; ++i) {
-    const int g = threadIdx.x * each + i;
-    if (g >= groups) break;
-    cursor[g] = run + before[i];
-    if (cta == 0) p.first[g] = run;
-    run += total[i];
-    if (cta == 0 && g == groups - 1) p.first[groups] = run;
+  run += warp_total[warp] - total;
+  if (g < groups) {
+    cursor[g] = run + before;
+    if (cta == 0) {
+      p.first[g] = run;
+      if (g == groups - 1) p.first[groups] = run + total;
+    }
   }
   __syncthreads();
   auto place = [&](int g, int64_t r) {
@@ -390,6 +387,24 @@ __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const Ada
     }
     __syncthreads();
   }
+  if (p.out == p.base && p.out_stride == p.base_stride) return;
+  // Rows without an adapter, a row a warp, from the last block on: the first
+  // ones may have had a tile more.
+  const int plain = groups.first[p.S], plain_end = p.first[p.S + 1];
+  for (int i = plain + (int)(gridDim.x - 1 - blockIdx.x) * kDownWarps + warp; i < plain_end; i += gridDim.x * kDownWarps) {
+    const int64_t r = p.order[i];
+    const uint16_t* from = p.base + r * p.base_stride;
+    uint16_t* to = p.out + r * p.out_stride;
+    for (int c0 = lane * 8; c0 < p.N; c0 += 4 * 256) {
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c0 + 256 * j < p.N) v[j] = afd::ld_once(reinterpret_cast<const uint4*>(from + c0 + 256 * j));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c0 + 256 * j < p.N) *reinterpret_cast<uint4*>(to + c0 + 256 * j) = v[j];
+    }
+  }
 }
 
 // EL rank values (EL / 2 words) of a thread.
@@ -434,7 +449,7 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
   const GroupTable groups = table_at(&sh + 1, p.S);
   afd::pdl_wait();
   afd::pdl_launch_dependents();
-  const int tiles = load_groups<kUpRows>(p, groups, p.S + 1);
+  const int tiles = load_groups<kUpRows>(p, groups, p.S);
   // The columns are split so far that every warp has something to do.
   const int want = max(1, min(col_groups, slots / max(4 * tiles, 1)));
   const int each = (col_groups + want - 1) / want, parts = (col_groups + each - 1) / each;
@@ -442,12 +457,11 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
   for (int64_t item = (int64_t)blockIdx.x * (kUpThreads / 32) + warp; item < items; item += slots) {
     const int quarter = (int)(item & 3);
     const int t = (int)((item >> 2) / parts), part = (int)((item >> 2) % parts);
-    const int a = tile_group(groups, p.S + 1, t);
+    const int a = tile_group(groups, p.S, t);
     const int at = groups.first[a] + (t - groups.first_tile[a]) * kUpRows + 16 * quarter, end = groups.first[a + 1];
     if (at >= end) continue;
     const int g0 = part * each, g1 = min(g0 + each, col_groups);
-    const bool adapt = a < p.S;  // the last group has no adapter: its rows are copied
-    const uint16_t* base[2];     // this thread's rows at its first column: g / g + 8
+    const uint16_t* base[2];  // this thread's rows at its first column: g / g + 8
     uint16_t* out[2];
     uint32_t th[2][CH][EL / 2], tl[2][CH][EL / 2];
     bool live[2];
@@ -462,7 +476,7 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
     // column tile i holds columns 8 j + 2 i and 8 j + 2 i + 1, so that a thread
     // ends with eight neighbouring ones
     const int col = (g >> 1) * 8 + (g & 1);
-    const uint16_t* up = p.up + ((int64_t)(adapt ? a : 0) * p.N + col) * RANK + tig * EL;
+    const uint16_t* up = p.up + ((int64_t)a * p.N + col) * RANK + tig * EL;
     auto fetch = [&](int gi) {
       if (gi < g1) {
         UpStage<RANK>& st = stage[gi % kUpStages];
@@ -472,14 +486,12 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
           const bool in = live[h] && n0 + tig * 8 < p.N;
           copy_async<16>(&st.base[h][lane], in ? base[h] + n0 : p.base, in);
         }
-        if (adapt) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool in = n0 + col + 2 * i < p.N;
+        for (int i = 0; i < 4; ++i) {
+          const bool in = n0 + col + 2 * i < p.N;
 #pragma unroll
-            for (int q = 0; q < CH; ++q)
-              copy_async<2 * EL>(&st.up[i][q][lane], in ? up + (int64_t)(n0 + 2 * i) * RANK + q * 32 : p.up, in);
-          }
+          for (int q = 0; q < CH; ++q)
+            copy_async<2 * EL>(&st.up[i][q][lane], in ? up + (int64_t)(n0 + 2 * i) * RANK + q * 32 : p.up, in);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -491,8 +503,8 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
 #pragma unroll
       for (int q = 0; q < CH; ++q) {
         const int64_t o = (int64_t)(at + 8 * h + g) * RANK + q * 32 + tig * EL;
-        load_rank<EL>(p.t_hi + o, live[h] && adapt, th[h][q]);
-        load_rank<EL>(p.t_lo + o, live[h] && adapt, tl[h][q]);
+        load_rank<EL>(p.t_hi + o, live[h], th[h][q]);
+        load_rank<EL>(p.t_lo + o, live[h], tl[h][q]);
       }
     for (int gi = g0; gi < g1; ++gi) {
       fetch(gi + kUpStages - 1);
@@ -500,37 +512,35 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
       const UpStage<RANK>& st = stage[gi % kUpStages];
       const int n0 = gi * 32;
       uint4 bv[2] = {st.base[0][lane], st.base[1][lane]};
-      if (adapt) {
-        float acc[4][4];  // [column tile]
+      float acc[4][4];  // [column tile]
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+#pragma unroll
+        for (int q = 0; q < CH; ++q) {
+          const auto b = st.up[i][q][lane];
+#pragma unroll
+          for (int s = 0; s < STEPS; ++s) {
+            const int e0 = 2 * s, e1 = EL == 2 ? 0 : 2 * s + 1;
+            const bool two = EL != 2;  // rank 8 fills half of a product's K
+            mma_16816(acc[i], th[0][q][e0], th[1][q][e0], two ? th[0][q][e1] : 0u, two ? th[1][q][e1] : 0u, b.v[e0],
+                      two ? b.v[e1] : 0u);
+            mma_16816(acc[i], tl[0][q][e0], tl[1][q][e0], two ? tl[0][q][e1] : 0u, two ? tl[1][q][e1] : 0u, b.v[e0],
+                      two ? b.v[e1] : 0u);
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float f[8];
+        afd::bf16x8_to_float(bv[h], f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-#pragma unroll
-          for (int q = 0; q < CH; ++q) {
-            const auto b = st.up[i][q][lane];
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-              const int e0 = 2 * s, e1 = EL == 2 ? 0 : 2 * s + 1;
-              const bool two = EL != 2;  // rank 8 fills half of a product's K
-              mma_16816(acc[i], th[0][q][e0], th[1][q][e0], two ? th[0][q][e1] : 0u, two ? th[1][q][e1] : 0u, b.v[e0],
-                        two ? b.v[e1] : 0u);
-              mma_16816(acc[i], tl[0][q][e0], tl[1][q][e0], two ? tl[0][q][e1] : 0u, two ? tl[1][q][e1] : 0u, b.v[e0],
-                        two ? b.v[e1] : 0u);
-            }
-          }
+          f[2 * i] += acc[i][2 * h];
+          f[2 * i + 1] += acc[i][2 * h + 1];
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float f[8];
-          afd::bf16x8_to_float(bv[h], f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[2 * i] += acc[i][2 * h];
-            f[2 * i + 1] += acc[i][2 * h + 1];
-          }
-          bv[h] = afd::float_to_bf16x8(f);
-        }
+        bv[h] = afd::float_to_bf16x8(f);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -554,8 +564,8 @@ cudaError_t launch_adapters(const AdapterParams& p, int device, int sms, cudaStr
   if (e != cudaSuccess) return e;
   // A tile holds rows of one group: at most one partial tile for each. Blocks
   // beyond what fits at once would only queue, so each takes several tiles.
-  const int64_t down = p.R / kDownRows + (p.S < p.R ? p.S : p.R);
-  const int64_t up = (p.R / kUpRows + (p.S + 1 < p.R ? p.S + 1 : p.R)) * (((int64_t)p.N + 31) / 32);
+  const int64_t down = (int64_t)p.R / kDownRows + (p.S < p.R ? p.S : p.R);
+  const int64_t up = (p.R / kUpRows + (p.S < p.R ? p.S : p.R)) * (((int64_t)p.N + 31) / 32);
   const int64_t down_most = (int64_t)sms * (down_fit < 4 ? down_fit : 4), up_most = (int64_t)sms * (up_fit < 2 ? up_fit : 2);
   e = afd::launch_dependent(adapter_down_kernel<RANK>, down < down_most ? down : down_most, kDownWarps * 32, down_smem, stream, p);
   if (e != cudaSuccess) return e;

@@ -496,7 +496,8 @@ AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t
  * With row_src, rows r >= ends[num_groups-1] and rows whose row_src is
  * negative or names a token outside [0, num_tokens) are left as they were.
  *   base, out    device BF16 [num_rows, out_features], row strides
- *                base_stride / out_stride; out may be base (in place)
+ *                base_stride / out_stride; out may be base (in place), and must
+ *                not overlap the inputs in any other way
  *   x            device BF16 [num_rows, in_features], row stride x_stride
  *   down         device BF16 [num_slots, rank, in_features], contiguous
  *   up           device BF16 [num_slots, out_features, rank], contiguous
@@ -508,7 +509,7 @@ AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t
  *                num_slots, rank) bytes, 16-byte aligned; its contents need not be set
  *                and mean nothing afterwards. Calls that may run at the same
  *                time (other streams, other captured graphs) need one each.
- * Limits: num_slots <= 1024; rank 8, 16, 32 or 64; in_features a multiple of
+ * Limits: num_slots <= 1023; rank 8, 16, 32 or 64; in_features a multiple of
  * 16; out_features a multiple of 8; base, out, x, down, up and the strides multiples of 16
  * bytes. Buffers may be device, managed or page-locked host memory.
  * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (limits), AFD_ERR_CUDA. */

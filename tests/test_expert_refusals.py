@@ -92,7 +92,7 @@ def _adapter(lib, **over):
     (dict(scales=None), afd.ERR_ARG), (dict(out=None), afd.ERR_ARG), (dict(rank=24), afd.ERR_UNSUPPORTED),
     (dict(rank=128), afd.ERR_UNSUPPORTED), (dict(K=120), afd.ERR_UNSUPPORTED),
     (dict(N=60, base_stride=60, out_stride=60), afd.ERR_UNSUPPORTED), (dict(base_stride=68), afd.ERR_UNSUPPORTED),
-    (dict(S=1025, ws_bytes=1 << 20), afd.ERR_UNSUPPORTED), (dict(ws=None), afd.ERR_ARG), (dict(ws_bytes=48 + 511), afd.ERR_ARG),
+    (dict(S=1024, ws_bytes=1 << 20), afd.ERR_UNSUPPORTED), (dict(ws=None), afd.ERR_ARG), (dict(ws_bytes=48 + 511), afd.ERR_ARG),
     (dict(R=0, base=None, x=None, out=None, ws=None, ws_bytes=0), afd.OK)])
 def test_adapters(lib, over, status):
     assert _adapter(lib, **over) == status
