@@ -25,12 +25,22 @@
 // rows in shared memory, so the two sums of an output sit in neighbouring
 // lanes and one shuffle brings them together.
 //
+// What bounds it, measured (16.4 K rows of 64 experts, K 2048, 2 x 1024 weight
+// rows, gated, BF16: 116 us, 5.5 TB/s of DRAM traffic): the reads through L2,
+// 1.35 GB at 11.6 TB/s, about as fast as the box moves them; a decode step
+// (one token a source) streams the touched experts' weights at 5.4 TB/s in
+// 14 us. One lane alone in the loops of the loading and issuing warps, as a
+// first form had it, took 100 clocks an issue and 150 us.
+//
 // FP8: each 128-wide K block has scales of its own, so it gets an accumulator
 // of its own; the draining warps add it, scaled, to FP32 sums in registers:
 // one multiply-add a value, with x_scale * weight_scale multiplied once per
 // row and block by warps 2 and 3, which keep a ring of them in shared memory.
-// 128 sums a thread need more than an even share of the registers, so the
-// other warps hand theirs over.
+// 64 sums a thread need more than an even share of the registers, so the
+// other warps hand some of theirs over. This adding bounds it with many rows
+// (the shape above: 108 us against a floor of 50): one multiply-add a value
+// and K block, on issue slots that are 56% busy, with the products waiting for
+// it. Eight warps with twice the sums took 128 us.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -427,155 +437,155 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const Turns turns = {tmem, drain_full, drained, buf_shift, kColumns >> buf_shift};
 
   if (warp < 4) {
-  if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFrontRegs));
-  if (warp == 0) {
-    // ---------------------------------------------------------------- loads
-    // The whole warp walks the loop and one elected lane issues: with a single
-    // lane in it the compiler cannot keep the operands in uniform registers,
-    // and an issue takes 100 clocks and more.
-    uint64_t keep, once;
-    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
-    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-    const uint32_t lead_full = afd::map_to_rank(full, 0);
-    Ring ring(sh.widest);
-    bool ok = true;
-    Tile tile;
-    for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
-      const int half = tile.cols() >> 1;
-      const int row = tile.row + (int)rank * half;
-      const uint32_t bytes = 2 * (kHalfBytes + half * kBlockBytes);
-      const CUtensorMap* x_map = &maps.x[half / 16 - 1];
-      // this weight tile is read again if the expert has more row tiles
-      const uint64_t w_policy = tile.rows == group_count(sh, p, tile.group) ? once : keep;
-      const int w_row = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) : tile.m * kPairRows + (int)rank * kCtaRows;
-      for (int kb = 0; kb < p.k_blocks; ++kb, ring.advance()) {
-        const int s = ring.slot;
-        if (!(ok = afd::mbar_wait(empty + 8 * s, ring.phase ^ 1, gave_up))) break;
-        const uint32_t a = smem + s * ring.bytes, b = a + kHalfBytes, bar = lead_full + 8 * s;
-        const int k = kb * (FP8 ? 128 : 64);
-        if (afd::elect_one()) {
-          if (rank == 0) afd::mbar_expect(full + 8 * s, bytes);
-          if (GATED)
-            afd::tma_load_4d(a, &maps.w, bar, k, 0, w_row, tile.group, w_policy);
-          else
-            afd::tma_load_3d(a, &maps.w, bar, k, w_row, tile.group, w_policy);
-          afd::tma_load_2d(b, x_map, bar, k, row, keep);
-        }
-        __syncwarp();
-      }
-    }
-    // The pair's last products have read this CTA's operands.
-    ring.last([&](int slot, uint32_t parity) { ok = ok && afd::mbar_wait(empty + 8 * slot, parity, gave_up); });
-    if (!ok && rank == 0) {
-      // Copies in flight count on this CTA's barriers: wait for the last ring of them.
-      ring.last([&](int slot, uint32_t parity) {
-        const long long t0 = clock64();
-        while (!afd::mbar_try(full + 8 * slot, parity) && clock64() - t0 < 2000000) {
-        }
-      });
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------- products
-    if (rank == 0) {
+    if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFrontRegs));
+    if (warp == 0) {
+      // ---------------------------------------------------------------- loads
+      // The whole warp walks the loop and one elected lane issues: with a single
+      // lane in it the compiler cannot keep the operands in uniform registers,
+      // and an issue takes 100 clocks and more.
+      uint64_t keep, once;
+      asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+      asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+      const uint32_t lead_full = afd::map_to_rank(full, 0);
       Ring ring(sh.widest);
-      uint32_t unit = 0;
       bool ok = true;
       Tile tile;
       for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
-        const uint32_t idesc = afd::instr_desc(FP8, kPairRows, tile.cols());
+        const int half = tile.cols() >> 1;
+        const int row = tile.row + (int)rank * half;
+        const uint32_t bytes = 2 * (kHalfBytes + half * kBlockBytes);
+        const CUtensorMap* x_map = &maps.x[half / 16 - 1];
+        // this weight tile is read again if the expert has more row tiles
+        const uint64_t w_policy = tile.rows == group_count(sh, p, tile.group) ? once : keep;
+        const int w_row = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) : tile.m * kPairRows + (int)rank * kCtaRows;
         for (int kb = 0; kb < p.k_blocks; ++kb, ring.advance()) {
-          const bool opens = FP8 || kb == 0, closes = FP8 || kb == p.k_blocks - 1;
-          if (opens) {
-            const uint32_t buf = turns.buf(unit), ph = turns.phase(unit) ^ 1;
-            ok = afd::mbar_wait(drained + 8 * buf, ph, gave_up) && afd::mbar_wait(peer_drained + 8 * buf, ph, gave_up);
-            if (!ok) break;
-          }
           const int s = ring.slot;
-          if (!(ok = afd::mbar_wait(full + 8 * s, ring.phase, gave_up))) break;
-          afd::tcgen05_fence_after();
-          const uint64_t a = afd::operand_desc(smem + s * ring.bytes);
-          const uint64_t b = afd::operand_desc(smem + s * ring.bytes + kHalfBytes);
-          const uint32_t d = tmem + turns.buf(unit) * turns.cols;
+          if (!(ok = afd::mbar_wait(empty + 8 * s, ring.phase ^ 1, gave_up))) break;
+          const uint32_t a = smem + s * ring.bytes, b = a + kHalfBytes, bar = lead_full + 8 * s;
+          const int k = kb * (FP8 ? 128 : 64);
           if (afd::elect_one()) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)  // 32 bytes of K each
-              afd::mma_pair<FP8>(d, a + 2 * i, b + 2 * i, idesc, !(opens && i == 0));
-            afd::mma_commit_pair(empty + 8 * s);
-            if (closes) afd::mma_commit_pair(drain_full + 8 * turns.buf(unit));
+            if (rank == 0) afd::mbar_expect(full + 8 * s, bytes);
+            if (GATED)
+              afd::tma_load_4d(a, &maps.w, bar, k, 0, w_row, tile.group, w_policy);
+            else
+              afd::tma_load_3d(a, &maps.w, bar, k, w_row, tile.group, w_policy);
+            afd::tma_load_2d(b, x_map, bar, k, row, keep);
           }
           __syncwarp();
-          if (closes) ++unit;
         }
       }
-      if (!ok) {
-        // let the products in flight finish before TMEM is freed
-        const long long t0 = clock64();
-        while (clock64() - t0 < 2000000) {
-        }
-      }
-    } else {
-      // The odd CTA's warp passes on that its accumulators are read: one
-      // arrival across the pair instead of one for every draining warp.
-      const uint32_t lead = afd::map_to_rank(peer_drained, 0);
-      uint32_t unit = 0;
-      bool ok = true;
-      for (int turn = 0; ok && dealt(turn, pair, pairs) < tiles; ++turn) {
-        for (int kb = 0; kb < (FP8 ? p.k_blocks : 1); ++kb, ++unit) {
-          const uint32_t buf = turns.buf(unit);
-          if (!(ok = afd::mbar_wait(drained + 8 * buf, turns.phase(unit), gave_up))) break;
-          if (lane == 0) afd::mbar_arrive_cluster(lead + 8 * buf);
-        }
-      }
-    }
-    __syncwarp();
-  } else {
-    // --------------------------------------------------------------- scales
-    if (FP8) {
-      const int u = threadIdx.x - 64;
-      const int64_t w_rows = (int64_t)(GATED ? 2 : 1) * p.N / 128;
-      uint32_t it = 0;
-      bool ok = true;
-      Tile tile;
-      for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
-        const float* xs = p.x_scale + (int64_t)(tile.row + u) * p.k_blocks;
-        // the weight block of this CTA's rows (the last one for rows past N, which are not stored)
-        const int f = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) : tile.m * kPairRows + (int)rank * kCtaRows;
-        const float* wg = p.w_scale + (tile.group * w_rows + min(f, p.N - 1) / 128) * p.k_blocks;
-        const float* wu = wg + (int64_t)(p.N / 128) * p.k_blocks;
-        // kScaleAhead blocks are loaded at a time; the ring is twice as long,
-        // so the loads of the next ones overlap the use of these
-        for (int kb0 = 0; ok && kb0 < p.k_blocks; kb0 += kScaleAhead) {
-          float x[kScaleAhead][kScaleRows], w[kScaleAhead][2];
-#pragma unroll
-          for (int j = 0; j < kScaleAhead; ++j) {
-            const int kb = min(kb0 + j, p.k_blocks - 1);
-            w[j][0] = wg[kb];
-            w[j][1] = GATED ? wu[kb] : 0.f;
-#pragma unroll
-            for (int i = 0; i < kScaleRows; ++i)
-              x[j][i] = u + kScaleThreads * i < tile.rows ? xs[(int64_t)kScaleThreads * i * p.k_blocks + kb] : 0.f;
+      // The pair's last products have read this CTA's operands.
+      ring.last([&](int slot, uint32_t parity) { ok = ok && afd::mbar_wait(empty + 8 * slot, parity, gave_up); });
+      if (!ok && rank == 0) {
+        // Copies in flight count on this CTA's barriers: wait for the last ring of them.
+        ring.last([&](int slot, uint32_t parity) {
+          const long long t0 = clock64();
+          while (!afd::mbar_try(full + 8 * slot, parity) && clock64() - t0 < 2000000) {
           }
+        });
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------- products
+      if (rank == 0) {
+        Ring ring(sh.widest);
+        uint32_t unit = 0;
+        bool ok = true;
+        Tile tile;
+        for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
+          const uint32_t idesc = afd::instr_desc(FP8, kPairRows, tile.cols());
+          for (int kb = 0; kb < p.k_blocks; ++kb, ring.advance()) {
+            const bool opens = FP8 || kb == 0, closes = FP8 || kb == p.k_blocks - 1;
+            if (opens) {
+              const uint32_t buf = turns.buf(unit), ph = turns.phase(unit) ^ 1;
+              ok = afd::mbar_wait(drained + 8 * buf, ph, gave_up) && afd::mbar_wait(peer_drained + 8 * buf, ph, gave_up);
+              if (!ok) break;
+            }
+            const int s = ring.slot;
+            if (!(ok = afd::mbar_wait(full + 8 * s, ring.phase, gave_up))) break;
+            afd::tcgen05_fence_after();
+            const uint64_t a = afd::operand_desc(smem + s * ring.bytes);
+            const uint64_t b = afd::operand_desc(smem + s * ring.bytes + kHalfBytes);
+            const uint32_t d = tmem + turns.buf(unit) * turns.cols;
+            if (afd::elect_one()) {
 #pragma unroll
-          for (int j = 0; j < kScaleAhead; ++j) {
-            if (ok && kb0 + j < p.k_blocks) {
-              const uint32_t s = it % kScaleStages, ph = (it / kScaleStages) & 1;
-              ok = afd::mbar_wait(scale_empty + 8 * s, ph ^ 1, gave_up);
-              if (ok) {
-                ++it;
+              for (int i = 0; i < 4; ++i)  // 32 bytes of K each
+                afd::mma_pair<FP8>(d, a + 2 * i, b + 2 * i, idesc, !(opens && i == 0));
+              afd::mma_commit_pair(empty + 8 * s);
+              if (closes) afd::mma_commit_pair(drain_full + 8 * turns.buf(unit));
+            }
+            __syncwarp();
+            if (closes) ++unit;
+          }
+        }
+        if (!ok) {
+          // let the products in flight finish before TMEM is freed
+          const long long t0 = clock64();
+          while (clock64() - t0 < 2000000) {
+          }
+        }
+      } else {
+        // The odd CTA's warp passes on that its accumulators are read: one
+        // arrival across the pair instead of one for every draining warp.
+        const uint32_t lead = afd::map_to_rank(peer_drained, 0);
+        uint32_t unit = 0;
+        bool ok = true;
+        for (int turn = 0; ok && dealt(turn, pair, pairs) < tiles; ++turn) {
+          for (int kb = 0; kb < (FP8 ? p.k_blocks : 1); ++kb, ++unit) {
+            const uint32_t buf = turns.buf(unit);
+            if (!(ok = afd::mbar_wait(drained + 8 * buf, turns.phase(unit), gave_up))) break;
+            if (lane == 0) afd::mbar_arrive_cluster(lead + 8 * buf);
+          }
+        }
+      }
+      __syncwarp();
+    } else {
+      // --------------------------------------------------------------- scales
+      if (FP8) {
+        const int u = threadIdx.x - 64;
+        const int64_t w_rows = (int64_t)(GATED ? 2 : 1) * p.N / 128;
+        uint32_t it = 0;
+        bool ok = true;
+        Tile tile;
+        for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
+          const float* xs = p.x_scale + (int64_t)(tile.row + u) * p.k_blocks;
+          // the weight block of this CTA's rows (the last one for rows past N, which are not stored)
+          const int f = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) : tile.m * kPairRows + (int)rank * kCtaRows;
+          const float* wg = p.w_scale + (tile.group * w_rows + min(f, p.N - 1) / 128) * p.k_blocks;
+          const float* wu = wg + (int64_t)(p.N / 128) * p.k_blocks;
+          // kScaleAhead blocks are loaded at a time; the ring is twice as long,
+          // so the loads of the next ones overlap the use of these
+          for (int kb0 = 0; ok && kb0 < p.k_blocks; kb0 += kScaleAhead) {
+            float x[kScaleAhead][kScaleRows], w[kScaleAhead][2];
 #pragma unroll
-                for (int i = 0; i < kScaleRows; ++i) {
-                  sh.scale[s].s[0][u + kScaleThreads * i] = x[j][i] * w[j][0];
-                  if (GATED) sh.scale[s].s[1][u + kScaleThreads * i] = x[j][i] * w[j][1];
+            for (int j = 0; j < kScaleAhead; ++j) {
+              const int kb = min(kb0 + j, p.k_blocks - 1);
+              w[j][0] = wg[kb];
+              w[j][1] = GATED ? wu[kb] : 0.f;
+#pragma unroll
+              for (int i = 0; i < kScaleRows; ++i)
+                x[j][i] = u + kScaleThreads * i < tile.rows ? xs[(int64_t)kScaleThreads * i * p.k_blocks + kb] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < kScaleAhead; ++j) {
+              if (ok && kb0 + j < p.k_blocks) {
+                const uint32_t s = it % kScaleStages, ph = (it / kScaleStages) & 1;
+                ok = afd::mbar_wait(scale_empty + 8 * s, ph ^ 1, gave_up);
+                if (ok) {
+                  ++it;
+#pragma unroll
+                  for (int i = 0; i < kScaleRows; ++i) {
+                    sh.scale[s].s[0][u + kScaleThreads * i] = x[j][i] * w[j][0];
+                    if (GATED) sh.scale[s].s[1][u + kScaleThreads * i] = x[j][i] * w[j][1];
+                  }
+                  afd::mbar_arrive(scale_full + 8 * s);
                 }
-                afd::mbar_arrive(scale_full + 8 * s);
               }
             }
           }
         }
       }
     }
-  }
   } else {
     // ----------------------------------------------------------- accumulators
     if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
