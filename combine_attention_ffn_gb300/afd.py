@@ -105,7 +105,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "afd_route_topk": (i32, [v, i32, i64, v, v, i32, i32, i32, i32, i32, ctypes.c_float, v, v, v]),
         "afd_grouped_linear": (i32, [v, i64, v, v, v, v, i32, i32, i64, i32, i32, i32, i32, v, i64, v, v]),
         "afd_gated_rows": (i32, [v, i64, v, i32, i32, i64, i32, v, i64, v]),
-        "afd_adapter_add": (i32, [v, i64, v, i64, v, v, v, v, v, v, i32, i32, i64, i32, i32, i32, i32,
+        "afd_adapter_add": (i32, [v, i64, v, i64, v, v, v, v, v, v, v, i32, i32, i64, i32, i32, i32, i32,
                                   i32, v, i64, v, i64, v]),
         "afd_adapter_workspace_bytes": (i64, [i64, i32, i32]),
     }
@@ -587,20 +587,21 @@ def gated_rows(h: torch.Tensor, ends: torch.Tensor, *, expert_alignment: int = 1
 
 def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: torch.Tensor,
                 token_slots: torch.Tensor, scales: torch.Tensor, *, row_src: Optional[torch.Tensor] = None,
-                ends: Optional[torch.Tensor] = None, top_k: int = 1, out: Optional[torch.Tensor] = None,
-                stream=None) -> torch.Tensor:
+                ends: Optional[torch.Tensor] = None, top_k: int = 1, x_scale: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Low-rank adapters of many requests beside a shared projection, BF16:
     ``out[r] = base[r] + scales[a] * up[a] @ (down[a] @ x[r])`` with a =
     ``token_slots[row_src[r] // top_k]`` (received rows: `row_src`, `ends` and
     `top_k` of the exchange, token_slots over [A * bucket] tokens) or
     ``token_slots[r]`` (a source's own tokens). A slot outside [0, S) means no
-    adapter. `down` is [S, rank, K], `up` [S, N, rank]; `out` defaults to
-    `base` (in place). See afd_adapter_add in include/afd.h."""
+    adapter. `x` is bf16, or float8_e4m3fn with `x_scale` [R, K/128]; `down`
+    is [S, rank, K], `up` [S, N, rank]; `out` defaults to `base` (in place). See afd_adapter_add in include/afd.h."""
     if base.dim() != 2 or x.dim() != 2 or down.dim() != 3:
         raise AfdError(ERR_ARG, "base must be [R, N], x [R, K], down [S, rank, K] and up [S, N, rank]")
     (R, N), K, (S, rank, _) = base.shape, x.shape[1], down.shape
     base_stride = _want_rows(base, "base", torch.bfloat16, (R, N))
-    x_stride = _want_rows(x, "x", torch.bfloat16, (R, K))
+    x_stride = _want_rows(x, "x", torch.bfloat16 if x_scale is None else torch.float8_e4m3fn, (R, K))
+    xs_ptr = None if x_scale is None else _want(x_scale, "x_scale", torch.float32, (R, K // 128))
     down_ptr = _want(down, "down", torch.bfloat16, (S, rank, K))
     up_ptr = _want(up, "up", torch.bfloat16, (S, N, rank))
     scales_ptr = _want(scales, "scales", torch.float32, (S,))
@@ -622,7 +623,7 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
     size = (R + S + 5) // 4 * 16 + 4 * R * rank  # afd_adapter_workspace_bytes
     on = x.device if x.is_cuda else torch.device("cuda", _current_device())
     workspace = _empty(size, torch.uint8, on, stream)
-    _call("afd_adapter_add", workspace, stream, base.data_ptr(), base_stride, x.data_ptr(), x_stride, down_ptr, up_ptr,
+    _call("afd_adapter_add", workspace, stream, base.data_ptr(), base_stride, x.data_ptr(), x_stride, xs_ptr, down_ptr, up_ptr,
           slots_ptr, scales_ptr, src_ptr, ends_ptr, G, top_k, R, tokens, S, rank, K, N, out.data_ptr(), out_stride,
           workspace.data_ptr(), size)
     return out

@@ -2,6 +2,7 @@
 // (afd_gated_rows) and the low-rank adapters of many requests
 // (afd_adapter_add).
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -82,8 +83,9 @@ __global__ void __launch_bounds__(256) gated_rows_kernel(const GatedParams p) {
 struct AdapterParams {
   const uint16_t* base;
   int64_t base_stride;
-  const uint16_t* x;
-  int64_t x_stride;
+  const uint8_t* x;       // BF16, or E4M3 with x_scale
+  int64_t x_stride;       // bytes
+  const float* x_scale;   // [R][K / 128]
   const uint16_t* down;
   const uint16_t* up;
   const int32_t* token_slots;
@@ -293,30 +295,50 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, bool in) 
 
 // Operands of one 32-wide K chunk on their way: every thread copies exactly
 // what it uses itself, so no other thread has to be waited for.
-template <int RANK>
-struct DownStage {
-  uint4 x[2][32];            // rows g / g + 8
-  uint4 down[RANK / 8][32];  // rank rows 8 n + g
+template <bool FP8>
+struct DownRows;
+template <>
+struct DownRows<false> {
+  uint4 x[2][32];  // rows g / g + 8: eight values
+};
+template <>
+struct DownRows<true> {
+  uint2 x[2][32];
+  float scale[2][32];  // of the rows' block
 };
 
-template <int RANK>
+template <int RANK, bool FP8>
+struct alignas(16) DownStage : DownRows<FP8> {
+  alignas(16) uint4 down[RANK / 8][32];  // rank rows 8 n + g
+};
+
+template <int RANK, bool FP8>
 struct DownShared {
   static constexpr int kPad = RANK + 4;
   union {
-    DownStage<RANK> stage[kDownWarps][kDownStages];
+    DownStage<RANK, FP8> stage[kDownWarps][kDownStages];
     float part[kDownWarps][kDownRows][kPad];  // once the products are done
   };
 };
 
-template <int RANK>
+// Four E4M3 values as two pairs of BF16 (exact).
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  uint32_t a, b;
+  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}" : "=r"(a), "=r"(b) : "r"(v));
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  lo = afd::pack_bf16(x.x, x.y);
+  hi = afd::pack_bf16(y.x, y.y);
+}
+
+template <int RANK, bool FP8>
 __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const AdapterParams p) {
   extern __shared__ __align__(16) uint8_t ad_smem[];
-  DownShared<RANK>& sh = *reinterpret_cast<DownShared<RANK>*>(ad_smem);
+  DownShared<RANK, FP8>& sh = *reinterpret_cast<DownShared<RANK, FP8>*>(ad_smem);
   constexpr int NT = RANK / 8;             // 8-column tiles of the product
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tig = lane & 3;
   const int chunks = (p.K + 31) >> 5;
-  DownStage<RANK>* stage = sh.stage[warp];
+  DownStage<RANK, FP8>* stage = sh.stage[warp];
   const GroupTable groups = table_at(&sh + 1, p.S);
   afd::pdl_wait();
   afd::pdl_launch_dependents();
@@ -324,23 +346,30 @@ __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const Ada
   for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int a = tile_group(groups, p.S, t);
     const int at = groups.first[a] + (t - groups.first_tile[a]) * kDownRows, end = groups.first[a + 1];
-    const uint16_t* x[2];  // this thread's rows: g / g + 8
+    const uint8_t* x[2];  // this thread's rows: g / g + 8
+    const float* xs[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int i = at + 8 * h + g;
-      x[h] = i < end ? p.x + p.order[i] * p.x_stride : nullptr;
+      const int64_t r = i < end ? p.order[i] : -1;
+      x[h] = r >= 0 ? p.x + r * p.x_stride : nullptr;
+      xs[h] = FP8 && r >= 0 ? p.x_scale + r * (p.K / 128) : nullptr;
     }
     const uint16_t* down = p.down + ((int64_t)a * RANK + g) * p.K;
     auto fetch = [&](int i) {  // this warp's i-th chunk
       const int c = warp + i * kDownWarps;
       if (c < chunks) {
-        DownStage<RANK>& st = stage[i % kDownStages];
+        DownStage<RANK, FP8>& st = stage[i % kDownStages];
         const int k = c * 32 + tig * 8;
         const bool in = k < p.K;
 #pragma unroll
         for (int n = 0; n < NT; ++n) copy_async<16>(&st.down[n][lane], in ? down + (int64_t)n * 8 * p.K + k : p.down, in);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) copy_async<16>(&st.x[h][lane], in && x[h] ? x[h] + k : p.x, in && x[h]);
+        for (int h = 0; h < 2; ++h) {
+          const bool live = in && x[h];
+          copy_async<FP8 ? 8 : 16>(&st.x[h][lane], live ? x[h] + k * (FP8 ? 1 : 2) : p.x, live);
+          if constexpr (FP8) copy_async<4>(&st.scale[h][lane], live ? xs[h] + k / 128 : p.x_scale, live);
+        }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -354,13 +383,32 @@ __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const Ada
     for (int i = 0; warp + i * kDownWarps < chunks; ++i) {
       fetch(i + kDownStages - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kDownStages - 1) : "memory");
-      const DownStage<RANK>& st = stage[i % kDownStages];
-      const uint4 x0 = st.x[0][lane], x1 = st.x[1][lane];
+      const DownStage<RANK, FP8>& st = stage[i % kDownStages];
+      uint32_t x0[4], x1[4];
+      const auto v0 = st.x[0][lane], v1 = st.x[1][lane];
+      if constexpr (FP8) {
+        e4m3_to_bf16(v0.x, x0[0], x0[1]);
+        e4m3_to_bf16(v0.y, x0[2], x0[3]);
+        e4m3_to_bf16(v1.x, x1[0], x1[1]);
+        e4m3_to_bf16(v1.y, x1[2], x1[3]);
+      } else {
+        x0[0] = v0.x, x0[1] = v0.y, x0[2] = v0.z, x0[3] = v0.w;
+        x1[0] = v1.x, x1[1] = v1.y, x1[2] = v1.z, x1[3] = v1.w;
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint4 b = st.down[n][lane];
-        mma_16816(acc[n], x0.x, x1.x, x0.y, x1.y, b.x, b.y);
-        mma_16816(acc[n], x0.z, x1.z, x0.w, x1.w, b.z, b.w);
+        if constexpr (FP8) {
+          // a chunk lies in one block of 128: its product takes the rows' scales
+          float v[4] = {};
+          mma_16816(v, x0[0], x1[0], x0[1], x1[1], b.x, b.y);
+          mma_16816(v, x0[2], x1[2], x0[3], x1[3], b.z, b.w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[n][e] = fmaf(v[e], st.scale[e >> 1][lane], acc[n][e]);
+        } else {
+          mma_16816(acc[n], x0[0], x1[0], x0[1], x1[1], b.x, b.y);
+          mma_16816(acc[n], x0[2], x1[2], x0[3], x1[3], b.z, b.w);
+        }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -555,13 +603,13 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
   }
 }
 
-template <int RANK>
+template <int RANK, bool FP8>
 cudaError_t launch_adapters(const AdapterParams& p, int device, int sms, cudaStream_t stream) {
-  constexpr int kDownBase = sizeof(DownShared<RANK>), kUpBase = sizeof(UpShared<RANK>);
+  constexpr int kDownBase = sizeof(DownShared<RANK, FP8>), kUpBase = sizeof(UpShared<RANK>);
   static std::atomic<uint64_t> down_set{0}, up_set{0};
   cudaError_t e = afd::allow_shared(adapter_up_kernel<RANK>, kUpBase + (int)table_bytes(kMaxSlots), device, up_set);
   if (e == cudaSuccess)
-    e = afd::allow_shared(adapter_down_kernel<RANK>, kDownBase + (int)table_bytes(kMaxSlots), device, down_set);
+    e = afd::allow_shared(adapter_down_kernel<RANK, FP8>, kDownBase + (int)table_bytes(kMaxSlots), device, down_set);
   if (e != cudaSuccess) return e;
   const int down_smem = kDownBase + (int)table_bytes(p.S), up_smem = kUpBase + (int)table_bytes(p.S);
   const int down_fit = 227 * 1024 / (down_smem + 1024), up_fit = 227 * 1024 / (up_smem + 1024);  // blocks of an SM
@@ -572,9 +620,19 @@ cudaError_t launch_adapters(const AdapterParams& p, int device, int sms, cudaStr
   const int64_t down = (int64_t)p.R / kDownRows + (p.S < p.R ? p.S : p.R);
   const int64_t up = (p.R / kUpRows + (p.S < p.R ? p.S : p.R)) * (((int64_t)p.N + 31) / 32);
   const int64_t down_most = (int64_t)sms * (down_fit < 4 ? down_fit : 4), up_most = (int64_t)sms * (up_fit < 2 ? up_fit : 2);
-  e = afd::launch_dependent(adapter_down_kernel<RANK>, down < down_most ? down : down_most, kDownWarps * 32, down_smem, stream, p);
+  e = afd::launch_dependent(adapter_down_kernel<RANK, FP8>, down < down_most ? down : down_most, kDownWarps * 32, down_smem, stream, p);
   if (e != cudaSuccess) return e;
   return afd::launch_dependent(adapter_up_kernel<RANK>, up < up_most ? up : up_most, kUpThreads, up_smem, stream, p);
+}
+
+template <bool FP8>
+cudaError_t launch_adapters_rank(const AdapterParams& p, int device, int sms, cudaStream_t stream) {
+  switch (p.rank) {
+    case 8: return launch_adapters<8, FP8>(p, device, sms, stream);
+    case 16: return launch_adapters<16, FP8>(p, device, sms, stream);
+    case 32: return launch_adapters<32, FP8>(p, device, sms, stream);
+    default: return launch_adapters<64, FP8>(p, device, sms, stream);
+  }
 }
 
 // Bytes of the groups' starts and the order, up to a 16-byte boundary.
@@ -621,7 +679,7 @@ AFD_API int64_t afd_adapter_workspace_bytes(int64_t num_rows, int32_t num_slots,
 }
 
 AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const void* x, int64_t x_stride,
-                                   const void* down, const void* up, const int32_t* token_slots, const float* scales,
+                                   const float* x_scale, const void* down, const void* up, const int32_t* token_slots, const float* scales,
                                    const int32_t* row_src, const int32_t* ends, int32_t num_groups, int32_t top_k,
                                    int64_t num_rows, int32_t num_tokens, int32_t num_slots, int32_t rank,
                                    int32_t in_features, int32_t out_features, void* out, int64_t out_stride,
@@ -631,18 +689,19 @@ AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const 
   if (base_stride < out_features || out_stride < out_features || x_stride < in_features) return AFD_ERR_ARG;
   if (row_src ? (!ends || num_groups < 1 || top_k < 1) : num_tokens < num_rows) return AFD_ERR_ARG;
   if (rank != 8 && rank != 16 && rank != 32 && rank != 64) return AFD_ERR_UNSUPPORTED;
-  if (in_features % 16 || out_features % 8 || base_stride % 8 || out_stride % 8 || x_stride % 8 ||
+  const bool fp8 = x_scale != nullptr;
+  if (in_features % (fp8 ? 128 : 16) || out_features % 8 || base_stride % 8 || out_stride % 8 || x_stride % (fp8 ? 16 : 8) ||
       num_rows > INT32_MAX - 64 || num_slots > kMaxSlots)
     return AFD_ERR_UNSUPPORTED;
   if (num_rows == 0) return AFD_OK;
   if (!base || !x || !down || !up || !token_slots || !scales || !out || !workspace) return AFD_ERR_ARG;
   if (workspace_bytes < afd_adapter_workspace_bytes(num_rows, num_slots, rank)) return AFD_ERR_ARG;
   AdapterParams p = {};
-  p.base_stride = base_stride, p.x_stride = x_stride, p.out_stride = out_stride;
+  p.base_stride = base_stride, p.x_stride = x_stride * (fp8 ? 1 : 2), p.out_stride = out_stride;
   p.G = num_groups, p.top_k = top_k, p.R = (int32_t)num_rows, p.tokens = num_tokens, p.S = num_slots, p.rank = rank;
   p.K = in_features, p.N = out_features;
   if (!afd::device_view(static_cast<const uint16_t*>(base), &p.base) ||
-      !afd::device_view(static_cast<const uint16_t*>(x), &p.x) ||
+      !afd::device_view(static_cast<const uint8_t*>(x), &p.x) || (fp8 && !afd::device_view(x_scale, &p.x_scale)) ||
       !afd::device_view(static_cast<const uint16_t*>(down), &p.down) ||
       !afd::device_view(static_cast<const uint16_t*>(up), &p.up) || !afd::device_view(token_slots, &p.token_slots) ||
       !afd::device_view(scales, &p.scales) || !afd::device_view(static_cast<uint16_t*>(out), &p.out) ||
@@ -652,7 +711,7 @@ AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const 
   p.order = p.first + num_slots + 2;
   p.t_hi = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(p.first) + adapter_table_bytes(num_rows, num_slots));
   p.t_lo = p.t_hi + num_rows * rank;
-  if (!afd::aligned_to(p.first, 16) || !afd::aligned_to(p.token_slots, 4) || !afd::aligned_to(p.scales, 4) || !afd::aligned_to(p.row_src, 4) ||
+  if (!afd::aligned_to(p.first, 16) || !afd::aligned_to(p.token_slots, 4) || !afd::aligned_to(p.scales, 4) || !afd::aligned_to(p.x_scale, 4) || !afd::aligned_to(p.row_src, 4) ||
       !afd::aligned_to(p.ends, 4))
     return AFD_ERR_ARG;
   if (!afd::aligned_to(p.base, 16) || !afd::aligned_to(p.x, 16) || !afd::aligned_to(p.down, 16) ||
@@ -663,10 +722,7 @@ AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const 
   const int sms = sm_count(dev);
   if (sms < 1) return AFD_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = rank == 8    ? launch_adapters<8>(p, dev, sms, st)
-                        : rank == 16 ? launch_adapters<16>(p, dev, sms, st)
-                        : rank == 32 ? launch_adapters<32>(p, dev, sms, st)
-                                     : launch_adapters<64>(p, dev, sms, st);
+  const cudaError_t e = fp8 ? launch_adapters_rank<true>(p, dev, sms, st) : launch_adapters_rank<false>(p, dev, sms, st);
   return e == cudaSuccess ? AFD_OK : AFD_ERR_CUDA;
 }
 

@@ -498,7 +498,9 @@ AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t
  *   base, out    device BF16 [num_rows, out_features], row strides
  *                base_stride / out_stride; out may be base (in place), and must
  *                not overlap the inputs in any other way
- *   x            device BF16 [num_rows, in_features], row stride x_stride
+ *   x            device [num_rows, in_features], row stride x_stride elements:
+ *                BF16, or E4M3 with x_scale
+ *   x_scale      device FP32 [num_rows, in_features/128], or NULL (BF16)
  *   down         device BF16 [num_slots, rank, in_features], contiguous
  *   up           device BF16 [num_slots, out_features, rank], contiguous
  *   token_slots  device int32 [num_tokens]
@@ -510,11 +512,11 @@ AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t
  *                and mean nothing afterwards. Calls that may run at the same
  *                time (other streams, other captured graphs) need one each.
  * Limits: num_slots <= 1023; rank 8, 16, 32 or 64; in_features a multiple of
- * 16; out_features a multiple of 8; base, out, x, down, up and the strides multiples of 16
+ * 16 (E4M3: of 128); out_features a multiple of 8; base, out, x, down, up and the strides multiples of 16
  * bytes. Buffers may be device, managed or page-locked host memory.
  * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (limits), AFD_ERR_CUDA. */
 AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const void* x,
-                                   int64_t x_stride, const void* down, const void* up,
+                                   int64_t x_stride, const float* x_scale, const void* down, const void* up,
                                    const int32_t* token_slots, const float* scales,
                                    const int32_t* row_src, const int32_t* ends, int32_t num_groups,
                                    int32_t top_k, int64_t num_rows, int32_t num_tokens,

@@ -77,7 +77,7 @@ def test_gated_rows(lib, over, status):
 
 
 def _adapter(lib, **over):
-    a = dict(base=P, base_stride=64, x=P, x_stride=128, down=P, up=P, slots=P, scales=P, row_src=None, ends=None, G=0,
+    a = dict(base=P, base_stride=64, x=P, x_stride=128, x_scale=None, down=P, up=P, slots=P, scales=P, row_src=None, ends=None, G=0,
              top_k=1, R=8, tokens=8, S=2, rank=16, K=128, N=64, out=P, out_stride=64, ws=P, ws_bytes=48 + 2 * 8 * 16 * 2)
     a.update(over)
     return lib.afd_adapter_add(*a.values(), None)
@@ -90,7 +90,8 @@ def _adapter(lib, **over):
     (dict(row_src=P, ends=P, G=1, top_k=0), afd.ERR_ARG), (dict(base=None), afd.ERR_ARG), (dict(x=None), afd.ERR_ARG),
     (dict(down=None), afd.ERR_ARG), (dict(up=None), afd.ERR_ARG), (dict(slots=None), afd.ERR_ARG),
     (dict(scales=None), afd.ERR_ARG), (dict(out=None), afd.ERR_ARG), (dict(rank=24), afd.ERR_UNSUPPORTED),
-    (dict(rank=128), afd.ERR_UNSUPPORTED), (dict(K=120), afd.ERR_UNSUPPORTED),
+    (dict(rank=128), afd.ERR_UNSUPPORTED), (dict(K=120), afd.ERR_UNSUPPORTED), (dict(x_scale=P, K=64), afd.ERR_UNSUPPORTED),
+    (dict(x_scale=P, x_stride=136), afd.ERR_UNSUPPORTED),
     (dict(N=60, base_stride=60, out_stride=60), afd.ERR_UNSUPPORTED), (dict(base_stride=68), afd.ERR_UNSUPPORTED),
     (dict(S=1024, ws_bytes=1 << 20), afd.ERR_UNSUPPORTED), (dict(ws=None), afd.ERR_ARG), (dict(ws_bytes=48 + 511), afd.ERR_ARG),
     (dict(R=0, base=None, x=None, out=None, ws=None, ws_bytes=0), afd.OK)])
@@ -125,6 +126,10 @@ def test_binding_refuses_wrong_types_and_shapes(lib):
         lambda: pkg.grouped_linear(z(4, 64), z(2, 64, 64).transpose(1, 2), ends),
         lambda: pkg.gated_rows(z(4, 7), ends),
         lambda: pkg.gated_rows(z(4, 8), ends, out=z(4, 8)),
+        lambda: pkg.adapter_add(z(4, 64), z(4, 128).to(torch.float8_e4m3fn), z(2, 16, 128), z(2, 64, 16), z(4, dtype=torch.int32),
+                                z(2, dtype=torch.float32)),
+        lambda: pkg.adapter_add(z(4, 64), z(4, 128), z(2, 16, 128), z(2, 64, 16), z(4, dtype=torch.int32),
+                                z(2, dtype=torch.float32), x_scale=z(4, 1, dtype=torch.float32)),
         lambda: pkg.adapter_add(z(4, 64), z(4, 32), z(2, 16, 32), z(2, 64, 8), z(4, dtype=torch.int32), z(2, dtype=torch.float32)),
         lambda: pkg.adapter_add(z(4, 64), z(4, 32), z(2, 16, 32), z(2, 64, 16), z(3, dtype=torch.int32), z(2, dtype=torch.float32)),
         lambda: pkg.adapter_add(z(4, 64), z(4, 32), z(2, 16, 32), z(2, 64, 16), z(4, dtype=torch.int32), z(2, dtype=torch.float32),

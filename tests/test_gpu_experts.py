@@ -309,6 +309,23 @@ def test_adapters_of_own_tokens(R, K, N, rank):
     assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("rank", [8, 16, 32, 64])
+@pytest.mark.parametrize("R,K,N", [(1, 128, 8), (17, 2048, 264), (300, 1152, 512)])
+def test_adapters_of_fp8_rows(R, K, N, rank):
+    _, base, down, up, scales, slots = _adapter_case(R, K, N, rank, 5, R + rank, R)
+    q, qs = eh.quantise_rows(torch.randn(R, K, generator=_gen(R), device="cuda"))
+    x = q.double() * qs.double().repeat_interleave(128, 1)
+    dead = slots < 0
+    q.view(torch.uint8)[dead], qs[dead] = 0x7F, float("nan")  # rows without an adapter are not read
+    x[dead] = 0
+    want, err = _adapter_want(base, x, down, up, scales, slots.long())
+    wide = torch.zeros(R, 2 * K, dtype=torch.uint8, device="cuda").view(FP8)
+    wide[:, K:] = q
+    for rows in (q, wide[:, K:]):
+        out = lib.adapter_add(base, rows, down, up, slots, scales, x_scale=qs, out=torch.empty_like(base))
+        eh.check_bf16(out, want, err, torch.ones(R, dtype=torch.bool, device="cuda"))
+
+
 @pytest.mark.parametrize("run", [1, 40])
 @pytest.mark.parametrize("alpha", [1, 16])
 def test_adapters_of_received_rows(alpha, run):
@@ -545,8 +562,8 @@ def test_whole_expert_path(fp8, T):
             kw = dict(expert_alignment=alpha)
             h = lib.grouped_linear(r.rows, w13[mine], r.ends, x_scale=r.row_scales,
                                    weight_scale=None if s13 is None else s13[mine], **kw)
-            if not fp8:
-                lib.adapter_add(h, r.rows, down, up, slots, scales, row_src=r.row_src, ends=r.ends, top_k=K)
+            lib.adapter_add(h, r.rows, down, up, slots, scales, row_src=r.row_src, ends=r.ends, top_k=K,
+                            x_scale=r.row_scales)
             a = lib.gated_rows(h, r.ends, **kw)
             replies.append(lib.grouped_linear(a, w2[mine], r.ends, **kw))
             buf.worker_reply(f, replies[f], r.receipt)
@@ -566,7 +583,7 @@ def test_whole_expert_path(fp8, T):
                 for k in range(K):
                     e = int(ids[t, k])
                     h = w13v[e] @ xv[s][t]
-                    if a >= 0 and not fp8:
+                    if a >= 0:
                         h = h + scales[a].double() * (up[a].double() @ (down[a].double() @ xv[s][t]))
                     gt, u = h.chunk(2)
                     act = eh.silu(gt) * u
