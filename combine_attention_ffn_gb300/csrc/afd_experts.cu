@@ -27,7 +27,7 @@
 //
 // What bounds it, measured (16.4 K rows of 64 experts, K 2048, 2 x 1024 weight
 // rows, gated, BF16: 116 us, 5.5 TB/s of DRAM traffic): the reads through L2,
-// 1.35 GB at 11.6 TB/s, about as fast as the box moves them; a decode step
+// 1.35 GB at 11.6 TB/s, about as fast as they go on this GPU; a decode step
 // (one token a source) streams the touched experts' weights at 5.4 TB/s in
 // 14 us. One lane alone in the loops of the loading and issuing warps, as a
 // first form had it, took 100 clocks an issue and 150 us.
