@@ -107,7 +107,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "afd_gated_rows": (i32, [v, i64, v, i32, i32, i64, i32, v, i64, v]),
         "afd_adapter_add": (i32, [v, i64, v, i64, v, v, v, v, v, v, v, i32, i32, i64, i32, i32, i32, i32,
                                   i32, v, i64, v, i64, v]),
-        "afd_adapter_workspace_bytes": (i64, [i64, i32, i32]),
+        "afd_adapter_workspace_bytes": (i64, [i64, i32, i32, i32, i32, i32, i32]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -620,10 +620,12 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
         out, out_stride = base, base_stride
     else:
         out_stride = _want_rows(out, "out", torch.bfloat16, (R, N))
-    size = (R + S + 5) // 4 * 16 + 4 * R * rank  # afd_adapter_workspace_bytes
-    on = x.device if x.is_cuda else torch.device("cuda", _current_device())
-    workspace = _empty(size, torch.uint8, on, stream)
-    _call("afd_adapter_add", workspace, stream, base.data_ptr(), base_stride, x.data_ptr(), x_stride, xs_ptr, down_ptr, up_ptr,
+    size = (_lib or load_library()).afd_adapter_workspace_bytes(R, tokens, top_k if G else 0, S, rank, K, N)
+    workspace = None
+    if size > 0:
+        on = x.device if x.is_cuda else torch.device("cuda", _current_device())
+        workspace = _empty(size, torch.uint8, on, stream)
+    _call("afd_adapter_add", x, stream, base.data_ptr(), base_stride, x.data_ptr(), x_stride, xs_ptr, down_ptr, up_ptr,
           slots_ptr, scales_ptr, src_ptr, ends_ptr, G, top_k, R, tokens, S, rank, K, N, out.data_ptr(), out_stride,
-          workspace.data_ptr(), size)
+          None if workspace is None else workspace.data_ptr(), size)
     return out

@@ -46,21 +46,31 @@ inline bool device_view(T* p, T** out) {
 
 // Launches a kernel as a programmatic dependent of the work before it on the
 // stream: its blocks may start while that work still runs, and the kernel
-// waits (pdl_wait) before it touches memory.
+// waits (pdl_wait) before it touches memory. `cluster`: blocks of a cluster,
+// where the kernel leaves that to the launch.
 template <typename... Params, typename... Args>
-inline cudaError_t launch_dependent(void (*kernel)(Params...), int64_t grid, int block, size_t smem, cudaStream_t stream,
-                                    Args&&... args) {
-  cudaLaunchAttribute attr[1];
+inline cudaError_t launch_clusters(void (*kernel)(Params...), int64_t grid, int block, int cluster, size_t smem,
+                                   cudaStream_t stream, Args&&... args) {
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+}
+
+template <typename... Params, typename... Args>
+inline cudaError_t launch_dependent(void (*kernel)(Params...), int64_t grid, int block, size_t smem, cudaStream_t stream,
+                                    Args&&... args) {
+  return launch_clusters(kernel, grid, block, 0, smem, stream, static_cast<Args&&>(args)...);
 }
 
 // Whether p is on an `align`-byte boundary.

@@ -100,8 +100,179 @@ struct AdapterParams {
   uint16_t *t_hi, *t_lo;  // workspace: scale * down[a] x of each of them, [R][rank]
 };
 
-// Low-rank adapters, in three launches that follow each other by programmatic
-// dependent launch.
+// The group of a row: its adapter, S for none, -1 for what is not a row.
+__device__ __forceinline__ int row_group(const AdapterParams& p, int r) {
+  int t = r;
+  if (p.row_src) {
+    const int src = p.row_src[r];
+    if (src < 0) return -1;
+    t = src / p.top_k;
+  }
+  if (t >= p.tokens) return -1;
+  const int a = p.token_slots[t];
+  return a >= 0 && a < p.S ? a : p.S;
+}
+
+// Four E4M3 values as two pairs of BF16 (exact).
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  uint32_t a, b;
+  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}" : "=r"(a), "=r"(b) : "r"(v));
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  lo = afd::pack_bf16(x.x, x.y);
+  hi = afd::pack_bf16(y.x, y.y);
+}
+
+// The generic address of this shared address in another CTA of the cluster.
+template <typename T>
+__device__ __forceinline__ T* remote(T* p, uint32_t rank) {
+  uint64_t a;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(p), "r"(rank));
+  return reinterpret_cast<T*>(a);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Low-rank adapters of few rows (a decode step): a cluster of `ctas` blocks per
+// row, in one launch and without a workspace. The blocks share the K columns of
+// the rank's dot products and leave each other their parts, then share the
+// columns of the result; a lane reads 16 bytes of an adapter at a time, next to
+// its neighbour's. With few rows a call is a chain of latencies (2.9 us for one
+// row of 2048 columns, rank 16; 9.7 us by the three launches below), with many
+// every row reads its adapter from L2 again. Blocks of a cluster, 2048 columns,
+// rank 16: with 16 rows 8 take 3.1 us, 4 3.3, 2 4.1 and 1 6.0; with 64 rows 6.8,
+// 4.1, 4.3 and 6.2; with 128 11.0, 6.8, 5.5 and 6.2; with 512 38, 20, 12.4 and
+// 13.7. So 8 up to 32 rows, 4 up to 64 and 2 beyond.
+// Rows are dealt to the clusters one by one, as the live ones of a padded layout
+// sit next to each other, and to an odd number of clusters, as groups start at
+// multiples of a power of two (152 clusters: 13.6 us, 151: 11.1). A cluster
+// looks 32 of its rows up at a time.
+constexpr int kRowCtas = 8, kRowThreads = 256;
+
+template <int RANK, bool FP8>
+__global__ void __launch_bounds__(kRowThreads, RANK <= 16 ? 3 : 2) adapter_rows_kernel(const AdapterParams p, const int ctas) {
+  __shared__ float part[2][kRowCtas][RANK];
+  __shared__ __align__(16) float low[RANK];
+  constexpr int JW = RANK / 8;                          // dot products of a warp
+  constexpr int L = RANK / 8;                           // lanes of a column's up row
+  constexpr int COLS = kRowThreads / L;                 // columns a block takes in one go
+  constexpr int U = 4;                                  // times it, loaded together
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int cta = blockIdx.x % ctas;
+  const int64_t cluster = blockIdx.x / ctas, clusters = gridDim.x / ctas;
+  cluster_sync();  // the others have started: their shared memory may be written
+  afd::pdl_wait();
+  afd::pdl_launch_dependents();
+  const int limit = p.row_src ? afd::group_end(p.ends[p.G - 1], p.R) : p.R;
+  const bool in_place = p.out == p.base && p.out_stride == p.base_stride;
+  int turn = 0;
+  for (int64_t i0 = cluster; i0 < limit; i0 += 32 * clusters) {
+    const int64_t mine = i0 + (int64_t)lane * clusters;
+    const int group = mine < limit ? row_group(p, (int)mine) : -1;
+    unsigned todo = __ballot_sync(0xffffffffu, group >= 0 && !(group == p.S && in_place));
+    for (; todo; todo &= todo - 1) {
+      const int which = __ffs(todo) - 1;
+      const int64_t r = i0 + (int64_t)which * clusters;
+      const int a = __shfl_sync(0xffffffffu, group, which);
+      const uint16_t* base = p.base + r * p.base_stride;
+      uint16_t* out = p.out + r * p.out_stride;
+      if (a == p.S) {  // no adapter
+        for (int c = (cta * kRowThreads + threadIdx.x) * 8; c < p.N; c += ctas * kRowThreads * 8)
+          *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(base + c);
+        continue;
+      }
+      const uint8_t* x = p.x + r * p.x_stride;
+      const uint16_t* down = p.down + (int64_t)a * RANK * p.K;
+      const uint16_t* up = p.up + (int64_t)a * p.N * RANK + threadIdx.x % L * 8;
+      // The first columns' operands are on their way while the dot products run.
+      const int c0 = cta * COLS + threadIdx.x / L;
+      uint4 uv[U];
+      uint16_t bv[U];
+      auto fetch = [&](int c) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int col = c + u * ctas * COLS;
+          uv[u] = col < p.N ? __ldg(reinterpret_cast<const uint4*>(up + (int64_t)col * RANK)) : make_uint4(0, 0, 0, 0);
+          bv[u] = col < p.N ? base[col] : 0;
+        }
+      };
+      fetch(c0);
+      float sum[JW] = {};
+#pragma unroll 1
+      for (int k = (cta * 32 + lane) * 8; k < p.K; k += ctas * 32 * 8) {
+        uint4 xv, dv[JW];
+        float xs = 1.f;
+        if (FP8) {
+          const uint2 q = *reinterpret_cast<const uint2*>(x + k);
+          e4m3_to_bf16(q.x, xv.x, xv.y);
+          e4m3_to_bf16(q.y, xv.z, xv.w);
+          xs = p.x_scale[r * (p.K / 128) + k / 128];
+        } else {
+          xv = *reinterpret_cast<const uint4*>(x + 2 * k);
+        }
+#pragma unroll
+        for (int j = 0; j < JW; ++j)
+          dv[j] = __ldg(reinterpret_cast<const uint4*>(down + (int64_t)(warp + 8 * j) * p.K + k));
+        float xf[8];
+        afd::bf16x8_to_float(xv, xf);
+        if (FP8)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) xf[e] *= xs;
+#pragma unroll
+        for (int j = 0; j < JW; ++j) {
+          float df[8];
+          afd::bf16x8_to_float(dv[j], df);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[j] = fmaf(xf[e], df[e], sum[j]);
+        }
+      }
+      const float scale = p.scales[a];
+#pragma unroll
+      for (int j = 0; j < JW; ++j) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+        if (lane < ctas) *remote(&part[turn][cta][warp + 8 * j], lane) = sum[j];
+      }
+      cluster_sync();
+      if (threadIdx.x < RANK) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRowCtas; ++i)
+          if (i < ctas) t += part[turn][i][threadIdx.x];
+        low[threadIdx.x] = t * scale;
+      }
+      // The other half of `part` is written next; this one again only after the
+      // cluster's next barrier, which comes after these reads.
+      turn ^= 1;
+      __syncthreads();
+      float t[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = low[threadIdx.x % L * 8 + e];
+      for (int c = c0;;) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int col = c + u * ctas * COLS;
+          float f[8], add = 0.f;
+          afd::bf16x8_to_float(uv[u], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) add = fmaf(t[e], f[e], add);
+#pragma unroll
+          for (int d = 1; d < L; d <<= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
+          if (threadIdx.x % L == 0 && col < p.N)
+            out[col] = (uint16_t)afd::pack_bf16(__uint_as_float((uint32_t)bv[u] << 16) + add, 0.f);
+        }
+        c += U * ctas * COLS;
+        if (c - threadIdx.x / L >= p.N) break;  // (the same for the whole block)
+        fetch(c);
+      }
+    }
+  }
+  cluster_sync();  // nobody leaves while its shared memory may be written
+}
+
+// Low-rank adapters of many rows, in three launches that follow each other by
+// programmatic dependent launch.
 //   group: the live rows sorted by adapter (a request's rows are spread over
 //          every expert's range, so rows that follow one another mostly differ
 //          in theirs), and where each adapter starts; rows without one last.
@@ -123,6 +294,8 @@ struct AdapterParams {
 // Measured with 16.4 K rows, K = N = 2048, rank 32, eight adapters, two rows in
 // three with one: 50 us (8 + 20 + 17 and the launches) against a floor of 27;
 // without the grouping, 64 neighbouring rows at a time, 192 us.
+constexpr int kFewRows = 512;
+constexpr int64_t kFewRowsBytes = (int64_t)64 << 20;
 constexpr int kMaxSlots = 1023;    // and the rows without one: a thread of the grouping each
 constexpr int kGroupCtas = 8;
 constexpr int kGroupThreads = 1024;
@@ -133,30 +306,6 @@ constexpr int kDownStages = 3;     // K chunks of a warp in flight
 constexpr int kUpRows = 64;        // rows of a tile: 16 for each of four warps
 constexpr int kUpThreads = 256;
 constexpr int kUpStages = 4;       // column groups whose operands are in flight
-
-// The group of a row: its adapter, S for none, -1 for what is not a row.
-__device__ __forceinline__ int row_group(const AdapterParams& p, int r) {
-  int t = r;
-  if (p.row_src) {
-    const int src = p.row_src[r];
-    if (src < 0) return -1;
-    t = src / p.top_k;
-  }
-  if (t >= p.tokens) return -1;
-  const int a = p.token_slots[t];
-  return a >= 0 && a < p.S ? a : p.S;
-}
-
-// The generic address of this shared address in another CTA of the cluster.
-__device__ __forceinline__ const int* remote(const int* p, uint32_t rank) {
-  uint64_t a;
-  asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(p), "r"(rank));
-  return reinterpret_cast<const int*>(a);
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // One cluster: counts per group and CTA, their prefix, then every row's place.
 // Inside a group the order is that of the atomics; no result depends on it.
@@ -320,15 +469,6 @@ struct DownShared {
     float part[kDownWarps][kDownRows][kPad];  // once the products are done
   };
 };
-
-// Four E4M3 values as two pairs of BF16 (exact).
-__device__ __forceinline__ void e4m3_to_bf16(uint32_t v, uint32_t& lo, uint32_t& hi) {
-  uint32_t a, b;
-  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}" : "=r"(a), "=r"(b) : "r"(v));
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  lo = afd::pack_bf16(x.x, x.y);
-  hi = afd::pack_bf16(y.x, y.y);
-}
 
 template <int RANK, bool FP8>
 __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const AdapterParams p) {
@@ -625,18 +765,53 @@ cudaError_t launch_adapters(const AdapterParams& p, int device, int sms, cudaStr
   return afd::launch_dependent(adapter_up_kernel<RANK>, up < up_most ? up : up_most, kUpThreads, up_smem, stream, p);
 }
 
+// Whether a cluster per row does; `rows` is the most rows that can be live. The
+// row kernel reads rows * rank * (K + N) * 2 bytes of adapters from L2. The three
+// launches read far less, but a tile's rank * K * 2 bytes by one block, at about
+// a 64th of the rate of all. Rank 16, K = N = 2048: 128 rows (16 MiB) 5.5 against
+// 10.5 us, 256 (32) 8.9 against 10.8, 512 (64) 12.4 against 11.8, padded to 128
+// rows a group 10.7 against 11.1; rank 64: 128 rows (64 of 80) 9.6 against 14.7,
+// 256 (128) 17.6 against 15.4. K = 7168, rank 16: 128 rows (36 of 78) 8.6 against
+// 13.8, 512 (144) 21.6 against 15.1; rank 64: 64 rows (72 of 120) 10.0 against
+// 24.6, 256 (288) 29.6 against 25.4. Rank 8 stops at 512 rows: 9.3 against 11.3
+// (32 MiB), where 256 took 6.8. One launch in place of three and no workspace
+// also take 12 us less of the caller's time.
+bool few_rows(int64_t rows, int32_t rank, int32_t in_features, int32_t out_features) {
+  const int64_t k = (int64_t)rank * in_features * 2, n = (int64_t)rank * out_features * 2;
+  return rows <= kFewRows && rows * (k + n) <= kFewRowsBytes + 64 * k;
+}
+
+int64_t live_rows_bound(int64_t num_rows, int32_t num_tokens, int32_t top_k) {
+  const int64_t routes = (int64_t)num_tokens * top_k;  // (top_k 0: rows are tokens)
+  return top_k > 0 && routes < num_rows ? routes : num_rows;
+}
+
+// `few`: the most rows that can be live, where a cluster per row does; else 0.
+template <int RANK, bool FP8>
+cudaError_t launch_adapters_of(const AdapterParams& p, int few, int device, int sms, cudaStream_t stream) {
+  if (!few) return launch_adapters<RANK, FP8>(p, device, sms, stream);
+  const int ctas = few <= 32 ? 8 : few <= 64 ? 4 : 2;
+  const int64_t most = (sms * (RANK <= 16 ? 3 : 2) / ctas - 1) | 1;
+  return afd::launch_clusters(adapter_rows_kernel<RANK, FP8>, (p.R < most ? p.R : most) * ctas, kRowThreads, ctas, 0,
+                              stream, p, ctas);
+}
+
 template <bool FP8>
-cudaError_t launch_adapters_rank(const AdapterParams& p, int device, int sms, cudaStream_t stream) {
+cudaError_t launch_adapters_rank(const AdapterParams& p, int few, int device, int sms, cudaStream_t stream) {
   switch (p.rank) {
-    case 8: return launch_adapters<8, FP8>(p, device, sms, stream);
-    case 16: return launch_adapters<16, FP8>(p, device, sms, stream);
-    case 32: return launch_adapters<32, FP8>(p, device, sms, stream);
-    default: return launch_adapters<64, FP8>(p, device, sms, stream);
+    case 8: return launch_adapters_of<8, FP8>(p, few, device, sms, stream);
+    case 16: return launch_adapters_of<16, FP8>(p, few, device, sms, stream);
+    case 32: return launch_adapters_of<32, FP8>(p, few, device, sms, stream);
+    default: return launch_adapters_of<64, FP8>(p, few, device, sms, stream);
   }
 }
 
 // Bytes of the groups' starts and the order, up to a 16-byte boundary.
 int64_t adapter_table_bytes(int64_t rows, int32_t slots) { return (rows + slots + 2 + 3) / 4 * 16; }
+
+int64_t adapter_workspace(int64_t rows, int32_t slots, int32_t rank) {
+  return adapter_table_bytes(rows, slots) + 2 * rows * rank * (int64_t)sizeof(uint16_t);
+}
 
 int sm_count(int device) {
   int n = 0;
@@ -673,9 +848,12 @@ AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t
   return e == cudaSuccess ? AFD_OK : AFD_ERR_CUDA;
 }
 
-AFD_API int64_t afd_adapter_workspace_bytes(int64_t num_rows, int32_t num_slots, int32_t rank) {
-  if (num_rows < 0 || num_slots < 1 || rank < 1) return -1;
-  return adapter_table_bytes(num_rows, num_slots) + 2 * num_rows * rank * (int64_t)sizeof(uint16_t);
+AFD_API int64_t afd_adapter_workspace_bytes(int64_t num_rows, int32_t num_tokens, int32_t top_k, int32_t num_slots,
+                                            int32_t rank, int32_t in_features, int32_t out_features) {
+  if (num_rows < 0 || num_tokens < 0 || top_k < 0 || num_slots < 1 || rank < 1 || in_features < 1 || out_features < 1)
+    return -1;
+  if (few_rows(live_rows_bound(num_rows, num_tokens, top_k), rank, in_features, out_features)) return 0;
+  return adapter_workspace(num_rows, num_slots, rank);
 }
 
 AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const void* x, int64_t x_stride,
@@ -693,9 +871,11 @@ AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const 
   if (in_features % (fp8 ? 128 : 16) || out_features % 8 || base_stride % 8 || out_stride % 8 || x_stride % (fp8 ? 16 : 8) ||
       num_rows > INT32_MAX - 64 || num_slots > kMaxSlots)
     return AFD_ERR_UNSUPPORTED;
-  if (num_rows == 0) return AFD_OK;
-  if (!base || !x || !down || !up || !token_slots || !scales || !out || !workspace) return AFD_ERR_ARG;
-  if (workspace_bytes < afd_adapter_workspace_bytes(num_rows, num_slots, rank)) return AFD_ERR_ARG;
+  if (num_rows == 0 || num_tokens == 0) return AFD_OK;
+  if (!base || !x || !down || !up || !token_slots || !scales || !out) return AFD_ERR_ARG;
+  const int64_t live = live_rows_bound(num_rows, num_tokens, row_src ? top_k : 0);
+  const bool few = few_rows(live, rank, in_features, out_features);
+  if (!few && (!workspace || workspace_bytes < adapter_workspace(num_rows, num_slots, rank))) return AFD_ERR_ARG;
   AdapterParams p = {};
   p.base_stride = base_stride, p.x_stride = x_stride * (fp8 ? 1 : 2), p.out_stride = out_stride;
   p.G = num_groups, p.top_k = top_k, p.R = (int32_t)num_rows, p.tokens = num_tokens, p.S = num_slots, p.rank = rank;
@@ -705,14 +885,16 @@ AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const 
       !afd::device_view(static_cast<const uint16_t*>(down), &p.down) ||
       !afd::device_view(static_cast<const uint16_t*>(up), &p.up) || !afd::device_view(token_slots, &p.token_slots) ||
       !afd::device_view(scales, &p.scales) || !afd::device_view(static_cast<uint16_t*>(out), &p.out) ||
-      !afd::device_view(static_cast<int32_t*>(workspace), &p.first) ||
+      (!few && !afd::device_view(static_cast<int32_t*>(workspace), &p.first)) ||
       (row_src && (!afd::device_view(row_src, &p.row_src) || !afd::device_view(ends, &p.ends))))
     return AFD_ERR_ARG;
-  p.order = p.first + num_slots + 2;
-  p.t_hi = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(p.first) + adapter_table_bytes(num_rows, num_slots));
-  p.t_lo = p.t_hi + num_rows * rank;
-  if (!afd::aligned_to(p.first, 16) || !afd::aligned_to(p.token_slots, 4) || !afd::aligned_to(p.scales, 4) || !afd::aligned_to(p.x_scale, 4) || !afd::aligned_to(p.row_src, 4) ||
-      !afd::aligned_to(p.ends, 4))
+  if (!few) {
+    p.order = p.first + num_slots + 2;
+    p.t_hi = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(p.first) + adapter_table_bytes(num_rows, num_slots));
+    p.t_lo = p.t_hi + num_rows * rank;
+  }
+  if (!afd::aligned_to(p.first, 16) || !afd::aligned_to(p.token_slots, 4) || !afd::aligned_to(p.scales, 4) ||
+      !afd::aligned_to(p.x_scale, 4) || !afd::aligned_to(p.row_src, 4) || !afd::aligned_to(p.ends, 4))
     return AFD_ERR_ARG;
   if (!afd::aligned_to(p.base, 16) || !afd::aligned_to(p.x, 16) || !afd::aligned_to(p.down, 16) ||
       !afd::aligned_to(p.up, 16) || !afd::aligned_to(p.out, 16))
@@ -722,7 +904,8 @@ AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const 
   const int sms = sm_count(dev);
   if (sms < 1) return AFD_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = fp8 ? launch_adapters_rank<true>(p, dev, sms, st) : launch_adapters_rank<false>(p, dev, sms, st);
+  const int rows = few ? (int)live : 0;
+  const cudaError_t e = fp8 ? launch_adapters_rank<true>(p, rows, dev, sms, st) : launch_adapters_rank<false>(p, rows, dev, sms, st);
   return e == cudaSuccess ? AFD_OK : AFD_ERR_CUDA;
 }
 

@@ -507,25 +507,30 @@ AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t
  *   scales       device FP32 [num_slots]
  *   row_src      device int32 [num_rows] with ends, or NULL (then num_tokens
  *                >= num_rows, and ends may be NULL)
- *   workspace    device, at least afd_adapter_workspace_bytes(num_rows,
- *                num_slots, rank) bytes, 16-byte aligned; its contents need not be set
- *                and mean nothing afterwards. Calls that may run at the same
- *                time (other streams, other captured graphs) need one each.
+ *   workspace    device, workspace_bytes >= afd_adapter_workspace_bytes(...)
+ *                bytes, 16-byte aligned (NULL where that is 0); its contents
+ *                need not be set and mean nothing afterwards. Calls that may
+ *                run at the same time (other streams, other captured graphs)
+ *                need one each.
  * Limits: num_slots <= 1023; rank 8, 16, 32 or 64; in_features a multiple of
- * 16 (E4M3: of 128); out_features a multiple of 8; base, out, x, down, up and the strides multiples of 16
- * bytes. Buffers may be device, managed or page-locked host memory.
+ * 16 (E4M3: of 128); out_features a multiple of 8; base, out, x, down, up and
+ * the strides multiples of 16 bytes. Buffers may be device, managed or page-locked host memory.
  * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (limits), AFD_ERR_CUDA. */
 AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const void* x,
-                                   int64_t x_stride, const float* x_scale, const void* down, const void* up,
-                                   const int32_t* token_slots, const float* scales,
-                                   const int32_t* row_src, const int32_t* ends, int32_t num_groups,
-                                   int32_t top_k, int64_t num_rows, int32_t num_tokens,
+                                   int64_t x_stride, const float* x_scale, const void* down,
+                                   const void* up, const int32_t* token_slots,
+                                   const float* scales, const int32_t* row_src,
+                                   const int32_t* ends, int32_t num_groups, int32_t top_k,
+                                   int64_t num_rows, int32_t num_tokens,
                                    int32_t num_slots, int32_t rank, int32_t in_features,
                                    int32_t out_features, void* out, int64_t out_stride,
                                    void* workspace, int64_t workspace_bytes, afd_stream stream);
 
-/* Bytes of workspace for afd_adapter_add with these sizes (-1 for sizes it refuses). */
-AFD_API int64_t afd_adapter_workspace_bytes(int64_t num_rows, int32_t num_slots, int32_t rank);
+/* Bytes of workspace for afd_adapter_add with these sizes (-1 for negative
+ * ones; 0 where few rows can be live). top_k: 0 for calls without row_src. */
+AFD_API int64_t afd_adapter_workspace_bytes(int64_t num_rows, int32_t num_tokens, int32_t top_k,
+                                            int32_t num_slots, int32_t rank, int32_t in_features,
+                                            int32_t out_features);
 
 /* Library version, (major << 16) | minor. */
 AFD_API int32_t afd_version(void);

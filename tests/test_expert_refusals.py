@@ -78,7 +78,7 @@ def test_gated_rows(lib, over, status):
 
 def _adapter(lib, **over):
     a = dict(base=P, base_stride=64, x=P, x_stride=128, x_scale=None, down=P, up=P, slots=P, scales=P, row_src=None, ends=None, G=0,
-             top_k=1, R=8, tokens=8, S=2, rank=16, K=128, N=64, out=P, out_stride=64, ws=P, ws_bytes=48 + 2 * 8 * 16 * 2)
+             top_k=1, R=8, tokens=8, S=2, rank=16, K=128, N=64, out=P, out_stride=64, ws=None, ws_bytes=0)
     a.update(over)
     return lib.afd_adapter_add(*a.values(), None)
 
@@ -93,16 +93,28 @@ def _adapter(lib, **over):
     (dict(rank=128), afd.ERR_UNSUPPORTED), (dict(K=120), afd.ERR_UNSUPPORTED), (dict(x_scale=P, K=64), afd.ERR_UNSUPPORTED),
     (dict(x_scale=P, x_stride=136), afd.ERR_UNSUPPORTED),
     (dict(N=60, base_stride=60, out_stride=60), afd.ERR_UNSUPPORTED), (dict(base_stride=68), afd.ERR_UNSUPPORTED),
-    (dict(S=1024, ws_bytes=1 << 20), afd.ERR_UNSUPPORTED), (dict(ws=None), afd.ERR_ARG), (dict(ws_bytes=48 + 511), afd.ERR_ARG),
+    (dict(S=1024, ws_bytes=1 << 20), afd.ERR_UNSUPPORTED), (dict(R=1 << 20, tokens=1 << 20, ws=None, ws_bytes=1 << 40), afd.ERR_ARG),
+    (dict(R=1 << 20, tokens=1 << 20, ws=P, ws_bytes=1 << 26), afd.ERR_ARG),
     (dict(R=0, base=None, x=None, out=None, ws=None, ws_bytes=0), afd.OK)])
 def test_adapters(lib, over, status):
     assert _adapter(lib, **over) == status
 
 
 def test_adapter_workspace(lib):
-    for R, S, rank in ((0, 1, 8), (1, 1, 8), (2, 1, 16), (7, 3, 32), (100_000, 1024, 64), (1 << 28, 5, 64)):
-        assert lib.afd_adapter_workspace_bytes(R, S, rank) == (R + S + 2 + 3) // 4 * 16 + 4 * R * rank
-    assert lib.afd_adapter_workspace_bytes(-1, 1, 8) == lib.afd_adapter_workspace_bytes(1, 0, 8) == -1
+    size = lib.afd_adapter_workspace_bytes
+    for R, S, rank in ((100_000, 1023, 64), (1 << 28, 5, 64), (65_536, 3, 32)):
+        assert size(R, R, 0, S, rank, 2048, 2048) == (R + S + 2 + 3) // 4 * 16 + 4 * R * rank
+        assert size(R, 65, 8, S, rank, 2048, 2048) == size(R, R, 0, S, rank, 2048, 2048)
+        assert size(R, 16, 8, S, rank, 2048, 2048) == 0  # few rows can be live
+    for rows, rank, K, N, few in ((512, 8, 16, 8, True), (513, 8, 16, 8, False), (512, 16, 2048, 2048, True),
+                                  (512, 16, 2048, 2560, False), (160, 64, 2048, 2048, True),
+                                  (161, 64, 2048, 2048, False), (64, 64, 7168, 2048, True),
+                                  (128, 64, 7168, 2048, False), (1, 64, 16, 2 ** 31 - 8, False)):
+        assert (size(rows, rows, 0, 4, rank, K, N) == 0) == few
+    assert size(0, 0, 0, 1, 8, 16, 8) == 0
+    for bad in ((-1, 0, 0, 1, 8, 16, 8), (1, -1, 0, 1, 8, 16, 8), (1, 1, -1, 1, 8, 16, 8), (1, 1, 0, 0, 8, 16, 8),
+                (1, 1, 0, 1, 0, 16, 8), (1, 1, 0, 1, 8, 0, 8), (1, 1, 0, 1, 8, 16, 0)):
+        assert size(*bad) == -1
 
 
 def test_binding_refuses_wrong_types_and_shapes(lib):

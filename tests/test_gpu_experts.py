@@ -295,7 +295,8 @@ def _adapter_want(base, x, down, up, scales, slot):
 
 
 @pytest.mark.parametrize("rank", [8, 16, 32, 64])
-@pytest.mark.parametrize("R,K,N", [(1, 16, 8), (2, 256, 24), (17, 2048, 264), (33, 48, 1000), (300, 1040, 512)])
+@pytest.mark.parametrize("R,K,N", [(1, 16, 8), (2, 256, 24), (17, 2048, 264), (33, 48, 1000), (300, 1040, 512),
+                                   (513, 16, 8), (600, 2048, 264), (700, 1040, 1000)])  # (from 513 on not a row at a time)
 def test_adapters_of_own_tokens(R, K, N, rank):
     x, base, down, up, scales, slots = _adapter_case(R, K, N, rank, 5, R + rank, R)
     want, err = _adapter_want(base, x, down, up, scales, slots.long())
@@ -310,7 +311,7 @@ def test_adapters_of_own_tokens(R, K, N, rank):
 
 
 @pytest.mark.parametrize("rank", [8, 16, 32, 64])
-@pytest.mark.parametrize("R,K,N", [(1, 128, 8), (17, 2048, 264), (300, 1152, 512)])
+@pytest.mark.parametrize("R,K,N", [(1, 128, 8), (17, 2048, 264), (300, 1152, 512), (513, 128, 8), (700, 2048, 264)])
 def test_adapters_of_fp8_rows(R, K, N, rank):
     _, base, down, up, scales, slots = _adapter_case(R, K, N, rank, 5, R + rank, R)
     q, qs = eh.quantise_rows(torch.randn(R, K, generator=_gen(R), device="cuda"))
@@ -328,11 +329,12 @@ def test_adapters_of_fp8_rows(R, K, N, rank):
 
 @pytest.mark.parametrize("run", [1, 40])
 @pytest.mark.parametrize("alpha", [1, 16])
-def test_adapters_of_received_rows(alpha, run):
+@pytest.mark.parametrize("counts", [(30, 0, 1, 70, 5, 16), (300, 0, 1, 270, 5, 16)])
+def test_adapters_of_received_rows(counts, alpha, run):
     """Rows in an exchange's order: padding (row_src -1), a row_src that names
     no token, and rows behind the last end stay as they were."""
-    K, N, rank, S, top_k, tokens = 128, 136, 16, 6, 3, 70
-    ends, R, spans = eh.ragged([30, 0, 1, 70, 5, 16], alpha, 9)
+    K, N, rank, S, top_k, tokens = 128, 136, 16, 6, 3, sum(counts) // 2 + 9
+    ends, R, spans = eh.ragged(list(counts), alpha, 9)
     x, base, down, up, scales, _ = _adapter_case(R, K, N, rank, S, 4, tokens)
     slots = (torch.arange(tokens, device="cuda") // run * 7 % (S + 2) - 1).int()
     live = eh.live_rows(R, spans, "cuda")
@@ -352,8 +354,35 @@ def test_adapters_of_received_rows(alpha, run):
     assert (out[~live] == 7.0).all()
 
 
-def test_adapters_strided_and_captured():
-    R, K, N, rank, S = 90, 256, 128, 32, 3
+@pytest.mark.parametrize("rank", [8, 64])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("tokens", [1, 4, 8, 60])
+def test_adapters_few_rows_of_a_long_layout(tokens, in_place, rank):
+    """A decode step in a padded layout: few live rows, far apart."""
+    K, N, S, top_k, groups, alpha = 144, 264, 3, 8, 300, 128
+    g = _gen(tokens + rank)
+    routes = torch.randint(0, groups, (tokens * top_k,), generator=g, device="cuda").sort().values
+    counts = torch.bincount(routes, minlength=groups).tolist()
+    ends, R, spans = eh.ragged(counts, alpha, 9)
+    x, base, down, up, scales, slots = _adapter_case(R, K, N, rank, S, 4, tokens)
+    live = eh.live_rows(R, spans, "cuda")
+    src = torch.full((R,), -1, dtype=torch.int32, device="cuda")
+    src[live] = torch.randperm(tokens * top_k, generator=g, device="cuda").int()
+    x[~live] = float("nan")
+    slot = slots[src.long().clamp_min(0) // top_k].long()
+    slot[~live] = -1
+    want, err = _adapter_want(base, x, down, up, scales, slot)
+    before = base.clone()
+    out = base if in_place else torch.full_like(base, 7.0)
+    lib.adapter_add(base, x, down, up, slots, scales, row_src=src, top_k=top_k, out=out,
+                    ends=torch.tensor(ends, dtype=torch.int32, device="cuda"))
+    eh.check_bf16(out, want, err, live)
+    assert torch.equal(out[~live], before[~live]) if in_place else (out[~live] == 7.0).all()
+
+
+@pytest.mark.parametrize("R", [90, 690])
+def test_adapters_strided_and_captured(R):
+    K, N, rank, S = 256, 128, 32, 3
     x, base, down, up, scales, slots = _adapter_case(R, K, N, rank, S, 6, R)
     want = lib.adapter_add(base, x, down, up, slots, scales, out=torch.empty_like(base))
     xw = torch.full((R, 3 * K), float("nan"), dtype=BF16, device="cuda")
@@ -393,9 +422,10 @@ def test_adapters_many_rows():
     eh.check_bf16(out, want, err, torch.ones(R, dtype=torch.bool, device="cuda"))
 
 
-def test_adapters_keep_requests_apart():
+@pytest.mark.parametrize("R", [70, 670])
+def test_adapters_keep_requests_apart(R):
     """An adapter full of infinities and NaN reaches its own rows only; so do rows of NaN."""
-    R, K, N, rank, S = 70, 64, 40, 16, 4
+    K, N, rank, S = 64, 40, 16, 4
     x, base, down, up, scales, _ = _adapter_case(R, K, N, rank, S, 8, R)
     slots = (torch.arange(R, device="cuda") % 4).int()
     clean = lib.adapter_add(base, x, down, up, slots, scales, out=torch.empty_like(base))
@@ -408,8 +438,9 @@ def test_adapters_keep_requests_apart():
     assert not torch.isfinite(out[own]).any()
 
 
-def test_adapters_two_streams_at_once():
-    R, K, N, rank, S = 500, 512, 256, 32, 6
+@pytest.mark.parametrize("R", [500, 1500])
+def test_adapters_two_streams_at_once(R):
+    K, N, rank, S = 512, 256, 32, 6
     a, b = (_adapter_case(R, K, N, rank, S, seed, R) for seed in (1, 2))
     call = lambda c, **kw: lib.adapter_add(c[1], c[0], c[2], c[3], c[5], c[4], out=torch.empty_like(c[1]), **kw)
     want = [call(a), call(b)]
@@ -698,12 +729,13 @@ def test_row_operators_take_pinned_host_buffers():
     h = torch.randn(5, 64, generator=_gen(2), device="cuda").to(BF16)
     act, pact = lib.gated_rows(h, ends), torch.zeros(5, 32, dtype=BF16).pin_memory()
     lib.gated_rows(pin(h), pin(ends), out=pact)
-    case = _adapter_case(20, 64, 40, 16, 3, 3, 20)
-    x, base, down, up, scales, slots = case
-    want = lib.adapter_add(base, x, down, up, slots, scales, out=torch.empty_like(base))
-    px, pbase, pdown, pup, pscales, pslots = (pin(t) for t in case)
-    lib.adapter_add(pbase, px, pdown, pup, pslots, pscales)
-    torch.cuda.synchronize()
+    for R in (20, 520):
+        case = _adapter_case(R, 64, 40, 16, 3, 3, R)
+        x, base, down, up, scales, slots = case
+        want = lib.adapter_add(base, x, down, up, slots, scales, out=torch.empty_like(base))
+        px, pbase, pdown, pup, pscales, pslots = (pin(t) for t in case)
+        lib.adapter_add(pbase, px, pdown, pup, pslots, pscales)
+        torch.cuda.synchronize()
+        assert torch.equal(pbase, want.cpu())
     assert torch.equal(pids, ids.cpu()) and torch.equal(pw, w.cpu())
     assert torch.equal(pact, act.cpu())
-    assert torch.equal(pbase, want.cpu())
