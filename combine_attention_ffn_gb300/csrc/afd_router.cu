@@ -6,14 +6,17 @@
 // index among its holders with a second one, so k rounds cost 2k warp
 // reductions and no shared memory. The work is a few KB per token: a decode
 // step is bound by the launch, a prefill bucket by the latency of one warp's
-// rounds, which is why tokens take a warp each and not a block: 2.5 us for one
-// token of 128 experts, 8 us for 2,048.
+// rounds, which is why tokens take a warp each and not a block: 2.4 us for one
+// token of 128 experts, 3.4 us for 2,048, with a bias 3.6 and 4.8 to 6.9.
 //
 // Softmax and sigmoid are monotone, so without a bias the logits themselves
 // are the keys, exactly. With a bias the keys score + bias are computed in
 // FP32 first; where neighbouring keys lie closer together than those sums'
 // error, the experts in question are put in order by 64-bit keys, one a lane
-// (rare: gaps are of the order of 1e-2, the error of 1e-5).
+// (rare: gaps are of the order of 1e-2, the error of 1e-6; the one token of a
+// bucket that needs it adds 2 us with sigmoid scores and 4 with softmax). The
+// rounds leave that question to a look at all slots after the last one (asked
+// in every round, 2,048 tokens took 8 us).
 
 #include <cuda_runtime.h>
 #include <float.h>
@@ -64,10 +67,12 @@ __device__ __forceinline__ double warp_sum(double v) {
 }
 
 // The largest FP32 distance at which two computed keys may be out of order:
-// twice the error of a score (exp, the sum, the quotient: below 2^-18
-// relative for 1,024 experts) plus that of the two additions.
-__device__ __forceinline__ float key_slack(float pa, float pb, float ka, float kb) {
-  return 1.6e-5f * fmaxf(pa, pb) + 2.4e-7f * fmaxf(fabsf(ka), fabsf(kb));
+// twice the error of a score plus that of the two additions (2^-23 of the larger
+// key, taken twice). Softmax (exp, the sum of up to 1,024, the quotient): below
+// 2^-17 relative. Sigmoid: exp 2^-22 and two roundings, below 2^-21 even where
+// the score is subnormal.
+__device__ __forceinline__ float key_slack(bool sigmoid, float pa, float pb, float ka, float kb) {
+  return (sigmoid ? 1.5e-6f : 1.6e-5f) * fmaxf(pa, pb) + 2.4e-7f * fmaxf(fabsf(ka), fabsf(kb));
 }
 
 // Selection with keys in 64 bits, for more than 32 keys that lie close
@@ -195,20 +200,13 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_topk_kernel(const Rou
       const float k = p.bias ? score_of(l[j]) + p.bias[lane + 32 * j] : l[j];
       key[j] = order_image(k);
     }
-    // Without a bias, K rounds. With one, the rounds go on while the last two
-    // keys are too close to tell: all experts that may belong to the first K
-    // are then in the lanes' slots.
-    float last_key = 0.f, last_logit = 0.f, last_bias = 0.f, last_score = 0.f;
-    bool close = false;
-    float logit = 0.f;  // lane k: the logit of slot k
-    int found = 0;
-    for (;; ++found) {
-      if (!p.bias && found == p.K) break;
+    // A round: the expert with the largest key, which it loses, and its logit.
+    auto pick = [&](int* expert, float* value) {
       uint32_t best = 0;
 #pragma unroll
       for (int j = 0; j < PER; ++j) best = max(best, key[j]);
       best = __reduce_max_sync(kFull, best);
-      if (best == 0) break;
+      if (best == 0) return best;
       uint32_t at = 0xffffffffu;
 #pragma unroll
       for (int j = PER - 1; j >= 0; --j)
@@ -218,24 +216,52 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_topk_kernel(const Rou
 #pragma unroll
       for (int j = 0; j < PER; ++j)
         if ((int)at == lane + 32 * j) v = l[j], key[j] = 0;
-      v = __shfl_sync(kFull, v, at & 31);
-      if (p.bias) {
-        const float kv = from_image(best), b = p.bias[at], s = score_of(v);
-        bool near = false;
-        if (found > 0)
-          near = !(v == last_logit && b == last_bias) && !(last_key - kv > key_slack(last_score, s, last_key, kv));
-        if (found >= p.K && !near) break;
-        close |= near;
-        if (found == 32) break;
-        last_key = kv, last_logit = v, last_bias = b, last_score = s;
-      }
-      if (lane == found) mine = (int)at, logit = v;
+      *expert = (int)at;
+      *value = __shfl_sync(kFull, v, at & 31);
+      return best;
+    };
+    float logit = 0.f, kept = 0.f;  // lane k: the logit and the key of slot k
+    int found = 0;
+    for (; found < p.K; ++found) {
+      int at;
+      float v;
+      const uint32_t best = pick(&at, &v);
+      if (best == 0) break;
+      if (lane == found) mine = at, logit = v, kept = from_image(best);
     }
-    if (close) {
-      if (found <= 31)
-        order_exact<PER>(l, p, top, lane, found, &mine, &logit);
-      else
+    if (p.bias) {
+      // Lane k looks whether its key is too close to the one before to tell (a
+      // score is at most 1, which spares most tokens its second reckoning).
+      auto near = [&](float va, int ea, float ka, float vb, int eb, float kb) {
+        if (ka - kb > key_slack(p.sigmoid, 1.f, 1.f, ka, kb)) return false;
+        if (va == vb && p.bias[ea] == p.bias[eb]) return false;
+        return !(ka - kb > key_slack(p.sigmoid, score_of(va), score_of(vb), ka, kb));
+      };
+      const float va = __shfl_up_sync(kFull, logit, 1), ka = __shfl_up_sync(kFull, kept, 1);
+      const int ea = __shfl_up_sync(kFull, mine, 1);
+      bool close = __any_sync(kFull, lane > 0 && lane < found && near(va, ea, ka, logit, mine, kept));
+      // The rounds go on while the last two keys are too close: all experts that
+      // may belong to the first K are then in the lanes' slots.
+      bool over = false;
+      while (found >= p.K) {
+        int at;
+        float v;
+        const uint32_t best = pick(&at, &v);
+        if (best == 0) break;
+        const float k = from_image(best);
+        if (!near(__shfl_sync(kFull, logit, found - 1), __shfl_sync(kFull, mine, found - 1),
+                  __shfl_sync(kFull, kept, found - 1), v, at, k))
+          break;
+        close = true;
+        over = found == 32;
+        if (over) break;
+        if (lane == found) mine = at, logit = v, kept = k;
+        ++found;
+      }
+      if (over)
         select_exact<PER>(l, p, top, lane, &mine, &logit);
+      else if (close)
+        order_exact<PER>(l, p, top, lane, found, &mine, &logit);
     }
     if (lane >= p.K) mine = -1;
     if (p.renormalize) {
