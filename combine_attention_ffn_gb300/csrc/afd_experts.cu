@@ -707,7 +707,8 @@ extern "C" AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride
   if (x_stride < K || out_stride < N || !weight || !ends || fp8 != (weight_scale != nullptr)) return AFD_ERR_ARG;
   if (num_rows > 0 && (!x || !out || fp8 != (x_scale != nullptr))) return AFD_ERR_ARG;
   const int elt = fp8 ? 1 : 2;
-  if (num_groups > afd::kMaxExperts || num_rows > INT32_MAX - (int64_t)expert_alignment || N > (1 << 24) || K > (1 << 24))
+  if (num_groups > afd::kMaxExperts || num_rows > afd::kMaxRows - expert_alignment || N > afd::kMaxFeatures ||
+      K > afd::kMaxFeatures)
     return AFD_ERR_UNSUPPORTED;
   if (K * elt % 16 || x_stride * elt % 16 || (fp8 && (K % 128 || N % 128))) return AFD_ERR_UNSUPPORTED;
   // the most tiles there can be, counted in 32 bits by the kernel

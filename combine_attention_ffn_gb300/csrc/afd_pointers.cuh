@@ -73,6 +73,11 @@ inline cudaError_t launch_dependent(void (*kernel)(Params...), int64_t grid, int
   return launch_clusters(kernel, grid, block, 0, smem, stream, static_cast<Args&&>(args)...);
 }
 
+// Sizes that leave a step of any loop over rows or columns, and a tile's
+// rounding up, below 2^31.
+constexpr int64_t kMaxRows = INT32_MAX - (1 << 20);
+constexpr int32_t kMaxFeatures = 1 << 24;
+
 // Whether p is on an `align`-byte boundary.
 inline bool aligned_to(const void* p, uintptr_t align) { return (reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0; }
 

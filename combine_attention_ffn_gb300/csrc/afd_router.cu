@@ -305,7 +305,7 @@ extern "C" AFD_API afd_status afd_route_topk(const void* logits, int32_t logits_
   if (logits_dtype != AFD_BF16 && logits_dtype != AFD_FP32) return AFD_ERR_ARG;
   if (scoring != AFD_SCORE_SOFTMAX && scoring != AFD_SCORE_SIGMOID) return AFD_ERR_ARG;
   if (renormalize != 0 && renormalize != 1) return AFD_ERR_ARG;
-  if (E > 1024) return AFD_ERR_UNSUPPORTED;
+  if (E > 1024 || T > afd::kMaxRows) return AFD_ERR_UNSUPPORTED;
   if (T == 0) return AFD_OK;
   RouterParams p = {logits, row_stride, bias, live_tokens, T, E, K, scoring == AFD_SCORE_SIGMOID, renormalize,
                     scale, ids, weights};

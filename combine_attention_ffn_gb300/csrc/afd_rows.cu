@@ -827,7 +827,8 @@ AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t
                                   int64_t out_stride, afd_stream stream) {
   if (num_groups < 1 || expert_alignment < 1 || num_rows < 0 || features < 1 || !ends) return AFD_ERR_ARG;
   if (h_stride < 2 * (int64_t)features || out_stride < features) return AFD_ERR_ARG;
-  if (num_groups > afd::kMaxExperts || num_rows > INT32_MAX - (int64_t)expert_alignment) return AFD_ERR_UNSUPPORTED;
+  if (num_groups > afd::kMaxExperts || num_rows > afd::kMaxRows - expert_alignment || features > afd::kMaxFeatures)
+    return AFD_ERR_UNSUPPORTED;
   if (num_rows == 0) return AFD_OK;
   if (!h || !out) return AFD_ERR_ARG;
   GatedParams p = {nullptr, h_stride, nullptr, num_groups, expert_alignment, (int32_t)num_rows, features, nullptr, out_stride};
@@ -869,7 +870,8 @@ AFD_API afd_status afd_adapter_add(const void* base, int64_t base_stride, const 
   if (rank != 8 && rank != 16 && rank != 32 && rank != 64) return AFD_ERR_UNSUPPORTED;
   const bool fp8 = x_scale != nullptr;
   if (in_features % (fp8 ? 128 : 16) || out_features % 8 || base_stride % 8 || out_stride % 8 || x_stride % (fp8 ? 16 : 8) ||
-      num_rows > INT32_MAX - 64 || num_slots > kMaxSlots)
+      num_rows > afd::kMaxRows || num_slots > kMaxSlots || in_features > afd::kMaxFeatures ||
+      out_features > afd::kMaxFeatures)
     return AFD_ERR_UNSUPPORTED;
   if (num_rows == 0 || num_tokens == 0) return AFD_OK;
   if (!base || !x || !down || !up || !token_slots || !scales || !out) return AFD_ERR_ARG;

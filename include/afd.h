@@ -395,7 +395,8 @@ AFD_API afd_status afd_route_layout_noalloc(const int64_t* ids, int32_t num_toke
  * any number of captured graphs, as long as their buffers do not overlap.
  * Work is enqueued on `stream`, a stream of the current device, on which
  * every buffer must be reachable (a buffer of another device returns
- * AFD_ERR_ARG and enqueues nothing). */
+ * AFD_ERR_ARG and enqueues nothing). They take at most 2^31 - 2^20 - 1 rows
+ * or tokens (less expert_alignment where there is one) and 2^24 features. */
 
 /* How afd_route_topk scores an expert. */
 enum { AFD_SCORE_SOFTMAX = 0, AFD_SCORE_SIGMOID = 1 };
@@ -423,7 +424,8 @@ enum { AFD_SCORE_SOFTMAX = 0, AFD_SCORE_SIGMOID = 1 };
  *   ids, weights device int64 / FP32 [num_tokens, top_k] out
  * Limits: top_k <= min(32, num_experts), num_experts <= 1024.
  * Buffers may be device, managed or page-locked host memory.
- * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (num_experts), AFD_ERR_CUDA. */
+ * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (num_experts, num_tokens),
+ * AFD_ERR_CUDA. */
 AFD_API afd_status afd_route_topk(const void* logits, int32_t logits_dtype, int64_t row_stride,
                                   const float* bias, const int32_t* live_tokens, int32_t num_tokens,
                                   int32_t num_experts, int32_t top_k, int32_t scoring,
@@ -458,8 +460,8 @@ AFD_API afd_status afd_route_topk(const void* logits, int32_t logits_dtype, int6
  * Buffers are device memory of the current device (the rows and weights move
  * by bulk copies). x, weight, x_stride and the rows of weight are multiples
  * of 16 bytes; FP8 takes in_features and out_features that are multiples of
- * 128. num_groups <= 1024, in_features and out_features <= 2^24, and at most
- * 2^30 tiles of 256 weight rows by 256 rows.
+ * 128. num_groups <= 1024, and at most 2^30 tiles of 256 weight rows by 256
+ * rows.
  * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (sizes or alignments above),
  * AFD_ERR_CUDA. */
 AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride, const float* x_scale,
@@ -479,7 +481,8 @@ AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride, const flo
  *   out  device BF16 [num_rows, features], row r at out + r * out_stride; may
  *        be the first half of h itself
  * Buffers may be device, managed or page-locked host memory.
- * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (num_groups > 1024), AFD_ERR_CUDA. */
+ * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (num_groups > 1024, sizes),
+ * AFD_ERR_CUDA. */
 AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t* ends,
                                   int32_t num_groups, int32_t expert_alignment, int64_t num_rows,
                                   int32_t features, void* out, int64_t out_stride,

@@ -30,6 +30,7 @@ def _route(lib, **over):
     (dict(E=0, K=1), afd.ERR_ARG), (dict(stride=63), afd.ERR_ARG), (dict(logits=None), afd.ERR_ARG),
     (dict(ids=None), afd.ERR_ARG), (dict(weights=None), afd.ERR_ARG), (dict(dtype=afd.FP8_E4M3), afd.ERR_ARG),
     (dict(scoring=2), afd.ERR_ARG), (dict(renorm=2), afd.ERR_ARG), (dict(E=1025, stride=1025), afd.ERR_UNSUPPORTED),
+    (dict(T=(1 << 31) - (1 << 20)), afd.ERR_UNSUPPORTED),
     (dict(T=0, logits=None, ids=None, weights=None), afd.OK)])
 def test_router(lib, over, status):
     assert _route(lib, **over) == status
@@ -48,7 +49,7 @@ def _grouped(lib, **over):
     (dict(x_stride=255), afd.ERR_ARG), (dict(out_stride=127), afd.ERR_ARG), (dict(x=None), afd.ERR_ARG),
     (dict(w=None), afd.ERR_ARG), (dict(ends=None), afd.ERR_ARG), (dict(out=None), afd.ERR_ARG),
     (dict(x_scale=P), afd.ERR_ARG), (dict(w_scale=P), afd.ERR_ARG), (dict(dtype=afd.FP8_E4M3), afd.ERR_ARG),
-    (dict(G=1025), afd.ERR_UNSUPPORTED), (dict(R=(1 << 31) - 1), afd.ERR_UNSUPPORTED),
+    (dict(G=1025), afd.ERR_UNSUPPORTED), (dict(R=(1 << 31) - (1 << 20) - 1), afd.ERR_UNSUPPORTED),
     (dict(alpha=(1 << 31) - 1), afd.ERR_UNSUPPORTED), (dict(K=252), afd.ERR_UNSUPPORTED),
     (dict(x_stride=260), afd.ERR_UNSUPPORTED),
     (dict(dtype=afd.FP8_E4M3, x_scale=P, w_scale=P, K=192), afd.ERR_UNSUPPORTED),
@@ -71,7 +72,9 @@ def _gated(lib, **over):
     (dict(G=0), afd.ERR_ARG), (dict(alpha=0), afd.ERR_ARG), (dict(R=-1), afd.ERR_ARG), (dict(N=0), afd.ERR_ARG),
     (dict(ends=None), afd.ERR_ARG), (dict(h=None), afd.ERR_ARG), (dict(out=None), afd.ERR_ARG),
     (dict(h_stride=63), afd.ERR_ARG), (dict(out_stride=31), afd.ERR_ARG), (dict(G=1025), afd.ERR_UNSUPPORTED),
-    (dict(R=(1 << 31) - 1), afd.ERR_UNSUPPORTED), (dict(R=0, h=None, out=None), afd.OK)])
+    (dict(R=(1 << 31) - (1 << 20) - 1), afd.ERR_UNSUPPORTED), (dict(alpha=(1 << 31) - 1), afd.ERR_UNSUPPORTED),
+    (dict(N=(1 << 24) + 1, h_stride=1 << 26, out_stride=1 << 25), afd.ERR_UNSUPPORTED),
+    (dict(R=0, h=None, out=None), afd.OK)])
 def test_gated_rows(lib, over, status):
     assert _gated(lib, **over) == status
 
@@ -93,6 +96,9 @@ def _adapter(lib, **over):
     (dict(rank=128), afd.ERR_UNSUPPORTED), (dict(K=120), afd.ERR_UNSUPPORTED), (dict(x_scale=P, K=64), afd.ERR_UNSUPPORTED),
     (dict(x_scale=P, x_stride=136), afd.ERR_UNSUPPORTED),
     (dict(N=60, base_stride=60, out_stride=60), afd.ERR_UNSUPPORTED), (dict(base_stride=68), afd.ERR_UNSUPPORTED),
+    (dict(R=(1 << 31) - (1 << 20), tokens=(1 << 31) - 1), afd.ERR_UNSUPPORTED),
+    (dict(N=(1 << 24) + 8, base_stride=1 << 25, out_stride=1 << 25), afd.ERR_UNSUPPORTED),
+    (dict(K=(1 << 24) + 16, x_stride=1 << 25), afd.ERR_UNSUPPORTED),
     (dict(S=1024, ws_bytes=1 << 20), afd.ERR_UNSUPPORTED), (dict(R=1 << 20, tokens=1 << 20, ws=None, ws_bytes=1 << 40), afd.ERR_ARG),
     (dict(R=1 << 20, tokens=1 << 20, ws=P, ws_bytes=1 << 26), afd.ERR_ARG),
     (dict(R=0, base=None, x=None, out=None, ws=None, ws_bytes=0), afd.OK)])
