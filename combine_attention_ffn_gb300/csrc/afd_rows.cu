@@ -302,10 +302,14 @@ constexpr int kGroupThreads = 1024;
 constexpr int kGroupKeep = 4;      // rows of a thread whose group it remembers
 constexpr int kDownRows = 16;      // rows of a block
 constexpr int kDownWarps = 8;      // ... whose warps share K
-constexpr int kDownStages = 3;     // K chunks of a warp in flight
 constexpr int kUpRows = 64;        // rows of a tile: 16 for each of four warps
 constexpr int kUpThreads = 256;
-constexpr int kUpStages = 4;       // column groups whose operands are in flight
+// K chunks of a warp in flight, and column groups. At rank 64 so few that two
+// blocks share an SM (2,048 tokens a source: 71 us, with 3 and 4 stages and one
+// block 85); at rank 32 three and four blocks with 3 and 4 take 50.5 us, with 2
+// and 2 52.4, with 4 and 4 53.
+constexpr int down_stages(int rank) { return rank <= 32 ? 3 : 2; }
+constexpr int up_stages(int rank) { return rank <= 32 ? 4 : 2; }
 
 // One cluster: counts per group and CTA, their prefix, then every row's place.
 // Inside a group the order is that of the atomics; no result depends on it.
@@ -465,7 +469,7 @@ template <int RANK, bool FP8>
 struct DownShared {
   static constexpr int kPad = RANK + 4;
   union {
-    DownStage<RANK, FP8> stage[kDownWarps][kDownStages];
+    DownStage<RANK, FP8> stage[kDownWarps][down_stages(RANK)];
     float part[kDownWarps][kDownRows][kPad];  // once the products are done
   };
 };
@@ -475,6 +479,7 @@ __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const Ada
   extern __shared__ __align__(16) uint8_t ad_smem[];
   DownShared<RANK, FP8>& sh = *reinterpret_cast<DownShared<RANK, FP8>*>(ad_smem);
   constexpr int NT = RANK / 8;             // 8-column tiles of the product
+  constexpr int kStages = down_stages(RANK);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tig = lane & 3;
   const int chunks = (p.K + 31) >> 5;
@@ -499,7 +504,7 @@ __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const Ada
     auto fetch = [&](int i) {  // this warp's i-th chunk
       const int c = warp + i * kDownWarps;
       if (c < chunks) {
-        DownStage<RANK, FP8>& st = stage[i % kDownStages];
+        DownStage<RANK, FP8>& st = stage[i % kStages];
         const int k = c * 32 + tig * 8;
         const bool in = k < p.K;
 #pragma unroll
@@ -514,16 +519,16 @@ __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const Ada
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < kDownStages - 1; ++i) fetch(i);
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
     float acc[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
     for (int i = 0; warp + i * kDownWarps < chunks; ++i) {
-      fetch(i + kDownStages - 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kDownStages - 1) : "memory");
-      const DownStage<RANK, FP8>& st = stage[i % kDownStages];
+      fetch(i + kStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      const DownStage<RANK, FP8>& st = stage[i % kStages];
       uint32_t x0[4], x1[4];
       const auto v0 = st.x[0][lane], v1 = st.x[1][lane];
       if constexpr (FP8) {
@@ -626,15 +631,16 @@ struct UpStage {
 
 template <int RANK>
 struct UpShared {
-  alignas(16) UpStage<RANK> stage[kUpThreads / 32][kUpStages];
+  alignas(16) UpStage<RANK> stage[kUpThreads / 32][up_stages(RANK)];
 };
 
 template <int RANK>
-__global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_kernel(const AdapterParams p) {
+__global__ void __launch_bounds__(kUpThreads, 2) adapter_up_kernel(const AdapterParams p) {
   extern __shared__ __align__(16) uint8_t ad_smem[];
   UpShared<RANK>& sh = *reinterpret_cast<UpShared<RANK>*>(ad_smem);
   constexpr int EL = UpStage<RANK>::EL, CH = UpStage<RANK>::CH;
   constexpr int STEPS = EL == 8 ? 2 : 1;              // products per chunk
+  constexpr int kStages = up_stages(RANK);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tig = lane & 3;
   const int col_groups = (p.N + 31) >> 5, slots = gridDim.x * (kUpThreads / 32);
@@ -672,7 +678,7 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
     const uint16_t* up = p.up + ((int64_t)a * p.N + col) * RANK + tig * EL;
     auto fetch = [&](int gi) {
       if (gi < g1) {
-        UpStage<RANK>& st = stage[gi % kUpStages];
+        UpStage<RANK>& st = stage[gi % kStages];
         const int n0 = gi * 32;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -690,7 +696,7 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < kUpStages - 1; ++i) fetch(g0 + i);
+    for (int i = 0; i < kStages - 1; ++i) fetch(g0 + i);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -700,9 +706,9 @@ __global__ void __launch_bounds__(kUpThreads, RANK <= 32 ? 2 : 1) adapter_up_ker
         load_rank<EL>(p.t_lo + o, live[h], tl[h][q]);
       }
     for (int gi = g0; gi < g1; ++gi) {
-      fetch(gi + kUpStages - 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kUpStages - 1) : "memory");
-      const UpStage<RANK>& st = stage[gi % kUpStages];
+      fetch(gi + kStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      const UpStage<RANK>& st = stage[gi % kStages];
       const int n0 = gi * 32;
       uint4 bv[2] = {st.base[0][lane], st.base[1][lane]};
       float acc[4][4];  // [column tile]
@@ -770,10 +776,10 @@ cudaError_t launch_adapters(const AdapterParams& p, int device, int sms, cudaStr
 // launches read far less, but a tile's rank * K * 2 bytes by one block, at about
 // a 64th of the rate of all. Rank 16, K = N = 2048: 128 rows (16 MiB) 5.5 against
 // 10.5 us, 256 (32) 8.9 against 10.8, 512 (64) 12.4 against 11.8, padded to 128
-// rows a group 10.7 against 11.1; rank 64: 128 rows (64 of 80) 9.6 against 14.7,
-// 256 (128) 17.6 against 15.4. K = 7168, rank 16: 128 rows (36 of 78) 8.6 against
+// rows a group 10.7 against 11.1; rank 64: 128 rows (64 of 80) 9.6 against 14.2,
+// 256 (128) 17.6 against 14.7. K = 7168, rank 16: 128 rows (36 of 78) 8.6 against
 // 13.8, 512 (144) 21.6 against 15.1; rank 64: 64 rows (72 of 120) 10.0 against
-// 24.6, 256 (288) 29.6 against 25.4. Rank 8 stops at 512 rows: 9.3 against 11.3
+// 21.5, 256 (288) 29.6 against 22.7. Rank 8 stops at 512 rows: 9.3 against 11.3
 // (32 MiB), where 256 took 6.8. One launch in place of three and no workspace
 // also take 12 us less of the caller's time.
 bool few_rows(int64_t rows, int32_t rank, int32_t in_features, int32_t out_features) {
