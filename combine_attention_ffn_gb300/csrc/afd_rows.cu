@@ -101,16 +101,14 @@ struct AdapterParams {
 };
 
 // The group of a row: its adapter, S for none, -1 for what is not a row.
-__device__ __forceinline__ int row_group(const AdapterParams& p, int r) {
-  int t = r;
-  if (p.row_src) {
-    const int src = p.row_src[r];
-    if (src < 0) return -1;
-    t = src / p.top_k;
-  }
-  if (t >= p.tokens) return -1;
+__device__ __forceinline__ int token_group(const AdapterParams& p, int src) {
+  const int t = src < 0 ? -1 : p.row_src ? src / p.top_k : src;
+  if (t < 0 || t >= p.tokens) return -1;
   const int a = p.token_slots[t];
   return a >= 0 && a < p.S ? a : p.S;
+}
+__device__ __forceinline__ int row_group(const AdapterParams& p, int r) {
+  return token_group(p, p.row_src ? p.row_src[r] : r);
 }
 
 // Four E4M3 values as two pairs of BF16 (exact).
@@ -292,7 +290,7 @@ __global__ void __launch_bounds__(kRowThreads, RANK <= 16 ? 3 : 2) adapter_rows_
 // adapter holds reaches a result.
 // t is FP32; between the two it is kept as two BF16 (16 bits and more).
 // Measured with 16.4 K rows, K = N = 2048, rank 32, eight adapters, two rows in
-// three with one: 50 us (8 + 20 + 17 and the launches) against a floor of 27;
+// three with one: 49 us (7 + 20 + 17 and the launches) against a floor of 27;
 // without the grouping, 64 neighbouring rows at a time, 192 us.
 constexpr int kFewRows = 512;
 constexpr int64_t kFewRowsBytes = (int64_t)64 << 20;
@@ -306,8 +304,8 @@ constexpr int kUpRows = 64;        // rows of a tile: 16 for each of four warps
 constexpr int kUpThreads = 256;
 // K chunks of a warp in flight, and column groups. At rank 64 so few that two
 // blocks share an SM (2,048 tokens a source: 71 us, with 3 and 4 stages and one
-// block 85); at rank 32 three and four blocks with 3 and 4 take 50.5 us, with 2
-// and 2 52.4, with 4 and 4 53.
+// block 85, both before the grouping's loads overlapped); at rank 32 3 and 4 take
+// 50.5 us, 2 and 2 52.4, 4 and 4 53.
 constexpr int down_stages(int rank) { return rank <= 32 ? 3 : 2; }
 constexpr int up_stages(int rank) { return rank <= 32 ? 4 : 2; }
 
@@ -321,26 +319,32 @@ __global__ void __cluster_dims__(kGroupCtas, 1, 1) __launch_bounds__(kGroupThrea
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t cta = blockIdx.x;
   const int groups = p.S + 1;  // at most kGroupThreads
-  const int limit = p.row_src ? afd::group_end(p.ends[p.G - 1], p.R) : p.R;
-  const int share = ((limit + kGroupCtas - 1) / kGroupCtas + 31) & ~31;
-  const int64_t lo = (int64_t)cta * share, hi = lo + share < limit ? lo + share : limit;
-  for (int g = threadIdx.x; g < groups; g += kGroupThreads) count[g] = 0;
-  __syncthreads();
-  // The first rows' groups stay in registers, all their loads in flight at once.
+  // Rows go to the CTAs 1024 at a time, whatever the last end is: the first
+  // ones' row_src and that end are on their way together (a contiguous share
+  // each, known after the end only: 1.3 us more).
+  constexpr int kStep = kGroupCtas * kGroupThreads;
+  const int64_t lo = (int64_t)cta * kGroupThreads;
   int keep[kGroupKeep];
 #pragma unroll
   for (int i = 0; i < kGroupKeep; ++i) {
-    const int64_t r = lo + i * kGroupThreads + threadIdx.x;
-    keep[i] = r < hi ? row_group(p, (int)r) : -1;
+    const int64_t r = lo + i * kStep + threadIdx.x;
+    keep[i] = r >= p.R ? -1 : p.row_src ? p.row_src[r] : (int)r;
   }
+  const int limit = p.row_src ? afd::group_end(p.ends[p.G - 1], p.R) : p.R;
+  for (int g = threadIdx.x; g < groups; g += kGroupThreads) count[g] = 0;
+  __syncthreads();
+  // The first rows' groups stay in registers, all their loads in flight at once.
+#pragma unroll
+  for (int i = 0; i < kGroupKeep; ++i)
+    keep[i] = lo + i * kStep + threadIdx.x < limit ? token_group(p, keep[i]) : -1;
   auto tally = [&](int g) {
     const unsigned same = __match_any_sync(0xffffffffu, g);
     if (g >= 0 && lane == __ffs(same) - 1) atomicAdd(&count[g], __popc(same));
   };
 #pragma unroll
   for (int i = 0; i < kGroupKeep; ++i) tally(keep[i]);
-  const int64_t rest = lo + kGroupKeep * kGroupThreads + 32 * warp;
-  for (int64_t r0 = rest; r0 < hi; r0 += kGroupThreads) tally(r0 + lane < hi ? row_group(p, (int)r0 + lane) : -1);
+  const int64_t rest = lo + kGroupKeep * kStep + 32 * warp;
+  for (int64_t r0 = rest; r0 < limit; r0 += kStep) tally(r0 + lane < limit ? row_group(p, (int)r0 + lane) : -1);
   cluster_sync();
   // a thread per group of the prefix sum
   const int g = threadIdx.x;
@@ -378,8 +382,8 @@ __global__ void __cluster_dims__(kGroupCtas, 1, 1) __launch_bounds__(kGroupThrea
     if (g >= 0) p.order[at] = (int)r;
   };
 #pragma unroll
-  for (int i = 0; i < kGroupKeep; ++i) place(keep[i], lo + i * kGroupThreads + threadIdx.x);
-  for (int64_t r0 = rest; r0 < hi; r0 += kGroupThreads) place(r0 + lane < hi ? row_group(p, (int)r0 + lane) : -1, r0 + lane);
+  for (int i = 0; i < kGroupKeep; ++i) place(keep[i], lo + i * kStep + threadIdx.x);
+  for (int64_t r0 = rest; r0 < limit; r0 += kStep) place(r0 + lane < limit ? row_group(p, (int)r0 + lane) : -1, r0 + lane);
   cluster_sync();  // nobody leaves while its counts may be read
 }
 
