@@ -139,17 +139,20 @@ __device__ __forceinline__ void cluster_sync() {
 // its neighbour's. With few rows a call is a chain of latencies (2.9 us for one
 // row of 2048 columns, rank 16; 9.7 us by the three launches below), with many
 // every row reads its adapter from L2 again. Blocks of a cluster, 2048 columns,
-// rank 16: with 16 rows 8 take 3.1 us, 4 3.3, 2 4.1 and 1 6.0; with 64 rows 6.8,
-// 4.1, 4.3 and 6.2; with 128 11.0, 6.8, 5.5 and 6.2; with 512 38, 20, 12.4 and
-// 13.7. So 8 up to 32 rows, 4 up to 64 and 2 beyond.
+// rank 16: with 16 rows 8 take 3.2 us, 4 3.3, 2 4.2 and 1 5.9; with 64 rows 4.6,
+// 3.6, 4.3 and 6.1; with 128 8.4, 4.9, 5.0 and 6.2; with 512 30, 16, 11.2 and
+// 10.3, padded to 128 rows a group 13.8, 10.6, 9.3 and 12.2. So 8 up to 32 rows,
+// 4 up to 64 and 2 beyond. Four blocks share an SM up to rank 16 (256 rows: 6.7
+// us, with three 8.9; five at rank 8 5.5, with four 5.0), two above (rank 32, 128
+// rows: 6.4, with three 7.7).
 // Rows are dealt to the clusters one by one, as the live ones of a padded layout
 // sit next to each other, and to an odd number of clusters, as groups start at
-// multiples of a power of two (152 clusters: 13.6 us, 151: 11.1). A cluster
-// looks 32 of its rows up at a time.
+// multiples of a power of two (the padded 512 rows in 304 clusters: 13.5 us, in
+// 303: 9.1). A cluster looks 32 of its rows up at a time.
 constexpr int kRowCtas = 8, kRowThreads = 256;
 
 template <int RANK, bool FP8>
-__global__ void __launch_bounds__(kRowThreads, RANK <= 16 ? 3 : 2) adapter_rows_kernel(const AdapterParams p, const int ctas) {
+__global__ void __launch_bounds__(kRowThreads, RANK <= 16 ? 4 : 2) adapter_rows_kernel(const AdapterParams p, const int ctas) {
   __shared__ float part[2][kRowCtas][RANK];
   __shared__ __align__(16) float low[RANK];
   constexpr int JW = RANK / 8;                          // dot products of a warp
@@ -778,13 +781,13 @@ cudaError_t launch_adapters(const AdapterParams& p, int device, int sms, cudaStr
 // Whether a cluster per row does; `rows` is the most rows that can be live. The
 // row kernel reads rows * rank * (K + N) * 2 bytes of adapters from L2. The three
 // launches read far less, but a tile's rank * K * 2 bytes by one block, at about
-// a 64th of the rate of all. Rank 16, K = N = 2048: 128 rows (16 MiB) 5.5 against
-// 10.5 us, 256 (32) 8.9 against 10.8, 512 (64) 12.4 against 11.8, padded to 128
-// rows a group 10.7 against 11.1; rank 64: 128 rows (64 of 80) 9.6 against 14.2,
-// 256 (128) 17.6 against 14.7. K = 7168, rank 16: 128 rows (36 of 78) 8.6 against
-// 13.8, 512 (144) 21.6 against 15.1; rank 64: 64 rows (72 of 120) 10.0 against
-// 21.5, 256 (288) 29.6 against 22.7. Rank 8 stops at 512 rows: 9.3 against 11.3
-// (32 MiB), where 256 took 6.8. One launch in place of three and no workspace
+// a 64th of the rate of all. Rank 16, K = N = 2048: 128 rows (16 MiB) 4.9 against
+// 10.5 us, 256 (32) 6.7 against 10.8, 512 (64) 11.2 against 11.7, padded to 128
+// rows a group 9.3 against 11.0; rank 64: 128 rows (64 of 80) 9.6 against 14.2,
+// 256 (128) 17.6 against 14.7. K = 7168, rank 16: 128 rows (36 of 78) 7.5 against
+// 13.6, 512 (144) 19.0 against 15.0; rank 64: 64 rows (72 of 120) 10.0 against
+// 21.5, 256 (288) 29.6 against 22.7. Rank 8 stops at 512 rows: 7.7 against 11.1
+// (32 MiB), where 256 took 5.0. One launch in place of three and no workspace
 // also take 12 us less of the caller's time.
 bool few_rows(int64_t rows, int32_t rank, int32_t in_features, int32_t out_features) {
   const int64_t k = (int64_t)rank * in_features * 2, n = (int64_t)rank * out_features * 2;
@@ -801,7 +804,7 @@ template <int RANK, bool FP8>
 cudaError_t launch_adapters_of(const AdapterParams& p, int few, int device, int sms, cudaStream_t stream) {
   if (!few) return launch_adapters<RANK, FP8>(p, device, sms, stream);
   const int ctas = few <= 32 ? 8 : few <= 64 ? 4 : 2;
-  const int64_t most = (sms * (RANK <= 16 ? 3 : 2) / ctas - 1) | 1;
+  const int64_t most = (sms * (RANK <= 16 ? 4 : 2) / ctas - 1) | 1;
   return afd::launch_clusters(adapter_rows_kernel<RANK, FP8>, (p.R < most ? p.R : most) * ctas, kRowThreads, ctas, 0,
                               stream, p, ctas);
 }
