@@ -62,7 +62,8 @@ int g_seg2_blocks_per_sm = 0;
 // receipts: L2-only loads.
 //
 // A combine launched right after the previous combine of the same exchange
-// on the same stream (p.early != 0) needs no dependency wait to start: its
+// on the same stream, with no other call of the library between them there
+// (p.early != 0), needs no dependency wait to start: its
 // launch implies that every block of that combine has passed its own wait
 // (it lets dependents launch only after it), so the scatter, the expert and
 // everything before them have completed, and the replies stay unchanged for

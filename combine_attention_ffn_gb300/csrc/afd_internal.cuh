@@ -5,7 +5,27 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace afd {
+
+// What the library has enqueued on a stream, as a count: a call that launches
+// kernels which let their dependents start early takes a turn. A combine may
+// start beside its predecessor only if nobody has taken one since (see
+// afd_source_collect). Streams share the counters, and the two handles of the
+// legacy stream are one: a turn of another stream's then only costs an early
+// start.
+constexpr int kTurnSlots = 256;
+inline std::atomic<uint32_t> g_stream_turns[kTurnSlots];
+
+inline std::atomic<uint32_t>& stream_turns(cudaStream_t stream) {
+  const uint64_t h = stream == cudaStreamLegacy ? 0 : reinterpret_cast<uintptr_t>(stream);
+  return g_stream_turns[(h * 0x9e3779b97f4a7c15ull) >> 56];
+}
+inline uint32_t stream_turn(cudaStream_t stream) { return stream_turns(stream).load(std::memory_order_acquire); }
+inline uint32_t take_stream_turn(cudaStream_t stream) {
+  return stream_turns(stream).fetch_add(1, std::memory_order_acq_rel) + 1;
+}
 
 constexpr int kMaxSources = 64;
 constexpr int kMaxWorkers = 64;

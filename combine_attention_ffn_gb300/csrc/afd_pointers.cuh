@@ -7,6 +7,8 @@
 
 #include <atomic>
 
+#include "afd_internal.cuh"
+
 namespace afd {
 
 // Sets a kernel's dynamic shared memory limit once per device (`done`: one
@@ -64,6 +66,7 @@ inline cudaError_t launch_clusters(void (*kernel)(Params...), int64_t grid, int 
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = cluster ? 2 : 1;
+  take_stream_turn(stream);
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
 }
 

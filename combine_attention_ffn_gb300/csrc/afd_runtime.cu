@@ -72,9 +72,11 @@ struct afd_ctx {
   int rhc;
   bool cached;          // this exchange reuses the last layout
   // the last call of this exchange launched a combine on combine_stream (the
-  // next combine on that stream may start without the dependency wait)
+  // next combine on that stream may start without the dependency wait, if no
+  // other call of the library took the stream's turn after combine_turn)
   bool combine_last;
   cudaStream_t combine_stream;
+  uint32_t combine_turn;
   bool combine_captured;
   // the last layout that a dispatch computed (what a cached dispatch reuses)
   bool layout_valid;
@@ -213,6 +215,7 @@ void reset_exchange(afd_ctx* c) {
   c->cached = false;
   c->combine_last = false;
   c->combine_stream = nullptr;
+  c->combine_turn = 0;
   c->combine_captured = false;
   c->staged_n = c->replied_n = c->collected_n = 0;
   c->bucket = -1;
@@ -312,6 +315,7 @@ afd_status launch_exchange_dispatch(afd_ctx* c, cudaStream_t stream, bool cached
   p.row_w = c->row_w;
   p.rows = c->rows;
   p.row_scales = c->row_scales;
+  afd::take_stream_turn(stream);
   cudaError_t e = cached ? afd::launch_cached_scatter(p, c->sm_cap, stream)
                          : afd::launch_dispatch(p, c->sm_cap, stream);
   if (e != cudaSuccess) return cuda_fail(c, e, "dispatch launch");
@@ -700,10 +704,15 @@ afd_status afd_source_collect(afd_ctx* c, int32_t source, void* out, int32_t vie
     CombineParams p;
     memset(&p, 0, sizeof p);
     // Started at once when the previous call was a collect of this exchange
-    // that launched a combine on the same stream (and capture state): the
-    // stream then holds nothing between the two combines but host-side marks.
+    // that launched a combine on the same stream (and capture state), and no
+    // call of the library, with another context or with none, has enqueued
+    // anything there since. Between the two combines the stream then holds
+    // host-side marks, and at most kernels of the caller's that start after
+    // the first combine and let this one start only once they have finished.
+    // (Other kernels of the library let their dependents start while they
+    // still read: this one's `out` may be memory that they read.)
     p.early = AFD_COMBINE_EARLY && c->combine_last && c->combine_stream == stream &&
-              c->combine_captured == is_capturing(stream);
+              c->combine_turn == afd::stream_turn(stream) && c->combine_captured == is_capturing(stream);
     p.share = g.num_sources;  // each source collects on its own
     p.routes[0] = c->routes + (int64_t)c->src[source].tok_off * g.top_k;
     p.out[0] = as_view ? inbox : static_cast<uint16_t*>(out);
@@ -715,6 +724,7 @@ afd_status afd_source_collect(afd_ctx* c, int32_t source, void* out, int32_t vie
     p.K = g.top_k;
     p.H = g.hidden;
     p.total_tokens = T;
+    c->combine_turn = afd::take_stream_turn(stream);
     cudaError_t e = afd::launch_combine(p, c->sm_cap, stream);
     if (e != cudaSuccess) return cuda_fail(c, e, "combine launch");
   }
@@ -777,6 +787,7 @@ afd_status afd_source_collect_all(afd_ctx* c, void* const* outs, int32_t view, a
   p.K = g.top_k;
   p.H = g.hidden;
   p.total_tokens = tok;
+  afd::take_stream_turn(stream);
   cudaError_t e = afd::launch_combine(p, c->sm_cap, stream);
   if (e != cudaSuccess) return cuda_fail(c, e, "combine launch");
   for (int s = 0; s < g.num_sources; ++s) {

@@ -257,11 +257,16 @@ typedef struct afd_view {
  *         view_out->is_view = 0.
  *   view_out  host; filled on success (may be NULL when view = 0)
  * When the previous call on this context was a collect of the same exchange
- * that launched a combine on the same stream, this call's combine starts
+ * that launched a combine on the same stream, and no other call of this
+ * library has enqueued kernels there since, this call's combine starts
  * without waiting for that one (both only read the replies) and completes
- * after it, so stream order still holds for whatever follows. Work enqueued on
- * the stream between the two calls must therefore not write the reply rows
- * or this source's `out`.
+ * after it, so stream order still holds for whatever follows. Work that the
+ * caller enqueues on the stream between the two calls must therefore not
+ * write the reply rows or this source's `out`, and work that lets its
+ * dependents start before it has finished (a programmatic trigger in a kernel
+ * of the caller's own) must not read this source's `out` either. Calls of
+ * this library in between may read and write either: the combine then waits
+ * for them.
  * Errors: AFD_ERR_STATE (replies missing, or source already collected),
  * AFD_ERR_ARG, AFD_ERR_CUDA. */
 AFD_API afd_status afd_source_collect(afd_ctx* ctx, int32_t source, void* out, int32_t view,
