@@ -77,6 +77,9 @@ struct afd_ctx {
   bool combine_last;
   cudaStream_t combine_stream;
   uint32_t combine_turn;
+  // where this exchange's combines write: of each collected source, as the
+  // kernels address it
+  const uint16_t* combine_out[afd::kMaxSources];
   bool combine_captured;
   // the last layout that a dispatch computed (what a cached dispatch reuses)
   bool layout_valid;
@@ -226,6 +229,17 @@ void reset_exchange(afd_ctx* c) {
     c->recv_rows[i] = -1;
     c->reply[i] = nullptr;
   }
+}
+
+// Whether T rows at `out` share memory with the result of a source of this
+// exchange that is collected already.
+bool overlaps_collected(const afd_ctx* c, const uint16_t* out, int T) {
+  for (int s = 0; s < c->cfg.num_sources; ++s) {
+    if (!c->collected[s] || c->src[s].T == 0) continue;
+    const uint16_t* other = c->combine_out[s];
+    if (out < other + (int64_t)c->src[s].T * c->cfg.hidden && other < out + (int64_t)T * c->cfg.hidden) return true;
+  }
+  return false;
 }
 
 void free_all(afd_ctx* c) {
@@ -710,12 +724,16 @@ afd_status afd_source_collect(afd_ctx* c, int32_t source, void* out, int32_t vie
     // host-side marks, and at most kernels of the caller's that start after
     // the first combine and let this one start only once they have finished.
     // (Other kernels of the library let their dependents start while they
-    // still read: this one's `out` may be memory that they read.)
+    // still read: this one's `out` may be memory that they read.) Nor may any
+    // combine of the exchange, which may all still run, write where this one does.
+    uint16_t* to = as_view ? inbox : static_cast<uint16_t*>(out);
     p.early = AFD_COMBINE_EARLY && c->combine_last && c->combine_stream == stream &&
-              c->combine_turn == afd::stream_turn(stream) && c->combine_captured == is_capturing(stream);
+              c->combine_turn == afd::stream_turn(stream) && c->combine_captured == is_capturing(stream) &&
+              !overlaps_collected(c, to, T);
+    c->combine_out[source] = to;
     p.share = g.num_sources;  // each source collects on its own
     p.routes[0] = c->routes + (int64_t)c->src[source].tok_off * g.top_k;
-    p.out[0] = as_view ? inbox : static_cast<uint16_t*>(out);
+    p.out[0] = to;
     p.out_stride[0] = g.hidden;
     p.tok_off[0] = 0;
     for (int f = 0; f < g.num_workers; ++f) p.reply[f] = c->reply[f];

@@ -266,7 +266,8 @@ typedef struct afd_view {
  * dependents start before it has finished (a programmatic trigger in a kernel
  * of the caller's own) must not read this source's `out` either. Calls of
  * this library in between may read and write either: the combine then waits
- * for them.
+ * for them, as it does where its `out` shares memory with that of a source
+ * collected before it.
  * Errors: AFD_ERR_STATE (replies missing, or source already collected),
  * AFD_ERR_ARG, AFD_ERR_CUDA. */
 AFD_API afd_status afd_source_collect(afd_ctx* ctx, int32_t source, void* out, int32_t view,

@@ -232,3 +232,47 @@ def test_early_start_only_next_to_each_other(name):
             buf.close()
     finally:
         afd._lib = prev
+
+
+@pytest.mark.parametrize("T,shift", [(64, 0), (2048, 0), (2048, 1000), ((100, 2048), -64)])
+def test_second_result_over_the_first(T, shift):
+    """Collects into memory that the results share (the caller's own buffer,
+    or a dropped result's block): the later one's rows are the ones that stay,
+    and the combines do not run side by side."""
+    wl = W.named("2A2F", T=T) if isinstance(T, int) else W.named("2A2F").with_tokens(T)
+    exp = GH.expected(W.make_inputs(wl), GH.IDENTITY)
+    build.build()
+    prev = afd.load_library()
+    afd.use_library(build.build_timers())
+    try:
+        dev = GH.to_device(W.make_inputs(wl))
+        buf = GH.make_buffer(wl)
+        mem = torch.zeros(2 * wl.bucket, H, dtype=BF16, device="cuda")
+        at = 64
+        outs = [mem[at:at + wl.T[0]], mem[at + shift:at + shift + wl.T[1]]]
+
+        def check():
+            torch.cuda.synchronize()
+            got = outs[1].view(torch.int16).cpu().numpy().view(np.uint16)
+            assert np.array_equal(got, exp["out"][1, :wl.T[1]])
+
+        try:
+            torch.cuda.synchronize()
+            buf.phase_stamps(clear=True)
+            for _ in range(4):
+                _exchange(buf, wl, dev, lambda: None, outs)
+                check()
+            assert not (buf.phase_stamps()[3].astype(np.int64) > 0).any()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                _exchange(buf, wl, dev, lambda: None, outs)
+            for _ in range(4):
+                mem.zero_()
+                g.replay()
+                check()
+            del g
+        finally:
+            torch.cuda.synchronize()
+            buf.close()
+    finally:
+        afd._lib = prev
