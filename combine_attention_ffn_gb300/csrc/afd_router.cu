@@ -6,8 +6,9 @@
 // index among its holders with a second one, so k rounds cost 2k warp
 // reductions and no shared memory. The work is a few KB per token: a decode
 // step is bound by the launch, a prefill bucket by the latency of one warp's
-// rounds, which is why tokens take a warp each and not a block: 2.4 us for one
-// token of 128 experts, 3.4 us for 2,048, with a bias 3.6 and 4.8 to 6.9.
+// rounds, which is why tokens take a warp each and not a block: 2.3 us for one
+// token of 128 experts, 3.4 us for 2,048, with a bias 3.1 to 3.4 and 4.5 to 6.4
+// (softmax scores and a bias of zeros, whose keys crowd: 8.9).
 //
 // Softmax and sigmoid are monotone, so without a bias the logits themselves
 // are the keys, exactly. With a bias the keys score + bias are computed in
@@ -230,34 +231,58 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_topk_kernel(const Rou
       if (lane == found) mine = at, logit = v, kept = from_image(best);
     }
     if (p.bias) {
-      // Lane k looks whether its key is too close to the one before to tell (a
-      // score is at most 1, which spares most tokens its second reckoning).
+      // Whether two keys are too close to tell (a score is at most 1, which
+      // spares most tokens its second reckoning).
       auto near = [&](float va, int ea, float ka, float vb, int eb, float kb) {
         if (ka - kb > key_slack(p.sigmoid, 1.f, 1.f, ka, kb)) return false;
         if (va == vb && p.bias[ea] == p.bias[eb]) return false;
         return !(ka - kb > key_slack(p.sigmoid, score_of(va), score_of(vb), ka, kb));
       };
-      const float va = __shfl_up_sync(kFull, logit, 1), ka = __shfl_up_sync(kFull, kept, 1);
-      const int ea = __shfl_up_sync(kFull, mine, 1);
-      bool close = __any_sync(kFull, lane > 0 && lane < found && near(va, ea, ka, logit, mine, kept));
-      // The rounds go on while the last two keys are too close: all experts that
-      // may belong to the first K are then in the lanes' slots.
+      // The rounds go on until no expert that is left can belong to the first K:
+      // none has a key near enough to one of theirs for the largest score that
+      // is left (1 at first, which most tokens' gap exceeds). The next key alone
+      // does not tell: behind one that is apart, or equal to the last slot's,
+      // one with a larger score, and so a larger error, may follow.
       bool over = false;
+      float left = -1.f, own = 0.f;
+      auto apart = [&](float score_left, float score_own, float k) {
+        return __all_sync(kFull, lane >= p.K || kept - k > key_slack(p.sigmoid, score_left, score_own, kept, k));
+      };
       while (found >= p.K) {
         int at;
         float v;
         const uint32_t best = pick(&at, &v);
         if (best == 0) break;
         const float k = from_image(best);
-        if (!near(__shfl_sync(kFull, logit, found - 1), __shfl_sync(kFull, mine, found - 1),
-                  __shfl_sync(kFull, kept, found - 1), v, at, k))
-          break;
-        close = true;
+        if (apart(1.f, 1.f, k)) break;
+        if (left < 0.f) {
+          float most = v;
+#pragma unroll
+          for (int j = 0; j < PER; ++j)
+            if (key[j]) most = fmaxf(most, l[j]);
+#pragma unroll
+          for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, d));
+          left = score_of(most);
+          if (lane < p.K) own = score_of(logit);
+        }
+        if (apart(left, own, k)) break;
+        // Of equal experts (the same logit and bias) the first K will do.
+        const float b = p.bias[at];
+        if (__popc(__ballot_sync(kFull, lane < found && logit == v && p.bias[max(mine, 0)] == b)) >= p.K) {
+#pragma unroll
+          for (int j = 0; j < PER; ++j)
+            if (key[j] && l[j] == v && p.bias[lane + 32 * j] == b) key[j] = 0;
+          continue;
+        }
         over = found == 32;
         if (over) break;
         if (lane == found) mine = at, logit = v, kept = k;
         ++found;
       }
+      // If any two are near without being equal, two neighbours are.
+      const float va = __shfl_up_sync(kFull, logit, 1), ka = __shfl_up_sync(kFull, kept, 1);
+      const int ea = __shfl_up_sync(kFull, mine, 1);
+      const bool close = __any_sync(kFull, lane > 0 && lane < found && near(va, ea, ka, logit, mine, kept));
       if (over)
         select_exact<PER>(l, p, top, lane, &mine, &logit);
       else if (close)
