@@ -481,6 +481,13 @@ struct DownShared {
   };
 };
 
+// What of v is rounded to BF16 first: a finite number above the largest BF16
+// gives that one (rounded up it were infinite, and the rest minus infinity).
+__device__ __forceinline__ float high_part(float v) {
+  const float most = __uint_as_float(0x7f7f0000u);
+  return fabsf(v) > most && !isinf(v) ? copysignf(most, v) : v;
+}
+
 template <int RANK, bool FP8>
 __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const AdapterParams p) {
   extern __shared__ __align__(16) uint8_t ad_smem[];
@@ -582,7 +589,7 @@ __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const Ada
         v.x += o.x, v.y += o.y;
       }
       v.x *= scale, v.y *= scale;
-      const uint32_t hi = afd::pack_bf16(v.x, v.y);
+      const uint32_t hi = afd::pack_bf16(high_part(v.x), high_part(v.y));
       // (an infinite product leaves no rest)
       const uint32_t lo = afd::pack_bf16(isinf(v.x) ? 0.f : v.x - __uint_as_float(hi << 16),
                                          isinf(v.y) ? 0.f : v.y - __uint_as_float(hi & 0xffff0000u));

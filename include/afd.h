@@ -497,8 +497,9 @@ AFD_API afd_status afd_gated_rows(const void* h, int64_t h_stride, const int32_t
 /* Low-rank adapters of many requests beside a shared projection: row r of the
  * request whose adapter is a gets
  *   out[r] = base[r] + scales[a] * up[a] (down[a] x[r])
- * in FP32 with one rounding to BF16 (the low-rank product down[a] x[r] is
- * kept to at least 16 bits of precision between the two).
+ * in FP32 with one rounding to BF16 (the low-rank product scales[a] down[a]
+ * x[r] is kept to at least 16 bits of precision between the two, or to
+ * 2^-134 where that is more).
  * The adapter of a row: a = token_slots[t], where t = row_src[r] / top_k for
  * received rows (row_src as afd_recv gives it), or t = r without row_src. A
  * slot outside [0, num_slots) means no adapter: out[r] = base[r].
