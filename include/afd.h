@@ -446,8 +446,12 @@ AFD_API afd_status afd_route_topk(const void* logits, int32_t logits_dtype, int6
  *   out[r][n] = silu(y[r][n]) * y[r][N + n]     (gated = 1, N = out_features;
  *               weight then has 2N rows per expert, the gate's first)
  * with FP32 sums and one rounding to BF16. FP8: x and weight are E4M3 with
- * FP32 scales for blocks of 128, and the sum is that of x_scale[r][k/128] *
- * weight_scale[l][n/128][k/128] * x * weight.
+ * FP32 scales for blocks of 128, and the sum is that of (x_scale[r][k/128] *
+ * weight_scale[l][n/128][k/128]) * (the block's sum of x * weight). The two
+ * scales' product is rounded to FP32 first, so it has to lie in that type's
+ * normal range (2^-126 to 2^128) or be zero: below it a block's part loses
+ * digits or is lost, above it the part is infinite, or NaN where the block's
+ * sum is zero. The scales by themselves may be any FP32 numbers.
  * Rows of `out` outside every expert's range are left as they were; rows of
  * `x` there are never used for a result, whatever they hold. Ends beyond
  * num_rows are taken as num_rows.
