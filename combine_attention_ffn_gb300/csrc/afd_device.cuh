@@ -75,6 +75,17 @@ __device__ __forceinline__ uint4 ld_once(const uint4* p) {
   return v;
 }
 
+// The same of data that the kernel itself may overwrite afterwards (the
+// non-coherent loads above are for what nobody writes while the kernel runs).
+__device__ __forceinline__ uint4 ld_before_write(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // Rounds v up to a multiple of a (a >= 1); a power of two (the usual
 // expert_alignment) takes a mask instead of a division.
 __device__ __forceinline__ int align_up_dev(int v, int a) {

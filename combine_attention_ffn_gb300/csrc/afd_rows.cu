@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(256) gated_rows_kernel(const GatedParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (c0 + 256 * i < p.N) {
-            gv[i] = afd::ld_once(reinterpret_cast<const uint4*>(gate + c0 + 256 * i));
+            gv[i] = afd::ld_before_write(reinterpret_cast<const uint4*>(gate + c0 + 256 * i));  // `out` may be there
             uv[i] = afd::ld_once(reinterpret_cast<const uint4*>(up + c0 + 256 * i));
           }
 #pragma unroll
