@@ -667,13 +667,16 @@ bool encode(EncodeTiled f, CUtensorMap* map, bool fp8, uint32_t rank, const void
 template <bool FP8, bool GATED>
 cudaError_t launch_grouped(const Maps& maps, const ExpertParams& p, int device, int pairs, cudaStream_t stream) {
   if (FP8) {
-    // the registers that the hand-over gives out must be there at launch
-    static const bool enough = [] {
+    // the registers that the hand-over gives out must be there at launch (asked
+    // until there is an answer: a failed query says nothing about the next call)
+    static std::atomic<bool> enough{false};
+    if (!enough.load(std::memory_order_relaxed)) {
       cudaFuncAttributes a;
-      return cudaFuncGetAttributes(&a, grouped_linear_kernel<FP8, GATED>) == cudaSuccess &&
-             a.numRegs * kThreads >= kFrontRegs * 128 + kDrainRegs * 32 * kDrainWarps;
-    }();
-    if (!enough) return cudaErrorInvalidKernelImage;
+      const cudaError_t e = cudaFuncGetAttributes(&a, grouped_linear_kernel<FP8, GATED>);
+      if (e != cudaSuccess) return e;
+      if (a.numRegs * kThreads < kFrontRegs * 128 + kDrainRegs * 32 * kDrainWarps) return cudaErrorInvalidKernelImage;
+      enough.store(true, std::memory_order_relaxed);
+    }
   }
   static std::atomic<uint64_t> set{0};
   const cudaError_t e = afd::allow_shared(grouped_linear_kernel<FP8, GATED>, (int)kSmem, device, set);
