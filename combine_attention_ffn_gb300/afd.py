@@ -456,6 +456,13 @@ def _call(name: str, on: torch.Tensor, stream, *args) -> None:
         raise AfdError(st, f"{name}: {lib.afd_status_string(st).decode()}")
 
 
+def _fit_int32(*sizes: int) -> None:
+    """Refuses what the C ABI's 32-bit sizes cannot hold (ctypes would keep its
+    low bits and the call work on a part)."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise AfdError(ERR_UNSUPPORTED, f"sizes {sizes} must fit 32 bits")
+
+
 def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
     """A new tensor from the pool of the stream that will use it (what the
     allocator hands out on another one may still be in use there)."""
@@ -503,6 +510,7 @@ def route_topk(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
     if scoring not in SCORINGS:
         raise AfdError(ERR_ARG, f"scoring must be one of {sorted(SCORINGS)}, got {scoring!r}")
     T, E = logits.shape
+    _fit_int32(T, E, top_k)
     stride = _want_rows(logits, "logits", logits.dtype, (T, E))
     bias_ptr = None if bias is None else _want(bias, "bias", torch.float32, (E,))
     live_ptr = None if live_tokens is None else _want(live_tokens, "live_tokens", torch.int32, (1,))
@@ -540,6 +548,7 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, ends: torch.Tensor, *,
         raise AfdError(ERR_ARG, "x must be [R, K] bfloat16 or float8_e4m3fn and weight [G, N, K]")
     R, K = x.shape
     G, W = weight.shape[0], weight.shape[1]
+    _fit_int32(G, W, K, expert_alignment)
     fp8 = x.dtype == torch.float8_e4m3fn
     if gated and W % 2:
         raise AfdError(ERR_ARG, f"a gated weight has an even number of rows, got {W}")
@@ -576,6 +585,7 @@ def gated_rows(h: torch.Tensor, ends: torch.Tensor, *, expert_alignment: int = 1
     R, N = h.shape[0], h.shape[1] // 2
     h_stride = _want_rows(h, "h", torch.bfloat16, (R, 2 * N))
     G = ends.numel()
+    _fit_int32(G, N, expert_alignment)
     ends_ptr = _want(ends, "ends", torch.int32, (G,))
     if out is None:
         out = _empty((R, N), torch.bfloat16, h.device, stream)
@@ -606,6 +616,7 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
     up_ptr = _want(up, "up", torch.bfloat16, (S, N, rank))
     scales_ptr = _want(scales, "scales", torch.float32, (S,))
     tokens = token_slots.numel()
+    _fit_int32(tokens, S, rank, K, N, top_k, 0 if ends is None else ends.numel())
     slots_ptr = _want(token_slots, "token_slots", torch.int32, (tokens,))
     G, src_ptr, ends_ptr = 0, None, None
     if row_src is not None:
