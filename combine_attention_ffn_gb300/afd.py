@@ -432,6 +432,7 @@ def route_layout_noalloc(ids: torch.Tensor, num_experts: int, num_workers: int,
 
 
 # -- the experts' side of an exchange (afd.h: no context, no state) -----------
+# Forward only: with gradients enabled, inputs that require them are refused.
 # A decode step's call is shorter on the GPU than on the host, so the binding
 # asks PyTorch for the raw stream and device number where it has them: the
 # public objects around them cost 1 us a call.
@@ -456,11 +457,20 @@ def _call(name: str, on: torch.Tensor, stream, *args) -> None:
         raise AfdError(st, f"{name}: {lib.afd_status_string(st).decode()}")
 
 
-def _fit_int32(*sizes: int) -> None:
-    """Refuses what the C ABI's 32-bit sizes cannot hold (ctypes would keep its
-    low bits and the call work on a part)."""
-    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
-        raise AfdError(ERR_UNSUPPORTED, f"sizes {sizes} must fit 32 bits")
+_INT32 = 0x7fffffff
+_grad_enabled = torch.is_grad_enabled
+
+
+def _too_large(*sizes: int) -> AfdError:
+    """The C ABI's sizes have 32 bits (ctypes would keep their low ones, and the
+    call work on a part)."""
+    return AfdError(ERR_UNSUPPORTED, f"sizes {sizes} must fit 32 bits")
+
+
+def _no_backward() -> AfdError:
+    """Autograd would take the result for a constant."""
+    return AfdError(ERR_UNSUPPORTED, "no backward pass: inputs that require gradients are taken "
+                    "under torch.no_grad() only, or detached")
 
 
 def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
@@ -510,7 +520,11 @@ def route_topk(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
     if scoring not in SCORINGS:
         raise AfdError(ERR_ARG, f"scoring must be one of {sorted(SCORINGS)}, got {scoring!r}")
     T, E = logits.shape
-    _fit_int32(T, E, top_k)
+    if T > _INT32 or E > _INT32 or not -_INT32 <= top_k <= _INT32:
+        raise _too_large(T, E, top_k)
+    if _grad_enabled() and (logits.requires_grad or (bias is not None and bias.requires_grad)
+                            or (weights is not None and weights.requires_grad)):
+        raise _no_backward()
     stride = _want_rows(logits, "logits", logits.dtype, (T, E))
     bias_ptr = None if bias is None else _want(bias, "bias", torch.float32, (E,))
     live_ptr = None if live_tokens is None else _want(live_tokens, "live_tokens", torch.int32, (1,))
@@ -548,7 +562,12 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, ends: torch.Tensor, *,
         raise AfdError(ERR_ARG, "x must be [R, K] bfloat16 or float8_e4m3fn and weight [G, N, K]")
     R, K = x.shape
     G, W = weight.shape[0], weight.shape[1]
-    _fit_int32(G, W, K, expert_alignment)
+    if G > _INT32 or W > _INT32 or K > _INT32 or not -_INT32 <= expert_alignment <= _INT32:
+        raise _too_large(G, W, K, expert_alignment)
+    if _grad_enabled() and (x.requires_grad or weight.requires_grad or (out is not None and out.requires_grad)
+                            or (x_scale is not None and x_scale.requires_grad)
+                            or (weight_scale is not None and weight_scale.requires_grad)):
+        raise _no_backward()
     fp8 = x.dtype == torch.float8_e4m3fn
     if gated and W % 2:
         raise AfdError(ERR_ARG, f"a gated weight has an even number of rows, got {W}")
@@ -585,7 +604,10 @@ def gated_rows(h: torch.Tensor, ends: torch.Tensor, *, expert_alignment: int = 1
     R, N = h.shape[0], h.shape[1] // 2
     h_stride = _want_rows(h, "h", torch.bfloat16, (R, 2 * N))
     G = ends.numel()
-    _fit_int32(G, N, expert_alignment)
+    if G > _INT32 or N > _INT32 or not -_INT32 <= expert_alignment <= _INT32:
+        raise _too_large(G, N, expert_alignment)
+    if _grad_enabled() and (h.requires_grad or (out is not None and out.requires_grad)):
+        raise _no_backward()
     ends_ptr = _want(ends, "ends", torch.int32, (G,))
     if out is None:
         out = _empty((R, N), torch.bfloat16, h.device, stream)
@@ -616,13 +638,20 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
     up_ptr = _want(up, "up", torch.bfloat16, (S, N, rank))
     scales_ptr = _want(scales, "scales", torch.float32, (S,))
     tokens = token_slots.numel()
-    _fit_int32(tokens, S, rank, K, N, top_k, 0 if ends is None else ends.numel())
+    if tokens > _INT32 or S > _INT32 or rank > _INT32 or K > _INT32 or N > _INT32 or not -_INT32 <= top_k <= _INT32:
+        raise _too_large(tokens, S, rank, K, N, top_k)
+    if _grad_enabled() and (base.requires_grad or x.requires_grad or down.requires_grad or up.requires_grad
+                            or scales.requires_grad or (out is not None and out.requires_grad)
+                            or (x_scale is not None and x_scale.requires_grad)):
+        raise _no_backward()
     slots_ptr = _want(token_slots, "token_slots", torch.int32, (tokens,))
     G, src_ptr, ends_ptr = 0, None, None
     if row_src is not None:
         if ends is None:
             raise AfdError(ERR_ARG, "row_src needs the exchange's ends, int32 [G]")
         G = ends.numel()
+        if G > _INT32:
+            raise _too_large(G)
         src_ptr = _want(row_src, "row_src", torch.int32, (R,))
         ends_ptr = _want(ends, "ends", torch.int32, (G,))
     elif tokens < R:
