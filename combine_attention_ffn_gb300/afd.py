@@ -31,6 +31,7 @@ ERR_TIMEOUT = 11
 BF16, FP8_E4M3, FP32 = 0, 1, 2
 SCORINGS = {"softmax": 0, "sigmoid": 1}
 COMBINE_FUSED, COMBINE_TWO_STAGE, COMBINE_TWO_STAGE_FP8 = 0, 1, 2
+PRODUCT_WAIT_CYCLES = 4_000_000_000  # afd_set_product_wait_limit's default
 
 EXPORTS = ("afd_create", "afd_destroy", "afd_source_dispatch", "afd_source_dispatch_cached",
            "afd_worker_receive",
@@ -39,7 +40,8 @@ EXPORTS = ("afd_create", "afd_destroy", "afd_source_dispatch", "afd_source_dispa
            "afd_reset_exchange", "afd_status_string", "afd_error_detail", "afd_arena_rows",
            "afd_recv_rows_for_bucket", "afd_version", "afd_route_layout_noalloc",
            "afd_set_wait_limit", "afd_phase_stamps", "afd_l2_flush", "afd_route_topk",
-           "afd_grouped_linear", "afd_gated_rows", "afd_adapter_add", "afd_adapter_workspace_bytes")
+           "afd_grouped_linear", "afd_gated_rows", "afd_adapter_add", "afd_adapter_workspace_bytes",
+           "afd_set_product_wait_limit")
 
 
 class AfdError(RuntimeError):
@@ -104,6 +106,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "afd_l2_flush": (i32, [v, i64, v]),
         "afd_route_topk": (i32, [v, i32, i64, v, v, i32, i32, i32, i32, i32, ctypes.c_float, v, v, v]),
         "afd_grouped_linear": (i32, [v, i64, v, v, v, v, i32, i32, i64, i32, i32, i32, i32, v, i64, v, v]),
+        "afd_set_product_wait_limit": (i32, [i64]),
         "afd_gated_rows": (i32, [v, i64, v, i32, i32, i64, i32, v, i64, v]),
         "afd_adapter_add": (i32, [v, i64, v, i64, v, v, v, v, v, v, v, i32, i32, i64, i32, i32, i32, i32,
                                   i32, v, i64, v, i64, v]),
@@ -556,8 +559,8 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, ends: torch.Tensor, *,
     and the up projection's after them ([E/F, 2N, K]) and ``out = silu(gate) *
     up``. Rows outside every expert's range are left as they were (`out`) or
     unspecified (without `out`). `error` (int32 [1]) receives ERR_TIMEOUT if a
-    bounded wait of the kernel gave up. See afd_grouped_linear in
-    include/afd.h."""
+    bounded wait of the kernel gave up (:func:`set_product_wait_limit`); without
+    it nothing tells of that. See afd_grouped_linear in include/afd.h."""
     if x.dim() != 2 or weight.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
         raise AfdError(ERR_ARG, "x must be [R, K] bfloat16 or float8_e4m3fn and weight [G, N, K]")
     R, K = x.shape
@@ -591,6 +594,17 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, ends: torch.Tensor, *,
     _call("afd_grouped_linear", x, stream, x.data_ptr(), x_stride, xs_ptr, w_ptr, ws_ptr, ends_ptr, G, expert_alignment,
           R, K, N, FP8_E4M3 if fp8 else BF16, bool(gated), out.data_ptr(), out_stride, error_ptr)
     return out
+
+
+def set_product_wait_limit(cycles: int = PRODUCT_WAIT_CYCLES) -> None:
+    """The most clocks of an SM for which a wait inside :func:`grouped_linear`'s
+    kernel lasts, for the process's calls from now on (the default: about two
+    seconds; 0: give up at once). See afd_set_product_wait_limit in
+    include/afd.h."""
+    lib = _lib or load_library()
+    if not 0 <= cycles < 1 << 63:
+        raise AfdError(ERR_ARG, f"cycles must be in [0, 2^63), got {cycles}")
+    lib.afd_set_product_wait_limit(cycles)
 
 
 def gated_rows(h: torch.Tensor, ends: torch.Tensor, *, expert_alignment: int = 1,

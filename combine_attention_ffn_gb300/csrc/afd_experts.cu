@@ -97,6 +97,7 @@ struct ExpertParams {
   uint16_t* out;
   int64_t out_stride;
   int32_t* error;
+  int64_t wait_cycles;  // of every wait, at most; 0: give up without one
 };
 
 struct alignas(16) BlockScales {
@@ -288,8 +289,8 @@ __device__ __forceinline__ bool drain_blocks(const ExpertParams& p, Shared& sh, 
     for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
   for (int kb = 0; kb < p.k_blocks; ++kb, ++unit) {
     const uint32_t s = unit % kScaleStages, b = turns.buf(unit);
-    if (!afd::mbar_wait(scale_full + 8 * s, (unit / kScaleStages) & 1, &sh.gave_up) ||
-        !afd::mbar_wait(turns.full + 8 * b, turns.phase(unit), &sh.gave_up))
+    if (!afd::mbar_wait(scale_full + 8 * s, (unit / kScaleStages) & 1, &sh.gave_up, p.wait_cycles) ||
+        !afd::mbar_wait(turns.full + 8 * b, turns.phase(unit), &sh.gave_up, p.wait_cycles))
       return false;
     afd::tcgen05_fence_after();
     const uint32_t acc = turns.tmem + b * turns.cols + 16 * h;
@@ -348,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       afd::mbar_init(scale_full + 8 * i, kScaleThreads);
       afd::mbar_init(scale_empty + 8 * i, kDrainWarps);
     }
-    sh.gave_up = 0;
+    sh.gave_up = p.wait_cycles == 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) afd::tmem_alloc_pair(afd::smem_u32(&sh.tmem), kColumns);
@@ -451,7 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
       const uint32_t lead_full = afd::map_to_rank(full, 0);
       Ring ring(sh.widest);
-      bool ok = true;
+      bool ok = p.wait_cycles != 0;
       Tile tile;
       for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
         const int half = tile.cols() >> 1;
@@ -463,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int w_row = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) : tile.m * kPairRows + (int)rank * kCtaRows;
         for (int kb = 0; kb < p.k_blocks; ++kb, ring.advance()) {
           const int s = ring.slot;
-          if (!(ok = afd::mbar_wait(empty + 8 * s, ring.phase ^ 1, gave_up))) break;
+          if (!(ok = afd::mbar_wait(empty + 8 * s, ring.phase ^ 1, gave_up, p.wait_cycles))) break;
           const uint32_t a = smem + s * ring.bytes, b = a + kHalfBytes, bar = lead_full + 8 * s;
           const int k = kb * (FP8 ? 128 : 64);
           if (afd::elect_one()) {
@@ -478,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       // The pair's last products have read this CTA's operands.
-      ring.last([&](int slot, uint32_t parity) { ok = ok && afd::mbar_wait(empty + 8 * slot, parity, gave_up); });
+      ring.last([&](int slot, uint32_t parity) { ok = ok && afd::mbar_wait(empty + 8 * slot, parity, gave_up, p.wait_cycles); });
       if (!ok && rank == 0) {
         // Copies in flight count on this CTA's barriers: wait for the last ring of them.
         ring.last([&](int slot, uint32_t parity) {
@@ -493,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (rank == 0) {
         Ring ring(sh.widest);
         uint32_t unit = 0;
-        bool ok = true;
+        bool ok = p.wait_cycles != 0;
         Tile tile;
         for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
           const uint32_t idesc = afd::instr_desc(FP8, kPairRows, tile.cols());
@@ -501,11 +502,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const bool opens = FP8 || kb == 0, closes = FP8 || kb == p.k_blocks - 1;
             if (opens) {
               const uint32_t buf = turns.buf(unit), ph = turns.phase(unit) ^ 1;
-              ok = afd::mbar_wait(drained + 8 * buf, ph, gave_up) && afd::mbar_wait(peer_drained + 8 * buf, ph, gave_up);
+              ok = afd::mbar_wait(drained + 8 * buf, ph, gave_up, p.wait_cycles) && afd::mbar_wait(peer_drained + 8 * buf, ph, gave_up, p.wait_cycles);
               if (!ok) break;
             }
             const int s = ring.slot;
-            if (!(ok = afd::mbar_wait(full + 8 * s, ring.phase, gave_up))) break;
+            if (!(ok = afd::mbar_wait(full + 8 * s, ring.phase, gave_up, p.wait_cycles))) break;
             afd::tcgen05_fence_after();
             const uint64_t a = afd::operand_desc(smem + s * ring.bytes);
             const uint64_t b = afd::operand_desc(smem + s * ring.bytes + kHalfBytes);
@@ -521,22 +522,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (closes) ++unit;
           }
         }
-        if (!ok) {
-          // let the products in flight finish before TMEM is freed
-          const long long t0 = clock64();
-          while (clock64() - t0 < 2000000) {
-          }
-        }
       } else {
         // The odd CTA's warp passes on that its accumulators are read: one
         // arrival across the pair instead of one for every draining warp.
         const uint32_t lead = afd::map_to_rank(peer_drained, 0);
         uint32_t unit = 0;
-        bool ok = true;
+        bool ok = p.wait_cycles != 0;
         for (int turn = 0; ok && dealt(turn, pair, pairs) < tiles; ++turn) {
           for (int kb = 0; kb < (FP8 ? p.k_blocks : 1); ++kb, ++unit) {
             const uint32_t buf = turns.buf(unit);
-            if (!(ok = afd::mbar_wait(drained + 8 * buf, turns.phase(unit), gave_up))) break;
+            if (!(ok = afd::mbar_wait(drained + 8 * buf, turns.phase(unit), gave_up, p.wait_cycles))) break;
             if (lane == 0) afd::mbar_arrive_cluster(lead + 8 * buf);
           }
         }
@@ -548,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int u = threadIdx.x - 64;
         const int64_t w_rows = (int64_t)(GATED ? 2 : 1) * p.N / 128;
         uint32_t it = 0;
-        bool ok = true;
+        bool ok = p.wait_cycles != 0;
         Tile tile;
         for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
           const float* xs = p.x_scale + (int64_t)(tile.row + u) * p.k_blocks;
@@ -573,7 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int j = 0; j < kScaleAhead; ++j) {
               if (ok && kb0 + j < p.k_blocks) {
                 const uint32_t s = it % kScaleStages, ph = (it / kScaleStages) & 1;
-                ok = afd::mbar_wait(scale_empty + 8 * s, ph ^ 1, gave_up);
+                ok = afd::mbar_wait(scale_empty + 8 * s, ph ^ 1, gave_up, p.wait_cycles);
                 if (ok) {
                   ++it;
 #pragma unroll
@@ -596,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Turns mine = turns;
     mine.tmem += (uint32_t)(32 * q) << 16;
     uint32_t unit = 0;
-    bool ok = true;
+    bool ok = p.wait_cycles != 0;
     Tile tile;
     for (int turn = 0; ok && next_tile(sh, p, turn, pair, pairs, tiles, &tile); ++turn) {
       const int n0 = GATED ? tile.m * (kPairRows / 2) + (int)rank * (kCtaRows / 2) + 16 * q
@@ -604,7 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Out out = lane_out<GATED>(p, tile, n0, lane);
       if (!FP8) {
         const uint32_t b = turns.buf(unit);
-        ok = afd::mbar_wait(drain_full + 8 * b, turns.phase(unit), gave_up);
+        ok = afd::mbar_wait(drain_full + 8 * b, turns.phase(unit), gave_up, p.wait_cycles);
         if (!ok) break;
         afd::tcgen05_fence_after();
         for (int c = 16 * h; c < tile.cols(); c += 16 * kDrainParts) {
@@ -629,7 +624,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   // Neither CTA leaves while the other may signal it or read its operands.
   __syncthreads();
-  if (threadIdx.x == 0 && *gave_up && p.error) *p.error = AFD_ERR_TIMEOUT;
+  if (*gave_up) {
+    // Whichever role gave up: the pair's copies and products in flight finish
+    // before shared memory and TMEM are freed (a millisecond; they take some us).
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000) {
+    }
+    if (threadIdx.x == 0 && p.error) *p.error = AFD_ERR_TIMEOUT;
+  }
   afd::tcgen05_fence_before();
   afd::cluster_sync_all();
   afd::tcgen05_fence_after();
@@ -637,6 +639,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------- host
+std::atomic<int64_t> g_wait_cycles{afd::kWaitCycles};
+
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
 
 // The driver's encoder, looked up once (a library without a driver loads).
@@ -695,6 +699,12 @@ bool on_device(const void* p, int dev) {
 }
 
 }  // namespace
+
+extern "C" AFD_API afd_status afd_set_product_wait_limit(int64_t cycles) {
+  if (cycles < 0) return AFD_ERR_ARG;
+  g_wait_cycles.store(cycles, std::memory_order_relaxed);
+  return AFD_OK;
+}
 
 extern "C" AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride, const float* x_scale,
                                                  const void* weight, const float* weight_scale, const int32_t* ends,
@@ -761,6 +771,7 @@ extern "C" AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride
   p.m_tiles = m_tiles;
   p.k_blocks = (K + block - 1) / block;
   p.out = static_cast<uint16_t*>(out), p.out_stride = out_stride, p.error = error;
+  p.wait_cycles = g_wait_cycles.load(std::memory_order_relaxed);
   p.vec = N % 2 == 0 && out_stride % 2 == 0 && afd::aligned_to(out, 4);
   const int pairs = (int)(most < sms / 2 ? most : sms / 2);  // no more than there can be tiles
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

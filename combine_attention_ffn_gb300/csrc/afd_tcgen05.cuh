@@ -64,19 +64,19 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// A whole warp waits for a barrier's phase, at most kWaitCycles of this SM's
-// clock (about two seconds). False, for all its lanes: it gave up, or another
-// wait of this CTA did (`gave_up`, in shared memory). The lanes stay together:
-// each waiting on its own and a vote afterwards cost 85 clocks more a wait.
-constexpr long long kWaitCycles = 4000000000ll;
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+// A whole warp waits for a barrier's phase, at most `limit` of this SM's clocks.
+// False, for all its lanes: it gave up, or another wait of this CTA did
+// (`gave_up`, in shared memory). The lanes stay together: each waiting on its
+// own and a vote afterwards cost 85 clocks more a wait.
+constexpr int64_t kWaitCycles = 4000000000ll;  // about two seconds
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up, int64_t limit) {
   if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
   const long long t0 = clock64();
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-    if (clock64() - t0 > kWaitCycles) *gave_up = 1;
+    if (clock64() - t0 > limit) *gave_up = 1;
     __syncwarp();
     if (__any_sync(0xffffffffu, *gave_up)) return false;
   }

@@ -396,7 +396,8 @@ AFD_API afd_status afd_route_layout_noalloc(const int64_t* ids, int32_t num_toke
 
 /* The experts' side of an exchange: the router that makes a dispatch's IDs
  * and weights, and the products a worker computes between worker_receive and
- * worker_reply. These calls take no context and keep no state: they allocate
+ * worker_reply. These calls take no context and keep no state (but for
+ * afd_set_product_wait_limit's limit): they allocate
  * nothing, never synchronize, and may run at the same time on any streams, in
  * any number of captured graphs, as long as their buffers do not overlap.
  * Work is enqueued on `stream`, a stream of the current device, on which
@@ -466,7 +467,8 @@ AFD_API afd_status afd_route_topk(const void* logits, int32_t logits_dtype, int6
  *                 out_stride elements; must not overlap the inputs
  *   error         device int32 [1], or NULL: set to AFD_ERR_TIMEOUT if a
  *                 bounded wait of the kernel gave up (the rows of `out` are
- *                 then unspecified), else left as it was
+ *                 then unspecified), else left as it was. Without it nothing
+ *                 tells of a wait that gave up.
  * Buffers are device memory of the current device (the rows and weights move
  * by bulk copies). x, weight, x_stride and the rows of weight are multiples
  * of 16 bytes; FP8 takes in_features and out_features that are multiples of
@@ -481,6 +483,14 @@ AFD_API afd_status afd_grouped_linear(const void* x, int64_t x_stride, const flo
                                       int32_t in_features, int32_t out_features, int32_t dtype,
                                       int32_t gated, void* out, int64_t out_stride, int32_t* error,
                                       afd_stream stream);
+
+/* Sets the most clocks of an SM for which a wait inside afd_grouped_linear's
+ * kernel lasts before the kernel gives up (default 4,000,000,000, about two
+ * seconds; see `error` there). It holds for the process's calls from then on;
+ * what was captured before keeps its own. 0: the kernel gives up at once,
+ * without a wait or a product: a way to exercise that path.
+ * Errors: AFD_ERR_ARG (negative). */
+AFD_API afd_status afd_set_product_wait_limit(int64_t cycles);
 
 /* The gated activation over received rows, for products whose activation
  * cannot be part of them (afd_adapter_add between the two): for every row r
