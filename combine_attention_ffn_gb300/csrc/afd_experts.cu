@@ -47,7 +47,6 @@
 #include <stdint.h>
 
 #include <atomic>
-#include <climits>
 
 #include "afd.h"
 #include "afd_device.cuh"

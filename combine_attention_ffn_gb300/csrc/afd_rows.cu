@@ -6,8 +6,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <climits>
-
 #include "afd.h"
 #include "afd_device.cuh"
 #include "afd_pointers.cuh"
