@@ -6,7 +6,7 @@ the pages' communication-only numbers), every source collects. The exchange
 is replayed from one CUDA graph; L2 is flushed (a 256 MB write, then a 256 MB
 read) before every timed step, outside the step's events.
 
-Prints ONE JSON line. `value` is microseconds per round trip (lower is
+Prints ONE JSON line (its sweep's rows in full go to stderr). `value` is microseconds per round trip (lower is
 better). With --gpus N > 1 (torchrun), every rank runs an independent replica
 (the exchange does not shard across GPUs) and the slowest rank's time is
 reported. `--impl reference` times the CPU oracle instead, on this host.
@@ -494,6 +494,21 @@ def measure_sweep(torch, afd, W, dev, flush, peak, with_oracle=True):
     return rows
 
 
+def compact_sweep(rows):
+    """The sweep as the headline's line holds it: {workload: [us, us back to
+    back, share of the copy peak from 512 tokens on]}. The rows in full (20 KB)
+    would be most of a line that is read from the end of a log."""
+    out = {}
+    for r in rows:
+        name = f"{r['config']} T={r['T']}"
+        if r["combine"] != "fused":
+            name += " " + r["combine"]
+        if r["variant"] != "full":
+            name += " " + r["variant"]
+        out[name] = [r["us"], r["us_back_to_back"]] + ([] if r["frac"] is None else [r["frac"]])
+    return out
+
+
 def measure_under_load(torch, afd, W, dev, name="2A2F", Ts=(512, 2048), settings=((0, False), (24, False)),
                        n_ex: int = 100, n_gemm: int = 100):
     """The exchange under compute load (afdEP-comm design page, section 14:
@@ -834,12 +849,8 @@ def main():
                          "phase_us": {"dispatch": round(d_cold * 1e3, 2), "receive_reply": round(r_cold * 1e3, 2),
                                       "collect": round(c_cold * 1e3, 2)},
                          "dispatch_phase_frac": round(d_cold_gbs / peak, 4),
-                         "note": "each phase's graph replayed alone with L2 flushed before it: the "
-                                 "combine finds none of the replies in L2"},
-                "note": "us_per_launch/frac: the per-phase graphs replayed one after another after "
-                        "each timed step, L2 flushed before the first (dispatch) phase only, as in "
-                        "the round trip: the combine finds the part of the scatter's rows that is "
-                        "still in L2"}
+                         "note": "each phase's graph alone after an L2 flush"},
+                "note": "the per-phase graphs one after another, L2 flushed before the dispatch only"}
 
     # end to end through the public API, host buffers, copies inside the region
     e2e = None
@@ -879,22 +890,21 @@ def main():
             "algorithmic_bytes": ab["total"],
             "roofline": roofline, "cpu_baseline": cpu, "e2e": e2e, "clocks": clk,
             "gpu_launches": (4 * launches_per_step - (wl.A - 1) + 6 * L2Flush.KERNELS) * args.steps,
-            "gpu_launches_note": "per step: the round-trip graph, the same exchange phase by phase "
-                                 "(one after another, then each after an L2 flush), the round trip "
-                                 "with one batched collect, and the six L2 flushes between them "
-                                 "(afd_l2_flush: three kernels each, outside every event pair)",
+            "gpu_launches_note": "per step: the round trip, its phases twice, the batched collect's "
+                                 "round trip, six L2 flushes of three kernels",
             "back_to_back_us": round(btb_us, 2),
             "eager_us": round(eager_us, 2),
             "collect_all_us": round(batched_us, 2),
-            "collect_all_note": "the same round trip with afd_source_collect_all (one combine "
-                                "launch for every source) in place of one collect per source",
+            "collect_all_note": "afd_source_collect_all in place of one collect per source",
             "wall_s": round(wall, 3),
             "context": pages_context(args.config, wl.T[0], args.combine_mode),
-            "sweep": sweep,
-            "under_load": under_load,
+            "sweep": sweep and compact_sweep(sweep),
+            "under_load": under_load and under_load["rows"],
             "native_digest": native_digest(),
         }
-        print(json.dumps(line))
+        if sweep:  # in full: bytes, the pages' numbers, the oracle's times
+            print(json.dumps({"sweep": sweep, "under_load": under_load}), file=sys.stderr)
+        print(json.dumps(line, separators=(",", ":")))
     if ws > 1:
         torch.distributed.destroy_process_group()
     return 0
@@ -988,12 +998,9 @@ def measure_e2e(torch, buf, wl, inp, dev, steps: int, flush):
             "method": best,
             "copies_us": round(graph_us, 2), "copies_eager_us": round(eager_us, 2),
             "zero_copy_us": round(zc_graph_us, 2), "zero_copy_eager_us": round(zc_eager_us, 2),
-            "note": "per step, from pinned host inputs to pinned host results, through the "
-                    "four calls. copies: cudaMemcpyAsync of x, ids and weights to the device, "
-                    "the calls on device buffers, the outputs copied back. zero-copy: the "
-                    "pinned buffers passed to the calls, which read and write them over the "
-                    "host link. *_us = the step captured once as a CUDA graph and replayed, "
-                    "*_eager_us = issued call by call; value = the faster method"}
+            "note": "per step, pinned host inputs to pinned host results through the four calls; copies: to "
+                    "the device and back; zero-copy: the calls on the pinned buffers; eager: no graph; "
+                    "value = the faster method"}
 
 
 if __name__ == "__main__":
