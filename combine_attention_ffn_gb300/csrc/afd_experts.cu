@@ -26,21 +26,23 @@
 // lanes and one shuffle brings them together.
 //
 // What bounds it, measured (16.4 K rows of 64 experts, K 2048, 2 x 1024 weight
-// rows, gated, BF16: 116 us, 5.5 TB/s of DRAM traffic): the reads through L2,
-// 1.35 GB at 11.6 TB/s, about as fast as they go on this GPU; a decode step
-// (one token a source) streams the touched experts' weights at 5.4 TB/s in
-// 14 us. One lane alone in the loops of the loading and issuing warps, as a
-// first form had it, took 100 clocks an issue and 150 us.
+// rows, gated, BF16: 116 us): no one thing. 1.35 GB come from L2 at 11.6 TB/s,
+// 640 MB from DRAM at 5.5 TB/s, the tensor pipes are 55% busy; without any row
+// loads it takes 106 us, without stores 108. A decode step (one token a source)
+// streams the touched experts' weights: 8 in 15.4 us, 9 in 16.4 at 4.6 TB/s.
+// One lane alone in the loops of the loading and issuing warps, as a first form
+// had it, took 100 clocks an issue and 150 us.
 //
 // FP8: each 128-wide K block has scales of its own, so it gets an accumulator
 // of its own; the draining warps add it, scaled, to FP32 sums in registers:
 // one multiply-add a value, with x_scale * weight_scale multiplied once per
 // row and block by warps 2 and 3, which keep a ring of them in shared memory.
 // 64 sums a thread need more than an even share of the registers, so the
-// other warps hand some of theirs over. This adding bounds it with many rows
-// (the shape above: 108 us against a floor of 50): one multiply-add a value
-// and K block, on issue slots that are 56% busy, with the products waiting for
-// it. Eight warps with twice the sums took 128 us.
+// other warps hand some of theirs over. With many rows (the shape above: 108 us
+// against a floor of 50) the hand-over bounds it: issue slots are 56% busy, the
+// tensor pipes 27%, and with two accumulators in TMEM a block's products wait
+// until all draining warps have added the one before the last. Eight warps with
+// twice the sums took 128 us.
 
 #include <cuda.h>
 #include <cuda_runtime.h>

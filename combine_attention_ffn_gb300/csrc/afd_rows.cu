@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kRowThreads, RANK <= 16 ? 4 : 2) adapter_rows_
 // adapter holds reaches a result.
 // t is FP32; between the two it is kept as two BF16 (16 bits and more).
 // Measured with 16.4 K rows, K = N = 2048, rank 32, eight adapters, two rows in
-// three with one: 49 us (7 + 20 + 17 and the launches) against a floor of 27;
+// three with one: 47.5 us (7 + 20 + 17 and the launches) against a floor of 27;
 // without the grouping, 64 neighbouring rows at a time, 192 us.
 constexpr int kFewRows = 512;
 constexpr int64_t kFewRowsBytes = (int64_t)64 << 20;
