@@ -266,7 +266,8 @@ typedef struct afd_view {
  * dependents start before it has finished (a programmatic trigger in a kernel
  * of the caller's own) must not read this source's `out` either. Calls of
  * this library in between may read and write either: the combine then waits
- * for them, as it does where its `out` shares memory with that of a source
+ * for them (a graph replayed in between has ended before the combine starts),
+ * as it does where its `out` shares memory with that of a source
  * collected before it.
  * Errors: AFD_ERR_STATE (replies missing, or source already collected),
  * AFD_ERR_ARG, AFD_ERR_CUDA. */

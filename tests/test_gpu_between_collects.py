@@ -171,6 +171,49 @@ def test_work_between_two_collects_keeps_its_inputs(name, T):
         buf.close()
 
 
+@pytest.mark.parametrize("name", ["gated", "adapters", "product"])
+def test_a_replayed_graph_between_two_collects(name):
+    """The operator's call is not seen then, but the combine starts only when
+    the replayed graph has ended: results as above, and (phase-timer build) it
+    has nothing left to wait for once its own sums are stored."""
+    T = 64
+    wl = W.named("2A2F", T=T)
+    exp = GH.expected(W.make_inputs(wl), GH.IDENTITY)
+    build.build()
+    prev = afd.load_library()
+    afd.use_library(build.build_timers())
+    try:
+        dev = GH.to_device(W.make_inputs(wl))
+        work = WORK[name](T)
+        before = work.buf.clone()
+        want = work.run().clone()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            work.run()
+        buf = GH.make_buffer(wl)
+        outs = [torch.empty(T, H, dtype=BF16, device="cuda"), work.out1]
+        try:
+            for _ in range(4):
+                work.buf.copy_(before)
+                work.res.zero_()
+                torch.cuda.synchronize()
+                buf.phase_stamps(clear=True)
+                _exchange(buf, wl, dev, g.replay, outs)
+                torch.cuda.synchronize()
+                assert torch.equal(work.res, want)
+                GH.check_outputs(wl, outs, exp)
+                st = buf.phase_stamps()[3].astype(np.int64)
+                st = st[(st[:, :4] > 0).all(1)]
+                assert len(st) and (st[:, 3] - st[:, 2]).max() < 3000  # ns; the operators take 17 us and more
+            del g
+        finally:
+            torch.cuda.synchronize()
+            buf.close()
+    finally:
+        afd._lib = prev
+
+
 @pytest.mark.parametrize("T", [64, 2048])
 def test_memory_freed_before_the_second_collect(T):
     """adapter_add's inputs and its workspace go back to the allocator when
