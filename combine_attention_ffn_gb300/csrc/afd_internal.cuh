@@ -76,8 +76,9 @@ constexpr int kSmallSmemMax = 110 * 1024;
 #endif
 static_assert(kChunk <= (1 << kRankBits), "rank in chunk must fit its field");
 
-// Every kernel of the library asks for the same split of each SM's unified
-// L1 / shared memory. The kernels of one exchange overlap on the same SMs
+// Every kernel of an exchange asks for the same split of each SM's unified
+// L1 / shared memory (the experts' operators do not: the products need nearly
+// all of it as shared memory). The kernels of one exchange overlap on the same SMs
 // through programmatic dependent launch; when their preferred splits differ
 // (the layout needs tens of KB of shared memory, the combines none), an
 // SM cannot take blocks of the next kernel until it has drained and changed
