@@ -11,7 +11,7 @@ of :class:`Buffer` does, and fails loudly if it has not been built.
 __all__ = ["Buffer", "AfdError", "load_library", "route_layout_noalloc",
            "COMBINE_FUSED", "COMBINE_TWO_STAGE", "COMBINE_TWO_STAGE_FP8",
            "route_topk", "grouped_linear", "gated_rows", "adapter_add",
-           "set_product_wait_limit"]
+           "set_product_wait_limit", "norm_rows", "NormRows", "cache_write", "decode_attention"]
 
 
 def __getattr__(name):

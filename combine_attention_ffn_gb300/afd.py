@@ -17,7 +17,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import numpy as np
 import torch
@@ -41,7 +41,8 @@ EXPORTS = ("afd_create", "afd_destroy", "afd_source_dispatch", "afd_source_dispa
            "afd_recv_rows_for_bucket", "afd_version", "afd_route_layout_noalloc",
            "afd_set_wait_limit", "afd_phase_stamps", "afd_l2_flush", "afd_route_topk",
            "afd_grouped_linear", "afd_gated_rows", "afd_adapter_add", "afd_adapter_workspace_bytes",
-           "afd_set_product_wait_limit")
+           "afd_set_product_wait_limit", "afd_norm_rows", "afd_cache_write", "afd_decode_attention",
+           "afd_decode_workspace_bytes")
 
 
 class AfdError(RuntimeError):
@@ -66,6 +67,13 @@ class Recv(ctypes.Structure):
 class View(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
                 ("num_tokens", ctypes.c_int32), ("is_view", ctypes.c_int32)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -111,6 +119,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "afd_adapter_add": (i32, [v, i64, v, i64, v, v, v, v, v, v, v, i32, i32, i64, i32, i32, i32, i32,
                                   i32, v, i64, v, i64, v]),
         "afd_adapter_workspace_bytes": (i64, [i64, i32, i32, i32, i32, i32, i32]),
+        "afd_norm_rows": (i32, [v, i64, v, i64, v, ctypes.c_float, i64, i32, v, i64, v, i64, v, v, v]),
+        "afd_cache_write": (i32, [v, i64, v, i64, v, i64, v, v, v, i32, i32, ctypes.c_float, i64, i32, P(Cache), v, i64, v]),
+        "afd_decode_attention": (i32, [v, i64, P(Cache), v, i64, i32, v, i32, i32, ctypes.c_float, i32, v, i64, v, v, i64, v]),
+        "afd_decode_workspace_bytes": (i64, [i32, i32, i32, i32, i32, i32]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -683,3 +695,213 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
           slots_ptr, scales_ptr, src_ptr, ends_ptr, G, top_k, R, tokens, S, rank, K, N, out.data_ptr(), out_stride,
           None if workspace is None else workspace.data_ptr(), size)
     return out
+
+
+# -- the source's side of an exchange (afd.h: no context, no state) -----------
+# Forward only, as the experts' side.
+
+
+class NormRows(NamedTuple):
+    """What :func:`norm_rows` computed; None for what was not asked for."""
+    rows: Optional[torch.Tensor]      # [T, H] bf16
+    fp8_rows: Optional[torch.Tensor]  # [T, H] float8_e4m3fn
+    scales: Optional[torch.Tensor]    # [T, H/128] f32, the scales of fp8_rows
+    residual: Optional[torch.Tensor]  # [T, H] bf16, x + residual
+
+
+def norm_rows(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+              rows: bool = True, fp8: bool = False, out: Optional[torch.Tensor] = None,
+              residual_out: Optional[torch.Tensor] = None, fp8_out: Optional[torch.Tensor] = None,
+              scale_out: Optional[torch.Tensor] = None, stream=None) -> NormRows:
+    """The rows a source dispatches, from its residual stream: ``r = x +
+    residual``, ``y = r / sqrt(mean(r^2) + eps) * weight``, as a
+    :class:`NormRows`: `rows` (bf16 y, for the router and BF16 exchanges; not
+    with rows=False), with fp8=True `fp8_rows` and `scales` in the form
+    :meth:`Buffer.source_dispatch` takes (H a multiple of 128), and the new
+    `residual` (bf16 r; None without one).
+
+    `x` and `residual` are bf16 [T, H], `weight` bf16 [H]. `out`,
+    `residual_out` (which may be `residual` or `x` itself), `fp8_out` and
+    `scale_out` are where the results go, new tensors by default. See
+    afd_norm_rows in include/afd.h."""
+    if x.dim() != 2:
+        raise AfdError(ERR_ARG, "x must be bfloat16 [T, H]")
+    shape = T, H = x.shape
+    if H > _INT32:
+        raise _too_large(H)
+    if _grad_enabled() and (x.requires_grad or weight.requires_grad
+                            or any(t is not None and t.requires_grad
+                                   for t in (residual, out, residual_out, fp8_out, scale_out))):
+        raise _no_backward()
+    bf16 = torch.bfloat16
+    x_stride = _want_rows(x, "x", bf16, shape)
+    weight_ptr = _want(weight, "weight", bf16, (H,))
+    res_ptr = res_out_ptr = out_ptr = fp8_ptr = scale_ptr = None
+    res_stride = res_out_stride = out_stride = 0
+    if residual is not None:
+        res_stride, res_ptr = _want_rows(residual, "residual", bf16, shape), residual.data_ptr()
+        if residual_out is None:
+            residual_out = _empty(shape, bf16, x.device, stream)
+        res_out_stride, res_out_ptr = _want_rows(residual_out, "residual_out", bf16, shape), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise AfdError(ERR_ARG, "residual_out needs a residual")
+    if rows or out is not None:
+        if out is None:
+            out = _empty(shape, bf16, x.device, stream)
+        out_stride, out_ptr = _want_rows(out, "out", bf16, shape), out.data_ptr()
+    if fp8 or fp8_out is not None or scale_out is not None:
+        if H % 128:
+            raise AfdError(ERR_ARG, f"float8_e4m3fn rows take a multiple of 128 columns, got {H}")
+        if fp8_out is None:
+            fp8_out = _empty(shape, torch.float8_e4m3fn, x.device, stream)
+        if scale_out is None:
+            scale_out = _empty((T, H // 128), torch.float32, x.device, stream)
+        fp8_ptr = _want(fp8_out, "fp8_out", torch.float8_e4m3fn, shape)
+        scale_ptr = _want(scale_out, "scale_out", torch.float32, (T, H // 128))
+    _call("afd_norm_rows", x, stream, x.data_ptr(), x_stride, res_ptr, res_stride, weight_ptr, eps, T, H, res_out_ptr,
+          res_out_stride, out_ptr, out_stride, fp8_ptr, scale_ptr)
+    return NormRows(out, fp8_out, scale_out, residual_out)
+
+
+def _heads(t: torch.Tensor, name: str, tokens: int, dim: int) -> int:
+    """Checks a [T, heads, dim] tensor whose rows may be strided; returns the
+    row stride in elements."""
+    if t.dim() == 3 and t.dtype is torch.bfloat16 and t.shape[0] == tokens and t.shape[2] == dim:
+        row, head, col = t.stride()
+        heads = t.shape[1]
+        if tokens <= 1:
+            row = heads * dim
+        if col == 1 and (head == dim or heads <= 1) and row >= heads * dim:
+            return row
+    raise AfdError(ERR_ARG, f"{name} must be bfloat16 [{tokens}, heads, {dim}] with dense rows, got {t.dtype} {list(t.shape)}")
+
+
+def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale) -> Cache:
+    """The descriptor of a cache."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype \
+            or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise AfdError(ERR_ARG, "k_cache and v_cache must be bfloat16 or float8_e4m3fn [pages, KV heads, page size, head size], "
+                       f"got {k_cache.dtype} {list(k_cache.shape)} and {v_cache.dtype} {list(v_cache.shape)}")
+    pages, heads, page, dim = k_cache.shape
+    if pages > _INT32 or heads > _INT32 or page > _INT32 or dim > _INT32:
+        raise _too_large(pages, heads, page, dim)
+    strides = []
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        s = t.stride()
+        dense = (page * dim, dim, 1)
+        if any(n > 1 and a != b for n, a, b in zip((heads, page, dim), s[1:], dense)):
+            raise AfdError(ERR_ARG, f"{name} must have dense pages, got strides {list(s)}")
+        strides.append(s[0] if pages > 1 else heads * page * dim)
+    ks = vs = None
+    if k_cache.dtype is torch.float8_e4m3fn:
+        if k_scale is None or v_scale is None:
+            raise AfdError(ERR_ARG, "a float8_e4m3fn cache takes k_scale and v_scale")
+        ks = _want(k_scale, "k_scale", torch.float32, (pages, heads, page))
+        vs = _want(v_scale, "v_scale", torch.float32, (pages, heads, page))
+    elif k_scale is not None or v_scale is not None:
+        raise AfdError(ERR_ARG, "a bfloat16 cache takes no scales")
+    return Cache(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, strides[0], strides[1], pages, page, heads, dim,
+                 BF16 if ks is None else FP8_E4M3)
+
+
+def cache_write(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
+                slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *,
+                inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False, factor: float = 1.0,
+                k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """New tokens' rotary positions and their way into a paged cache: returns
+    the rotated queries (`q_out`, which may be `q` itself, a new tensor by
+    default; None where `q` is None) and writes the rotated `k` and `v` to the
+    cache's `slots`.
+
+    `q` is bf16 [T, Hq, D], `k` and `v` [T, Hkv, D] (rows may be strided, as
+    parts of one projection), `positions` and `slots` int64 [T]; a slot is page
+    * page_size + place in the page, and a token with a negative one is not
+    kept. `inv_freq` (float32 [R]) rotates the first 2 R columns of a head by
+    position * inv_freq, pairs (i, R + i) or, interleaved, (2i, 2i + 1); sines
+    and cosines are multiplied by `factor`. None: no rotation. `k_cache` and
+    `v_cache` are [pages, Hkv, page_size, D], bf16, or float8_e4m3fn with
+    `k_scale` and `v_scale` float32 [pages, Hkv, page_size]. See
+    afd_cache_write in include/afd.h."""
+    if _grad_enabled() and any(t is not None and t.requires_grad for t in
+                               (q, k, v, inv_freq, k_cache, v_cache, k_scale, v_scale, q_out)):
+        raise _no_backward()
+    cache = _cache(k_cache, v_cache, k_scale, v_scale)
+    dim, heads = cache.head_dim, cache.num_kv_heads
+    T = k.shape[0] if k.dim() else 0
+    k_stride, v_stride = _heads(k, "k", T, dim), _heads(v, "v", T, dim)
+    if k.shape[1] != heads or v.shape[1] != heads:
+        raise AfdError(ERR_ARG, f"k and v must have the cache's {heads} heads, got {k.shape[1]} and {v.shape[1]}")
+    slots_ptr = _want(slots, "slots", torch.int64, (T,))
+    pos_ptr = freq_ptr = q_ptr = out_ptr = None
+    pairs = Hq = q_stride = out_stride = 0
+    if inv_freq is not None and inv_freq.numel():
+        pairs = inv_freq.numel()
+        if pairs > _INT32:
+            raise _too_large(pairs)
+        freq_ptr = _want(inv_freq, "inv_freq", torch.float32, (pairs,))
+        if positions is None:
+            raise AfdError(ERR_ARG, "inv_freq needs positions")
+        pos_ptr = _want(positions, "positions", torch.int64, (T,))
+    if q is not None:
+        q_stride, Hq = _heads(q, "q", T, dim), q.shape[1]
+        if Hq > _INT32:
+            raise _too_large(Hq)
+        if q_out is None:
+            q_out = _empty((T, Hq, dim), torch.bfloat16, q.device, stream)
+        out_stride = _heads(q_out, "q_out", T, dim)
+        if q_out.shape[1] != Hq:
+            raise AfdError(ERR_ARG, f"q_out must have {Hq} heads, got {q_out.shape[1]}")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise AfdError(ERR_ARG, "q_out needs q")
+    _call("afd_cache_write", k, stream, q_ptr, q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, pos_ptr, slots_ptr,
+          freq_ptr, pairs, bool(interleaved), factor, T, Hq, cache, out_ptr, out_stride)
+    return q_out
+
+
+def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                     lengths: torch.Tensor, *, scale: Optional[float] = None, window: int = 0,
+                     k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, return_lse: bool = False,
+                     stream=None):
+    """Attention of one new token a sequence over its paged cache: bf16 [B, Hq,
+    D]; with return_lse, or `lse` given, ``(out, lse)``, lse float32 [B, Hq]
+    (natural logarithm of the sum of the scores' exponentials).
+
+    `q` is bf16 [B, Hq, D]; the caches (and their scales) as in
+    :func:`cache_write`, Hq a multiple of their heads. `page_table` (int32 [B,
+    max_pages]) has each sequence's pages, `lengths` (int32 [B]) its tokens, the
+    new one counted; with `window` only that many last ones are seen. `scale`
+    defaults to D ** -0.5. A sequence that sees nothing gets zeros and an lse of
+    -inf. See afd_decode_attention in include/afd.h."""
+    if _grad_enabled() and any(t is not None and t.requires_grad for t in (q, k_cache, v_cache, k_scale, v_scale, out, lse)):
+        raise _no_backward()
+    cache = _cache(k_cache, v_cache, k_scale, v_scale)
+    dim, heads = cache.head_dim, cache.num_kv_heads
+    if q.dim() != 3 or page_table.dim() != 2:
+        raise AfdError(ERR_ARG, "q must be [B, Hq, D] and page_table [B, max_pages]")
+    B, Hq = q.shape[0], q.shape[1]
+    width = page_table.shape[1]
+    if B > _INT32 or Hq > _INT32 or width > _INT32 or not -_INT32 <= window <= _INT32:
+        raise _too_large(B, Hq, width, window)
+    q_stride = _heads(q, "q", B, dim)
+    table_stride = _want_rows(page_table, "page_table", torch.int32, (B, width))
+    lengths_ptr = _want(lengths, "lengths", torch.int32, (B,))
+    if out is None:
+        out = _empty((B, Hq, dim), torch.bfloat16, q.device, stream)
+    out_stride = _heads(out, "out", B, dim)
+    if out.shape[1] != Hq:
+        raise AfdError(ERR_ARG, f"out must have {Hq} heads, got {out.shape[1]}")
+    if lse is None and return_lse:
+        lse = _empty((B, Hq), torch.float32, q.device, stream)
+    lse_ptr = None if lse is None else _want(lse, "lse", torch.float32, (B, Hq))
+    size = (_lib or load_library()).afd_decode_workspace_bytes(B, Hq, heads, dim, width, cache.page_size)
+    workspace = None
+    if size > 0:
+        on = q.device if q.is_cuda else torch.device("cuda", _current_device())
+        workspace = _empty(size, torch.uint8, on, stream)
+    _call("afd_decode_attention", q, stream, q.data_ptr(), q_stride, cache, page_table.data_ptr(), table_stride, width,
+          lengths_ptr, B, Hq, dim ** -0.5 if scale is None else scale, window, out.data_ptr(), out_stride, lse_ptr,
+          None if workspace is None else workspace.data_ptr(), size)
+    return (out, lse) if lse is not None else out

@@ -557,6 +557,131 @@ AFD_API int64_t afd_adapter_workspace_bytes(int64_t num_rows, int32_t num_tokens
                                             int32_t num_slots, int32_t rank, int32_t in_features,
                                             int32_t out_features);
 
+/* The Attention source's side of an exchange: what a source runs around its
+ * attention before it dispatches, and the attention of a decode step itself.
+ * As the experts' side, these calls take no context, keep no state, allocate
+ * nothing, never synchronize, may run at the same time on any streams and in any
+ * number of captured graphs as long as what they write does not overlap, and work
+ * on a stream of the current device, on which every buffer must be reachable.
+ * They take at most 2^31 - 2^20 - 1 rows or tokens.
+ * Where values go to E4M3, a vector of them shares one FP32 scale,
+ *   scale = max(max |v| / 448, 2^-100), value = e4m3(v / scale),
+ * rounded to nearest even; all of a vector with an infinity or a NaN decodes to
+ * NaN. */
+
+/* The rows a source dispatches, from its residual stream:
+ *   r = x + residual                     residual_out = bf16(r)
+ *   y = r / sqrt(mean(r^2) + eps) * weight        out = bf16(y)
+ *   and y in E4M3 with a scale for each block of 128 columns, in the form
+ *   afd_source_dispatch takes (fp8_out, scale_out)
+ * in FP32, from the unrounded r; the sum of squares has to be finite in FP32.
+ *   x             device BF16 [num_rows, features], row stride x_stride elements
+ *   residual      device BF16 [num_rows, features], row stride residual_stride,
+ *                 or NULL (then residual_out is NULL too)
+ *   weight        device BF16 [features]
+ *   residual_out  device BF16, or NULL; may be residual or x itself (the same
+ *                 address and stride)
+ *   out           device BF16, or NULL; may be x or residual itself
+ *   fp8_out       device E4M3 [num_rows, features], contiguous, or NULL
+ *   scale_out     device FP32 [num_rows, features/128], contiguous; with fp8_out
+ * One output at least. Outputs must not overlap the inputs or each other in any
+ * other way. fp8_out takes features that are multiples of 128, up to 32,768, and
+ * rows of every array, and the weight, on 16-byte boundaries (fp8_out: 8).
+ * Features are at most 2^24. Buffers may be device, managed or page-locked host
+ * memory.
+ * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (limits), AFD_ERR_CUDA. */
+AFD_API afd_status afd_norm_rows(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                 const void* weight, float eps, int64_t num_rows, int32_t features,
+                                 void* residual_out, int64_t residual_out_stride, void* out, int64_t out_stride,
+                                 void* fp8_out, float* scale_out, afd_stream stream);
+
+/* A paged cache of keys and values. Token j of a sequence lies in the
+ * sequence's page j / page_size at j % page_size; a page holds each KV head's
+ * tokens one after another. */
+typedef struct afd_cache {
+  void* k;               /* device [num_pages][num_kv_heads][page_size][head_dim], BF16 or E4M3 bytes */
+  void* v;               /* the same of the values */
+  float* k_scale;        /* device FP32 [num_pages][num_kv_heads][page_size] (E4M3), else NULL */
+  float* v_scale;        /* not negative; zero or at least 2^-100 */
+  int64_t k_page_stride; /* elements from a page to the next (the rest is dense): keys and values may */
+  int64_t v_page_stride; /*   be two halves of one allocation's pages */
+  int32_t num_pages;
+  int32_t page_size;     /* tokens of a page, any number */
+  int32_t num_kv_heads;
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t dtype;         /* AFD_BF16 or AFD_FP8_E4M3 */
+} afd_cache;
+
+/* New tokens' rotary positions and their way into a cache: for every token t
+ *   q_out[t] = rotated q[t];  the cache's row slots[t] = rotated k[t], and v[t]
+ * Pair i < rotary_pairs of a head's columns, (i, rotary_pairs + i), or (2i, 2i + 1)
+ * with interleaved = 1, becomes
+ *   (a cos - b sin, b cos + a sin) * factor, angle = positions[t] * inv_freq[i]
+ * with the angle and its remainder in 64 bits (positions to 2^53); the head's other
+ * columns stay. A change of the frequencies for long contexts is in inv_freq and
+ * factor. BF16 caches hold the rotated values rounded, E4M3 ones a scale for
+ * each token and head, of the FP32 values.
+ *   q          device BF16 [num_tokens, num_q_heads, head_dim], row stride
+ *              q_stride elements; not used with num_q_heads = 0
+ *   k, v       device BF16 [num_tokens, num_kv_heads, head_dim], row strides
+ *   positions, inv_freq  device int64 [num_tokens] and FP32 [rotary_pairs]; not
+ *              used with rotary_pairs = 0
+ *   slots      device int64 [num_tokens]: page * page_size + place in the page.
+ *              A token whose slot is negative or beyond the cache (a bucket's
+ *              padding) leaves the cache as it is; its q_out is written. Two
+ *              tokens with the same slot leave parts of either there.
+ *   q_out      device BF16 [num_tokens, num_q_heads, head_dim], row stride
+ *              q_out_stride; may be q itself (the same address and stride)
+ * Limits: at most 1,024 heads of either kind; q, k, v, q_out, the caches' pages
+ * and the strides multiples of 16 bytes; num_pages * page_size below 2^31.
+ * Buffers may be device, managed or page-locked host memory.
+ * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (limits), AFD_ERR_CUDA. */
+AFD_API afd_status afd_cache_write(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                   const void* v, int64_t v_stride, const int64_t* positions,
+                                   const int64_t* slots, const float* inv_freq, int32_t rotary_pairs,
+                                   int32_t interleaved, float factor, int64_t num_tokens, int32_t num_q_heads,
+                                   const afd_cache* cache, void* q_out, int64_t q_out_stride, afd_stream stream);
+
+/* Attention of one new token a sequence over its cache: for every sequence b and
+ * query head h, with KV head h / (num_q_heads / num_kv_heads),
+ *   s_j = scale * q[b][h] . k_j,  p = softmax(s) over the tokens j that are seen,
+ *   out[b][h] = sum over j of p_j v_j,  lse[b][h] = log(sum over j of exp(s_j))
+ * Seen are j < lengths[b], and j >= lengths[b] - window where window > 0; the new
+ * token's own key and value are in the cache (afd_cache_write) and counted. A
+ * page number outside [0, num_pages) hides its tokens, a length beyond the
+ * table's pages ends there. A sequence that sees nothing (a bucket's padding:
+ * length 0) gets out = +0 and lse = -infinity. What the cache holds in places
+ * that are not seen is not read.
+ * Sums, maxima and exponentials are FP32; the probabilities are rounded for the
+ * product with the values (BF16 caches: to two BF16 parts, 16 bits; E4M3: to
+ * FP16, weighted by the values' scales first). Which tokens are summed together depends
+ * on all lengths of the call, so the last bits of a sequence's result may change
+ * with what it is batched with; the same call gives the same bits.
+ *   q           device BF16 [num_seqs, num_q_heads, head_dim], row stride q_stride
+ *   page_table  device int32 [num_seqs, max_pages], row stride table_stride
+ *   lengths     device int32 [num_seqs]
+ *   out         device BF16 [num_seqs, num_q_heads, head_dim], row stride
+ *               out_stride; must not overlap the inputs
+ *   lse         device FP32 [num_seqs, num_q_heads] (natural logarithm), or NULL
+ *   workspace   device, workspace_bytes >= afd_decode_workspace_bytes(...), 16-byte
+ *               aligned (NULL where that is 0); its contents need not be set and
+ *               mean nothing afterwards. Calls that may run at the same time
+ *               (other streams, other captured graphs) need one each.
+ * Limits: num_q_heads a multiple of num_kv_heads, at most 1,024; max_pages *
+ * page_size below 2^31 - 2^10; q, out and their strides multiples of 16 bytes.
+ * Buffers may be device, managed or page-locked host memory.
+ * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (limits), AFD_ERR_CUDA. */
+AFD_API afd_status afd_decode_attention(const void* q, int64_t q_stride, const afd_cache* cache,
+                                        const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                                        const int32_t* lengths, int32_t num_seqs, int32_t num_q_heads, float scale,
+                                        int32_t window, void* out, int64_t out_stride, float* lse,
+                                        void* workspace, int64_t workspace_bytes, afd_stream stream);
+
+/* Bytes of workspace for afd_decode_attention with these sizes (-1 for ones it
+ * does not take; 0 where nothing is split). */
+AFD_API int64_t afd_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                           int32_t head_dim, int32_t max_pages, int32_t page_size);
+
 /* Library version, (major << 16) | minor. */
 AFD_API int32_t afd_version(void);
 
