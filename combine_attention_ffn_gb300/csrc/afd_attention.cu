@@ -13,13 +13,14 @@
 // open by a second kernel.
 //
 // A warp works alone: its own ring of tiles in shared memory, filled by
-// asynchronous copies a few tiles ahead, its own running maximum and sum. The
-// products are m16n8k16 on tensor cores with the query heads as the 16 rows;
-// the rate of mma.sync is far more than the traffic needs, and its register
-// operands let the probabilities go from one product to the next in place. The
-// order of columns inside a product is free as long as both sides agree, so a
-// lane takes 16 neighbouring bytes of a key at a time, and 16 of four tokens'
-// values, whose pairs are then interleaved in registers.
+// asynchronous copies ahead of their use, its own running maximum and sum. The
+// products are m16n8k16 on tensor cores, transposed: 16 tokens by 8 query heads
+// for the scores, 16 columns by 8 heads for the result, so that no row of a
+// product is empty with up to eight heads; probabilities pass from one to the
+// other through registers (one 8 x 8 transposition each). The rate of mma.sync is
+// more than the traffic needs. The order of columns inside a product is free as
+// long as both sides agree, so a lane takes 16 neighbouring bytes of a key at a
+// time, and 16 of four tokens' values, whose pairs are then interleaved.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -33,8 +34,9 @@
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kRows = 16;       // query heads of a product
-constexpr int kMaxBlocks = 256;
+constexpr int kMaxBlocks = 160;
+constexpr int kMaxWarps = 16;
+constexpr float kLazy = 8.f;  // log2 of how far a score may pass the running maximum before that moves
 constexpr float kLn2 = 0.693147180559945f;
 
 // A split (sequence, head): where its last part is (see join).
@@ -52,14 +54,16 @@ struct AttentionParams {
   int64_t table_stride;
   int32_t max_pages;
   const int32_t* lengths;
-  int32_t B, Hq, Hkv, G, chunks;  // chunks: of at most 16 query heads, all KV heads'
+  int32_t B, Hq, Hkv, G, chunks;  // chunks: of at most 8 or 16 query heads, all KV heads'
+  int32_t page_shift;             // log2 of the page size, or -1
   float scale_log2;
   int32_t window;
   uint16_t* out;
   int64_t out_stride;
   float* lse;
   Split* splits;  // workspace, [blocks]
-  float* parts;   // workspace, [blocks][2][kRows][D + 2]: O, then the maxima and the sums
+  float* parts;   // workspace, [blocks][2][rows][D + 2]: O, then the maxima and the sums
+  float* kept;    // workspace, [blocks * warps][rows][D]: O of warps' first parts
 };
 
 template <int D, bool FP8>
@@ -72,16 +76,18 @@ struct Shape {
   static constexpr int H = D / 8 / E;                        // ... and how many such groups
 };
 
-// Warps of a block and stages of a warp's ring; HI: more than eight query heads.
-template <int D, bool FP8, bool HI>
+// Warps of a block and stages of a warp's ring; NH: query heads of a chunk, in
+// eights.
+template <int D, bool FP8, int NH>
 struct Layout {
   using S = Shape<D, FP8>;
-  static constexpr int kWarps = 6;
-  static constexpr int kPart = (HI ? 16 : 8) * D * 4;
-  static constexpr int kStages = (216 * 1024 / kWarps - kPart) / S::kStage < 4 ? (216 * 1024 / kWarps - kPart) / S::kStage : 4;
+  static constexpr int kWarps = S::kStage > 8000 ? 12 : 16;
+  static constexpr int kStages = S::kStage > 8000 ? 2 : 3;
+  static constexpr int kRows = 8 * NH;
   static constexpr int kRing = kStages * S::kStage;
-  static constexpr int kShared = kWarps * (kRing + kPart);
-  static_assert(kStages >= 2 && kRing >= kPart, "a part goes where the ring was");
+  static constexpr int kShared = kWarps * kRing;
+  static_assert(kStages >= 2 && kRing >= kRows * D * 4, "a part goes where the ring was");
+  static_assert(kWarps <= kMaxWarps);
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -98,15 +104,15 @@ template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <bool F16>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint32_t (&b)[2]) {
   if (F16)
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
   else
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
 }
 
 // Two E4M3 values (the low half of v, or the high one) as two FP16, exactly.
@@ -139,13 +145,27 @@ __device__ __forceinline__ float log2_of(float v) {
   return r;
 }
 
+// Over the eight lanes that hold other tokens of the same heads.
+__device__ __forceinline__ float tokens_max(float v) {
+#pragma unroll
+  for (int d = 4; d <= 16; d <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
+  return v;
+}
+__device__ __forceinline__ float tokens_sum(float v) {
+#pragma unroll
+  for (int d = 4; d <= 16; d <<= 1) v += __shfl_xor_sync(kFull, v, d);
+  return v;
+}
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(kFull, v, 1));
   return fmaxf(v, __shfl_xor_sync(kFull, v, 2));
 }
-__device__ __forceinline__ float quad_sum(float v) {
-  v += __shfl_xor_sync(kFull, v, 1);
-  return v + __shfl_xor_sync(kFull, v, 2);
+
+// An 8 x 8 matrix of 16-bit values, two of a row a lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 // Where 16-byte chunk `chunk` of a tile's row lies: eight lanes that read the
@@ -201,30 +221,31 @@ struct Lookup {
 template <int TILE>
 __device__ __forceinline__ Lookup look_up(const AttentionParams& p, const Cursor<TILE>& c, int lane) {
   Lookup l;
-  const int token = c.tile * TILE + lane;
-  l.in = lane < TILE && token >= c.span.from && token < c.span.len;
+  const int token = c.tile * TILE + (lane & (TILE - 1));
+  l.in = token >= c.span.from && token < c.span.len;
   l.chunk = c.chunk;
   l.page = 0;
   l.at = 0;
   if (l.in) {
-    const uint32_t page = (uint32_t)token / (uint32_t)p.cache.page_size;
+    const uint32_t page = p.page_shift >= 0 ? (uint32_t)token >> p.page_shift : (uint32_t)token / (uint32_t)p.cache.page_size;
     l.at = token - (int)(page * (uint32_t)p.cache.page_size);
     l.page = p.table[c.b * p.table_stride + page];
   }
   return l;
 }
 
-template <int D, bool FP8, bool HI>
-__global__ void __launch_bounds__(Layout<D, FP8, HI>::kWarps * 32, 1) decode_attention_kernel(const AttentionParams p) {
+template <int D, bool FP8, int NH>
+__global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_attention_kernel(const AttentionParams p) {
   using S = Shape<D, FP8>;
-  using Y = Layout<D, FP8, HI>;
-  constexpr int TILE = S::kTile, ROW = S::kRow, E = S::E, H = S::H, NT = TILE / 8, W = Y::kWarps;
-  constexpr int THREADS = W * 32, R = HI ? 2 : 1;  // R: rows of a lane (g, g + 8)
+  using Y = Layout<D, FP8, NH>;
+  constexpr int TILE = S::kTile, ROW = S::kRow, E = S::E, H = S::H, TB = TILE / 16, W = Y::kWarps, ROWS = Y::kRows;
+  constexpr int THREADS = W * 32;
+  constexpr uint32_t ALL = kFull;  // every token of a tile (of 16: twice)
   extern __shared__ __align__(128) uint8_t shared[];
   __shared__ int64_t before[THREADS + 1];          // tiles before each thread's sequences
   __shared__ uint32_t seen[W][Y::kStages];         // a staged tile's tokens that count
-  __shared__ float part_m[W][2][kRows], part_l[W][2][kRows];
-  __shared__ int seg_a[W], seg_b[W], done_a[W];
+  __shared__ float part_m[W][2][ROWS], part_l[W][2][ROWS];
+  __shared__ int seg_a[W], seg_b[W], done_a[W], away_a[W];
   __shared__ int64_t end_b[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
 
@@ -270,8 +291,8 @@ __global__ void __launch_bounds__(Layout<D, FP8, HI>::kWarps * 32, 1) decode_att
   }
 
   uint8_t* ring = shared + warp * Y::kRing;
-  float* kept = reinterpret_cast<float*>(shared + W * Y::kRing + warp * Y::kPart);
-  if (lane == 0) seg_a[warp] = seg_b[warp] = -1, done_a[warp] = 0, end_b[warp] = 0;
+  float* kept = p.kept + (int64_t)worker * ROWS * D;
+  if (lane == 0) seg_a[warp] = seg_b[warp] = -1, done_a[warp] = away_a[warp] = 0, end_b[warp] = 0;
 
   if (lo < hi) {
     // ---- where the share begins
@@ -297,6 +318,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, HI>::kWarps * 32, 1) decode_att
     }
     const int tiles = (int)(hi - lo);
     const int groups = p.chunks / p.Hkv;  // chunks of a KV head
+    const bool tiled = p.cache.page_size % TILE == 0;  // a tile is in one page
 
     Cursor<TILE> ahead = at;
     Lookup next = look_up(p, ahead, lane);
@@ -311,17 +333,30 @@ __global__ void __launch_bounds__(Layout<D, FP8, HI>::kWarps * 32, 1) decode_att
         if (lane == 0) seen[warp][stage] = mask;
         const int head = next.chunk / groups;
         const int64_t row = (int64_t)head * p.cache.page_size + next.at;
-        const int64_t k_off = in ? next.page * p.cache.k_page_bytes + row * ROW : 0;
-        const int64_t v_off = in ? next.page * p.cache.v_page_bytes + row * ROW : 0;
         constexpr int CH = ROW / 16;  // chunks of a row
+        if (tiled && mask == ALL) {
+          // one run of bytes: the same for every lane but for its own 16
+          const int64_t first = (row - (lane & (TILE - 1))) * ROW + lane * 16;
+          const uint8_t* k = p.cache.k + next.page * p.cache.k_page_bytes + first;
+          const uint8_t* v = p.cache.v + next.page * p.cache.v_page_bytes + first;
 #pragma unroll
-        for (int j = 0; j < S::kBytes / 512; ++j) {
-          const int idx = j * 32 + lane, r = idx / CH, ch = idx % CH;
-          const int64_t ko = __shfl_sync(kFull, k_off, r), vo = __shfl_sync(kFull, v_off, r);
-          const bool ok = (mask >> r) & 1u;
-          const uint32_t to = dst + swizzled<ROW>(r, ch);
-          copy16(to, p.cache.k + ko + ch * 16, ok);
-          copy16(to + S::kBytes, p.cache.v + vo + ch * 16, ok);
+          for (int j = 0; j < S::kBytes / 512; ++j) {
+            const uint32_t to = dst + swizzled<ROW>((j * 32 + lane) / CH, (j * 32 + lane) % CH);
+            copy16(to, k + j * 512, true);
+            copy16(to + S::kBytes, v + j * 512, true);
+          }
+        } else {
+          const int64_t k_off = in ? next.page * p.cache.k_page_bytes + row * ROW : 0;
+          const int64_t v_off = in ? next.page * p.cache.v_page_bytes + row * ROW : 0;
+#pragma unroll 1
+          for (int j = 0; j < S::kBytes / 512; ++j) {
+            const int r = (j * 32 + lane) / CH, ch = (j * 32 + lane) % CH;
+            const int64_t ko = __shfl_sync(kFull, k_off, r), vo = __shfl_sync(kFull, v_off, r);
+            const bool ok = (mask >> r) & 1u;
+            const uint32_t to = dst + swizzled<ROW>(r, ch);
+            copy16(to, p.cache.k + ko + ch * 16, ok);
+            copy16(to + S::kBytes, p.cache.v + vo + ch * 16, ok);
+          }
         }
         if (FP8) {
           const int64_t o = in ? (int64_t)next.page * p.Hkv * p.cache.page_size + row : 0;
@@ -338,64 +373,63 @@ __global__ void __launch_bounds__(Layout<D, FP8, HI>::kWarps * 32, 1) decode_att
 #pragma unroll 1
     for (int i = 0; i < Y::kStages - 1; ++i) issue(i);
 
-    uint32_t qa[D / 16][4];
-    float row_scale[2];
-    float o[D / 8][4];
-    float m[2], l[2];
+    uint32_t qb[NH][D / 16][2];
+    float row_scale[NH][2];
+    float o[D / 16][NH][4];
+    float m[NH][2], l[NH][2];  // of heads 2 c and 2 c + 1, l this lane's tokens' part
     bool began = at.tile == at.span.first;  // the segment's first tile is this warp's
 
     // Query heads of the segment, zeros beyond the KV head's.
     auto load_q = [&]() {
       const int head = at.chunk / groups, sub = at.chunk % groups;
-      const int rows = min(p.G - sub * kRows, kRows);
-      const uint16_t* q = p.q + at.b * p.q_stride + (int64_t)(head * p.G + sub * kRows) * D;
-      uint4 v[R][D / 32];
+      const int rows = min(p.G - sub * ROWS, ROWS);
+      const uint16_t* q = p.q + at.b * p.q_stride + (int64_t)(head * p.G + sub * ROWS) * D;
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int n = 0; n < NH; ++n) {
+        uint4 v[D / 32];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           // chunk i of this lane, as the keys' (16 bytes of theirs are 8 or 16 columns)
           const int col = FP8 ? (D == 128 ? (2 * c + i / 2) * 16 + i % 2 * 8 : c * 16 + i * 8)
                               : (D == 128 ? (2 * c + (i & 1) + 8 * (i >> 1)) * 8 : (2 * c + i) * 8);
-          v[r][i] = g + 8 * r < rows ? *reinterpret_cast<const uint4*>(q + (g + 8 * r) * D + col) : make_uint4(0, 0, 0, 0);
+          v[i] = g + 8 * n < rows ? *reinterpret_cast<const uint4*>(q + (g + 8 * n) * D + col) : make_uint4(0, 0, 0, 0);
         }
+        row_scale[n][0] = row_scale[n][1] = p.scale_log2;
+        if (FP8) {
+          // FP16 queries: the row's power of two taken out, so that the largest
+          // lies in [1, 2) and the others keep their digits down to 2^-24 of it.
+          float most = 0.f;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        row_scale[r] = p.scale_log2;
-        if (!FP8 || r >= R) continue;
-        // FP16 queries: the row's power of two taken out, so that the largest
-        // lies in [1, 2) and the others keep their digits down to 2^-24 of it.
-        float most = 0.f;
+          for (int i = 0; i < D / 32; ++i) {
+            float f[8];
+            afd::bf16x8_to_float(v[i], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
+          }
+          most = quad_max(most);
+          const int ex = min(max((int)(__float_as_uint(most) >> 23) - 127, -120), 120);
+          const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+          const float up = p.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23);
+          row_scale[n][0] = __shfl_sync(kFull, up, 8 * c);  // (a lane of head 2 c)
+          row_scale[n][1] = __shfl_sync(kFull, up, 8 * c + 4);
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            float f[8];
+            afd::bf16x8_to_float(v[i], f);
+            v[i] = make_uint4(pack_f16(f[0] * down, f[1] * down), pack_f16(f[2] * down, f[3] * down),
+                              pack_f16(f[4] * down, f[5] * down), pack_f16(f[6] * down, f[7] * down));
+          }
+        }
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          float f[8];
-          afd::bf16x8_to_float(v[r % R][i], f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
+          qb[n][2 * i][0] = v[i].x, qb[n][2 * i][1] = v[i].y;
+          qb[n][2 * i + 1][0] = v[i].z, qb[n][2 * i + 1][1] = v[i].w;
         }
-        most = quad_max(most);
-        int ex = (int)(__float_as_uint(most) >> 23) - 127;
-        ex = min(max(ex, -120), 120);
-        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-        row_scale[r] = p.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          float f[8];
-          afd::bf16x8_to_float(v[r % R][i], f);
-          v[r % R][i] = make_uint4(pack_f16(f[0] * down, f[1] * down), pack_f16(f[2] * down, f[3] * down),
-                               pack_f16(f[4] * down, f[5] * down), pack_f16(f[6] * down, f[7] * down));
-        }
+        for (int d = 0; d < D / 16; ++d) o[d][n][0] = o[d][n][1] = o[d][n][2] = o[d][n][3] = 0.f;
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
       }
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 a = v[0][i], b = HI ? v[R - 1][i] : make_uint4(0, 0, 0, 0);
-        qa[2 * i][0] = a.x, qa[2 * i][1] = b.x, qa[2 * i][2] = a.y, qa[2 * i][3] = b.y;
-        qa[2 * i + 1][0] = a.z, qa[2 * i + 1][1] = b.z, qa[2 * i + 1][2] = a.w, qa[2 * i + 1][3] = b.w;
-      }
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-      m[0] = m[1] = -INFINITY;
-      l[0] = l[1] = 0.f;
     };
 
     bool fresh = true;
@@ -411,141 +445,149 @@ __global__ void __launch_bounds__(Layout<D, FP8, HI>::kWarps * 32, 1) decode_att
       const uint8_t* vs = ks + S::kBytes;
       const uint32_t mask = seen[warp][stage];
 
-      // ---- scores
-      float s[NT][4];
+      // ---- scores: token 16 t + g (and + 8), heads 8 n + 2 c (and + 1)
+      float s[TB][NH][4];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int n = 0; n < NH; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
 #pragma unroll
       for (int ii = 0; ii < ROW / 64; ++ii) {
         const int chunk = ROW == 256 ? 2 * c + (ii & 1) + 8 * (ii >> 1) : ROW == 128 ? 2 * c + ii : c;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const uint4 kv = *reinterpret_cast<const uint4*>(ks + swizzled<ROW>(8 * j + g, chunk));
+        for (int t = 0; t < TB; ++t) {
+          const uint4 x = *reinterpret_cast<const uint4*>(ks + swizzled<ROW>(16 * t + g, chunk));
+          const uint4 y = *reinterpret_cast<const uint4*>(ks + swizzled<ROW>(16 * t + 8 + g, chunk));
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
           if (FP8) {
-            mma<true>(s[j], qa[(4 * ii) % (D / 16)], half2_of<0>(kv.x), half2_of<1>(kv.x));
-            mma<true>(s[j], qa[(4 * ii + 1) % (D / 16)], half2_of<0>(kv.y), half2_of<1>(kv.y));
-            mma<true>(s[j], qa[(4 * ii + 2) % (D / 16)], half2_of<0>(kv.z), half2_of<1>(kv.z));
-            mma<true>(s[j], qa[(4 * ii + 3) % (D / 16)], half2_of<0>(kv.w), half2_of<1>(kv.w));
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t a0 = half2_of<0>(xs[w]), a1 = half2_of<0>(ys[w]), a2 = half2_of<1>(xs[w]), a3 = half2_of<1>(ys[w]);
+#pragma unroll
+              for (int n = 0; n < NH; ++n) mma<true>(s[t][n], a0, a1, a2, a3, qb[n][(4 * ii + w) % (D / 16)]);
+            }
           } else {
-            mma<false>(s[j], qa[(2 * ii) % (D / 16)], kv.x, kv.y);
-            mma<false>(s[j], qa[(2 * ii + 1) % (D / 16)], kv.z, kv.w);
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+              for (int n = 0; n < NH; ++n)
+                mma<false>(s[t][n], xs[2 * w], ys[2 * w], xs[2 * w + 1], ys[2 * w + 1], qb[n][(2 * ii + w) % (D / 16)]);
           }
         }
       }
       // ---- softmax. E4M3: the weight of a token's values is p * its scale, so
-      // the running maximum is that of s + log2(scale): the FP16 weights are at
-      // most 1, and what they lose is small beside the largest contribution.
-      float top[2] = {m[0], m[1]};
-      float vscale[NT][2];
+      // the running maximum is that of s + log2(scale): the FP16 weights stay
+      // small, and what they lose is small beside the largest contribution. The
+      // maximum moves, and what was summed is rescaled, only where a score is
+      // kLazy above it; weights are then at most 2^kLazy.
+      float top[NH][2], vscale[TB][2];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int n = 0; n < NH; ++n) top[n][0] = top[n][1] = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int tok = 8 * j + 2 * c + x;
-          const bool in = (mask >> tok) & 1u;
+      for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int tok = 16 * t + 8 * y + g;
           float kscale = 1.f, lift = 0.f;
           if (FP8) {
             kscale = reinterpret_cast<const float*>(vs + S::kBytes)[tok];
-            vscale[j][x] = reinterpret_cast<const float*>(vs + S::kBytes)[TILE + tok];
-            lift = fmaxf(log2_of(vscale[j][x]), -120.f);
+            vscale[t][y] = reinterpret_cast<const float*>(vs + S::kBytes)[TILE + tok];
+            lift = fmaxf(log2_of(vscale[t][y]), -100.f);
           }
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            float& v = s[j][2 * r + x];
-            v = in ? v * row_scale[r] * kscale : -INFINITY;
-            top[r] = fmaxf(top[r], v + lift);
-          }
+          for (int n = 0; n < NH; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float& v = s[t][n][2 * y + x];
+              v *= FP8 ? row_scale[n][x] * kscale : row_scale[n][x];
+              if (mask != ALL) v = (mask >> tok) & 1u ? v : -INFINITY;
+              top[n][x] = fmaxf(top[n][x], v + lift);
+            }
         }
-      float minus[2];
-      bool moved = false;
+      bool over = false;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        top[r] = quad_max(top[r]);
-        moved |= top[r] != m[r];
-        minus[r] = top[r] == -INFINITY ? 0.f : top[r];
-      }
-      if (__any_sync(kFull, moved)) {
+      for (int n = 0; n < NH; ++n) over |= top[n][0] > m[n][0] + kLazy || top[n][1] > m[n][1] + kLazy;
+      if (__any_sync(kFull, over)) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float f = m[r] == -INFINITY ? 0.f : exp2_of(m[r] - minus[r]);
-          m[r] = top[r];
-          l[r] *= f;
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) o[n][2 * r] *= f, o[n][2 * r + 1] *= f;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int n = 0; n < NH; ++n)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float& v = s[j][2 * r + x];
-            v = exp2_of(v - minus[r]);
-            l[r] += v;
-            if (FP8) v *= vscale[j][x];
-          }
-      // ---- values
+            const float to = fmaxf(tokens_max(top[n][x]), m[n][x]);
+            const float f = m[n][x] == -INFINITY ? 0.f : exp2_of(m[n][x] - to);
+            m[n][x] = to;
+            l[n][x] *= f;
 #pragma unroll
-      for (int n = 0; n < NT / 2; ++n) {
-        uint32_t pa[4], pb[4];
-        const float(&s0)[4] = s[2 * n];
-        const float(&s1)[4] = s[2 * n + 1];
-        if (FP8) {
-          pa[0] = pack_f16(s0[0], s0[1]), pa[2] = pack_f16(s1[0], s1[1]);
-          pa[1] = HI ? pack_f16(s0[2], s0[3]) : 0u, pa[3] = HI ? pack_f16(s1[2], s1[3]) : 0u;
-        } else {
-          auto two = [](float a, float b, uint32_t& high, uint32_t& low) {
-            high = afd::pack_bf16(a, b);
-            low = afd::pack_bf16(a - __uint_as_float(high << 16), b - __uint_as_float(high & 0xffff0000u));
-          };
-          pa[1] = pa[3] = pb[1] = pb[3] = 0u;
-          two(s0[0], s0[1], pa[0], pb[0]);
-          two(s1[0], s1[1], pa[2], pb[2]);
-          if (HI) {
-            two(s0[2], s0[3], pa[1], pb[1]);
-            two(s1[2], s1[3], pa[3], pb[3]);
+            for (int d = 0; d < D / 16; ++d) o[d][n][x] *= f, o[d][n][2 + x] *= f;
           }
+      }
+#pragma unroll
+      for (int n = 0; n < NH; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float minus = m[n][x] == -INFINITY ? 0.f : m[n][x];
+#pragma unroll
+          for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float& v = s[t][n][2 * y + x];
+              v = exp2_of(v - minus);
+              l[n][x] += v;
+              if (FP8) v *= vscale[t][y];
+            }
         }
-        const int t0 = 16 * n + 2 * c;
-        if constexpr (!FP8) {
+      // ---- values: columns (8 h + g) E + e of heads 8 n + 2 c (and + 1)
 #pragma unroll
-          for (int h = 0; h < H; ++h) {
-            uint32_t v[4][4];
+      for (int t = 0; t < TB; ++t) {
+        uint32_t pa[NH][2], pb[NH][2];  // probabilities, and (BF16) what their rounding left
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const uint4 u = *reinterpret_cast<const uint4*>(vs + swizzled<ROW>(t0 + (t & 1) + 8 * (t >> 1), 8 * h + g));
-              v[t][0] = u.x, v[t][1] = u.y, v[t][2] = u.z, v[t][3] = u.w;
-            }
+        for (int n = 0; n < NH; ++n)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t b0 = __byte_perm(v[0][e / 2], v[1][e / 2], e & 1 ? 0x7632 : 0x5410);
-              const uint32_t b1 = __byte_perm(v[2][e / 2], v[3][e / 2], e & 1 ? 0x7632 : 0x5410);
-              mma<false>(o[h * 8 + e], pa, b0, b1);
-              mma<false>(o[h * 8 + e], pb, b0, b1);
-            }
-          }
-        } else {
-          uint32_t v[4][E / 4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int row = t0 + (t & 1) + 8 * (t >> 1);
-            if constexpr (D == 128) {
-              const uint4 u = *reinterpret_cast<const uint4*>(vs + swizzled<ROW>(row, g));
-              v[t][0] = u.x, v[t][1] = u.y, v[t][2] = u.z, v[t][3] = u.w;
+          for (int y = 0; y < 2; ++y) {
+            const float a = s[t][n][2 * y], b = s[t][n][2 * y + 1];
+            if (FP8) {
+              pa[n][y] = transposed(pack_f16(a, b));
             } else {
-              const uint2 u = *reinterpret_cast<const uint2*>(vs + swizzled<ROW>(row, g >> 1) + (g & 1) * 8);
-              v[t][0] = u.x, v[t][1] = u.y;
+              const uint32_t high = afd::pack_bf16(a, b);
+              pa[n][y] = transposed(high);
+              pb[n][y] = transposed(afd::pack_bf16(a - __uint_as_float(high << 16), b - __uint_as_float(high & 0xffff0000u)));
             }
           }
 #pragma unroll
-          for (int w = 0; w < E / 4; ++w) {
-            const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[2][w], v[3][w], 0x5140);
-            const uint32_t y0 = __byte_perm(v[0][w], v[1][w], 0x7362), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-            mma<true>(o[4 * w], pa, half2_of<0>(x0), half2_of<0>(x1));
-            mma<true>(o[4 * w + 1], pa, half2_of<1>(x0), half2_of<1>(x1));
-            mma<true>(o[4 * w + 2], pa, half2_of<0>(y0), half2_of<0>(y1));
-            mma<true>(o[4 * w + 3], pa, half2_of<1>(y0), half2_of<1>(y1));
+        for (int h = 0; h < H; ++h) {
+          uint32_t v[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 16 * t + 2 * c + (i & 1) + 8 * (i >> 1);
+            if constexpr (ROW == 64) {
+              const uint2 u = *reinterpret_cast<const uint2*>(vs + swizzled<ROW>(row, g >> 1) + (g & 1) * 8);
+              v[i][0] = u.x, v[i][1] = u.y;
+            } else {
+              const uint4 u = *reinterpret_cast<const uint4*>(vs + swizzled<ROW>(row, 8 * h + g));
+              v[i][0] = u.x, v[i][1] = u.y, v[i][2] = u.z, v[i][3] = u.w;
+            }
+          }
+          if constexpr (FP8) {
+#pragma unroll
+            for (int w = 0; w < E / 4; ++w) {
+              const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[2][w], v[3][w], 0x5140);
+              const uint32_t y0 = __byte_perm(v[0][w], v[1][w], 0x7362), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+#pragma unroll
+              for (int n = 0; n < NH; ++n) {
+                mma<true>(o[2 * w][n], half2_of<0>(x0), half2_of<1>(x0), half2_of<0>(x1), half2_of<1>(x1), pa[n]);
+                mma<true>(o[2 * w + 1][n], half2_of<0>(y0), half2_of<1>(y0), half2_of<0>(y1), half2_of<1>(y1), pa[n]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
+              const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410), a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+#pragma unroll
+              for (int n = 0; n < NH; ++n) {
+                mma<false>(o[4 * h + w][n], a0, a1, a2, a3, pa[n]);
+                mma<false>(o[4 * h + w][n], a0, a1, a2, a3, pb[n]);
+              }
+            }
           }
         }
       }
@@ -554,56 +596,59 @@ __global__ void __launch_bounds__(Layout<D, FP8, HI>::kWarps * 32, 1) decode_att
       const bool ends = at.tile + 1 == at.span.end;
       if (ends || i + 1 == tiles) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) l[r] = quad_sum(l[r]);
+        for (int n = 0; n < NH; ++n) l[n][0] = tokens_sum(l[n][0]), l[n][1] = tokens_sum(l[n][1]);
         const int seg = at.b * p.chunks + at.chunk;
         if (began && ends) {
           const int head = at.chunk / groups, sub = at.chunk % groups;
-          const int rows = min(p.G - sub * kRows, kRows), q0 = head * p.G + sub * kRows;
+          const int rows = min(p.G - sub * ROWS, ROWS), q0 = head * p.G + sub * ROWS;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const int row = g + 8 * r;
-            if (row >= rows) continue;
-            const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
-            uint16_t* out = p.out + at.b * p.out_stride + (int64_t)(q0 + row) * D;
+          for (int n = 0; n < NH; ++n)
 #pragma unroll
-            for (int h = 0; h < H; ++h)
+            for (int x = 0; x < 2; ++x) {
+              const int row = 8 * n + 2 * c + x;
+              if (row >= rows) continue;
+              const float inv = l[n][x] == 0.f ? 0.f : 1.f / l[n][x];
+              uint16_t* out = p.out + at.b * p.out_stride + (int64_t)(q0 + row) * D;
 #pragma unroll
-              for (int x = 0; x < 2; ++x)
+              for (int h = 0; h < H; ++h)
 #pragma unroll
                 for (int e = 0; e < E; e += 8) {
                   float f[8];
 #pragma unroll
-                  for (int k = 0; k < 8; ++k) f[k] = o[h * 8 + e + k][2 * r + x] * inv;
-                  *reinterpret_cast<uint4*>(out + (8 * h + 2 * c + x) * E + e) = afd::float_to_bf16x8(f);
+                  for (int k = 0; k < 8; ++k) f[k] = o[(h * E + e + k) / 2][n][2 * (k & 1) + x] * inv;
+                  *reinterpret_cast<uint4*>(out + (8 * h + g) * E + e) = afd::float_to_bf16x8(f);
                 }
-            if (p.lse && c == 0) p.lse[(int64_t)at.b * p.Hq + q0 + row] = l[r] == 0.f ? -INFINITY : m[r] * kLn2 + logf(l[r]);
-          }
+              if (p.lse && g == 0) p.lse[(int64_t)at.b * p.Hq + q0 + row] = l[n][x] == 0.f ? -INFINITY : m[n][x] * kLn2 + logf(l[n][x]);
+            }
         } else {
-          // Left open: in the warp's own place if it began in an earlier warp's
-          // share, else (then it is the share's last) where the ring was.
+          // Left open. What began in an earlier warp's share goes to the warp's own
+          // place if more follows; the share's last goes where the ring was.
           const int which = began ? 1 : 0;
+          const bool last = i + 1 == tiles;
           float* to = kept;
-          if (which) {
+          if (last) {
             copies_wait<0>();
             __syncwarp();
             to = reinterpret_cast<float*>(ring);
           }
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
+          for (int n = 0; n < NH; ++n)
 #pragma unroll
-            for (int h = 0; h < H; ++h)
+            for (int x = 0; x < 2; ++x) {
+              const int row = 8 * n + 2 * c + x;
 #pragma unroll
-              for (int x = 0; x < 2; ++x)
+              for (int h = 0; h < H; ++h)
 #pragma unroll
-                for (int e = 0; e < E; e += 4)
-                  *reinterpret_cast<float4*>(to + (g + 8 * r) * D + (8 * h + 2 * c + x) * E + e) =
-                      make_float4(o[h * 8 + e][2 * r + x], o[h * 8 + e + 1][2 * r + x], o[h * 8 + e + 2][2 * r + x],
-                                  o[h * 8 + e + 3][2 * r + x]);
-            if (c == 0) part_m[warp][which][g + 8 * r] = m[r], part_l[warp][which][g + 8 * r] = l[r];
-          }
+                for (int e = 0; e < E; e += 4) {
+                  const int d = (h * E + e) / 2;
+                  *reinterpret_cast<float4*>(to + row * D + (8 * h + g) * E + e) =
+                      make_float4(o[d][n][x], o[d][n][2 + x], o[d + 1][n][x], o[d + 1][n][2 + x]);
+                }
+              if (g == 0) part_m[warp][which][row] = m[n][x], part_l[warp][which][row] = l[n][x];
+            }
           if (lane == 0) {
             if (which) seg_b[warp] = seg, end_b[warp] = lo + i + (at.span.end - at.tile);
-            else seg_a[warp] = seg, done_a[warp] = ends;
+            else seg_a[warp] = seg, done_a[warp] = ends, away_a[warp] = !last;
           }
         }
         began = true;
@@ -618,7 +663,6 @@ __global__ void __launch_bounds__(Layout<D, FP8, HI>::kWarps * 32, 1) decode_att
   // ---- the block's open parts: a chain begins with the first warp's part of an
   // earlier block's segment, or with a warp's last one, and goes on through the
   // next warps' first ones.
-  const int valid = HI ? 16 : 8;
   int tail = -1;
   int64_t tail_end = 0;
 #pragma unroll 1
@@ -632,8 +676,8 @@ __global__ void __launch_bounds__(Layout<D, FP8, HI>::kWarps * 32, 1) decode_att
     if (w0 >= 0 && !done) tail = seg, tail_end = end_b[w0];
     const int b = seg / p.chunks, chunk = seg % p.chunks, groups = p.chunks / p.Hkv;
     const int head = chunk / groups, sub = chunk % groups;
-    const int rows = min(min(p.G - sub * kRows, kRows), valid), q0 = head * p.G + sub * kRows;
-    float* part = p.parts + ((int64_t)blockIdx.x * 2 + (w0 >= 0)) * kRows * (D + 2);
+    const int rows = min(p.G - sub * ROWS, ROWS), q0 = head * p.G + sub * ROWS;
+    float* part = p.parts + ((int64_t)blockIdx.x * 2 + (w0 >= 0)) * ROWS * (D + 2);
     for (int i = threadIdx.x; i < rows * (D / 8); i += THREADS) {
       const int row = i / (D / 8), col = i % (D / 8) * 8;
       float most = w0 >= 0 ? part_m[w0][1][row] : -INFINITY;
@@ -643,8 +687,8 @@ __global__ void __launch_bounds__(Layout<D, FP8, HI>::kWarps * 32, 1) decode_att
       for (int w = max(w0, 0); w < w1; ++w) {
         const int which = w == w0;
         const float scale = exp2_of(part_m[w][which][row] - minus);
-        const float* from = which ? reinterpret_cast<const float*>(shared + w * Y::kRing)
-                                  : reinterpret_cast<const float*>(shared + W * Y::kRing + w * Y::kPart);
+        const float* from = which || !away_a[w] ? reinterpret_cast<const float*>(shared + w * Y::kRing)
+                                                : p.kept + (int64_t)(blockIdx.x * W + w) * ROWS * D;
         sum += part_l[w][which][row] * scale;
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] = fmaf(from[row * D + col + k], scale, f[k]);
@@ -658,7 +702,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, HI>::kWarps * 32, 1) decode_att
       } else {
         *reinterpret_cast<float4*>(part + row * D + col) = make_float4(f[0], f[1], f[2], f[3]);
         *reinterpret_cast<float4*>(part + row * D + col + 4) = make_float4(f[4], f[5], f[6], f[7]);
-        if (col == 0) part[kRows * D + row] = most, part[kRows * (D + 1) + row] = sum;
+        if (col == 0) part[ROWS * D + row] = most, part[ROWS * (D + 1) + row] = sum;
       }
     }
   }
@@ -671,21 +715,22 @@ __global__ void __launch_bounds__(Layout<D, FP8, HI>::kWarps * 32, 1) decode_att
 
 // Joins what the blocks left open: a warp per row of a segment that began in
 // block `from`; its parts are that block's second and the next ones' first.
-template <int D>
+template <int D, int NH>
 __global__ void __launch_bounds__(256) decode_join_kernel(const AttentionParams p) {
   afd::pdl_wait();
   afd::pdl_launch_dependents();
+  constexpr int ROWS = 8 * NH;
   const int lane = threadIdx.x & 31;
-  const int item = blockIdx.x * 8 + (threadIdx.x >> 5), from = item / kRows, row = item % kRows;
+  const int item = blockIdx.x * 8 + (threadIdx.x >> 5), from = item / ROWS, row = item % ROWS;
   const Split split = p.splits[from];
   if (split.seg < 0) return;
   const int b = split.seg / p.chunks, chunk = split.seg % p.chunks, groups = p.chunks / p.Hkv;
   const int head = chunk / groups, sub = chunk % groups;
-  if (row >= min(p.G - sub * kRows, kRows)) return;
-  constexpr int64_t kPart = kRows * (D + 2);
+  if (row >= min(p.G - sub * ROWS, ROWS)) return;
+  constexpr int64_t kPart = ROWS * (D + 2);
   auto part = [&](int i) { return p.parts + ((int64_t)i * 2 + (i == from)) * kPart; };
   float most = -INFINITY;
-  for (int i = from + lane; i <= split.last; i += 32) most = fmaxf(most, part(i)[kRows * D + row]);
+  for (int i = from + lane; i <= split.last; i += 32) most = fmaxf(most, part(i)[ROWS * D + row]);
 #pragma unroll
   for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, d));
   const float minus = most == -INFINITY ? 0.f : most;
@@ -694,8 +739,8 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const AttentionParams 
 #pragma unroll 4
   for (int i = from; i <= split.last; ++i) {
     const float* q = part(i);
-    const float scale = exp2_of(q[kRows * D + row] - minus);
-    sum = fmaf(q[kRows * (D + 1) + row], scale, sum);
+    const float scale = exp2_of(q[ROWS * D + row] - minus);
+    sum = fmaf(q[ROWS * (D + 1) + row], scale, sum);
     if constexpr (N == 4) {
       const float4 v = *reinterpret_cast<const float4*>(q + row * D + lane * 4);
       f[0] = fmaf(v.x, scale, f[0]), f[1] = fmaf(v.y, scale, f[1]);
@@ -706,7 +751,7 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const AttentionParams 
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int q = head * p.G + sub * kRows + row;
+  const int q = head * p.G + sub * ROWS + row;
   uint32_t* out = reinterpret_cast<uint32_t*>(p.out + b * p.out_stride + (int64_t)q * D + lane * N);
 #pragma unroll
   for (int k = 0; k < N; k += 2) out[k / 2] = afd::pack_bf16(f[k] * inv, f[k + 1] * inv);
@@ -715,37 +760,42 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const AttentionParams 
 
 int tile_tokens(int head_dim, bool fp8) { return head_dim == 128 && !fp8 ? 16 : 32; }
 
-int64_t workspace_of(int head_dim) {
-  return kMaxBlocks * (int64_t)(sizeof(Split) + 2 * kRows * (head_dim + 2) * sizeof(float));
+int chunk_rows(int group) { return group > 8 ? 16 : 8; }
+
+int64_t parts_of(int head_dim, int rows) { return kMaxBlocks * (int64_t)2 * rows * (head_dim + 2); }
+int64_t workspace_of(int head_dim, int rows) {
+  return kMaxBlocks * (int64_t)sizeof(Split) +
+         (parts_of(head_dim, rows) + kMaxBlocks * (int64_t)kMaxWarps * rows * head_dim) * (int64_t)sizeof(float);
 }
 
 // The most tiles there can be: those of full tables.
 int64_t most_tiles(int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t tokens, int tile) {
-  const int64_t chunks = kv_heads * ((q_heads / kv_heads + kRows - 1) / kRows);
+  const int64_t rows = chunk_rows((int)(q_heads / kv_heads));
+  const int64_t chunks = kv_heads * ((q_heads / kv_heads + rows - 1) / rows);
   const int64_t tiles = (tokens + tile - 1) / tile;
   return tiles == 0 ? 0 : seqs * chunks > INT64_MAX / tiles ? INT64_MAX : seqs * chunks * tiles;
 }
 
-template <int D, bool FP8, bool HI>
+template <int D, bool FP8, int NH>
 cudaError_t launch_attention(const AttentionParams& p, int64_t tiles, int device, int sms, cudaStream_t stream) {
-  using Y = Layout<D, FP8, HI>;
+  using Y = Layout<D, FP8, NH>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = afd::allow_shared(decode_attention_kernel<D, FP8, HI>, Y::kShared, device, done);
+  cudaError_t e = afd::allow_shared(decode_attention_kernel<D, FP8, NH>, Y::kShared, device, done);
   if (e != cudaSuccess) return e;
   const int64_t want = tiles / Y::kWarps + (tiles % Y::kWarps != 0), most = sms < kMaxBlocks ? sms : kMaxBlocks;
   const int blocks = (int)(want < 1 ? 1 : want < most ? want : most);
-  e = afd::launch_dependent(decode_attention_kernel<D, FP8, HI>, blocks, Y::kWarps * 32, Y::kShared, stream, p);
+  e = afd::launch_dependent(decode_attention_kernel<D, FP8, NH>, blocks, Y::kWarps * 32, Y::kShared, stream, p);
   if (e != cudaSuccess || blocks == 1) return e;
-  return afd::launch_dependent(decode_join_kernel<D>, blocks * kRows / 8, 256, 0, stream, p);
+  return afd::launch_dependent(decode_join_kernel<D, NH>, blocks * NH, 256, 0, stream, p);
 }
 
 template <int D>
 cudaError_t launch_of(const AttentionParams& p, bool fp8, int64_t tiles, int device, int sms, cudaStream_t stream) {
   if (p.G > 8)
-    return fp8 ? launch_attention<D, true, true>(p, tiles, device, sms, stream)
-               : launch_attention<D, false, true>(p, tiles, device, sms, stream);
-  return fp8 ? launch_attention<D, true, false>(p, tiles, device, sms, stream)
-             : launch_attention<D, false, false>(p, tiles, device, sms, stream);
+    return fp8 ? launch_attention<D, true, 2>(p, tiles, device, sms, stream)
+               : launch_attention<D, false, 2>(p, tiles, device, sms, stream);
+  return fp8 ? launch_attention<D, true, 1>(p, tiles, device, sms, stream)
+             : launch_attention<D, false, 1>(p, tiles, device, sms, stream);
 }
 
 constexpr int64_t kMaxTokens = INT32_MAX - 1024;  // of a table's row
@@ -761,7 +811,7 @@ AFD_API int64_t afd_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads
     return -1;
   // (of the two types' tiles the smaller, so the larger number of them)
   const int64_t tiles = most_tiles(num_seqs, num_q_heads, num_kv_heads, (int64_t)max_pages * page_size, 16);
-  return tiles <= Layout<128, false, false>::kWarps ? 0 : workspace_of(head_dim);
+  return tiles <= 1 ? 0 : workspace_of(head_dim, chunk_rows(num_q_heads / num_kv_heads));
 }
 
 AFD_API afd_status afd_decode_attention(const void* q, int64_t q_stride, const afd_cache* cache,
@@ -773,10 +823,10 @@ AFD_API afd_status afd_decode_attention(const void* q, int64_t q_stride, const a
   const afd_status checked = afd::check_cache(cache);
   if (checked != AFD_OK) return checked;
   const int D = cache->head_dim, Hkv = cache->num_kv_heads;
-  const int64_t row = (int64_t)num_q_heads * D;
-  if (num_q_heads % Hkv || (num_seqs > 1 && (q_stride < row || out_stride < row || table_stride < max_pages))) return AFD_ERR_ARG;
+  const int64_t width = (int64_t)num_q_heads * D;
+  if (num_q_heads % Hkv || (num_seqs > 1 && (q_stride < width || out_stride < width || table_stride < max_pages))) return AFD_ERR_ARG;
   const int64_t tokens = (int64_t)max_pages * cache->page_size;
-  const int groups = (num_q_heads / Hkv + kRows - 1) / kRows;
+  const int rows = chunk_rows(num_q_heads / Hkv), groups = (num_q_heads / Hkv + rows - 1) / rows;
   if (num_q_heads > afd::kMaxHeads || tokens > kMaxTokens || (int64_t)num_seqs * Hkv * groups > afd::kMaxRows ||
       q_stride % 8 || out_stride % 8)
     return AFD_ERR_UNSUPPORTED;
@@ -797,7 +847,10 @@ AFD_API afd_status afd_decode_attention(const void* q, int64_t q_stride, const a
   p.q_stride = q_stride, p.table_stride = table_stride, p.max_pages = max_pages, p.out_stride = out_stride;
   p.B = num_seqs, p.Hq = num_q_heads, p.Hkv = Hkv, p.G = num_q_heads / Hkv, p.chunks = Hkv * groups;
   p.scale_log2 = scale * 1.4426950408889634f, p.window = window;
-  if (need > 0) p.parts = reinterpret_cast<float*>(p.splits + kMaxBlocks);
+  if (need > 0) p.parts = reinterpret_cast<float*>(p.splits + kMaxBlocks), p.kept = p.parts + parts_of(D, rows);
+  p.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (cache->page_size == 1 << i) p.page_shift = i;
   int dev = -1, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return AFD_ERR_CUDA;
