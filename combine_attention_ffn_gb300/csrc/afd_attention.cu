@@ -4,13 +4,14 @@
 // for G query heads a KV head: bound by DRAM, so everything here is about keeping
 // loads in flight and every SM busy whatever the lengths are.
 //
-// Tiles and their order: the tokens of a sequence that are seen, 16 or 32 at a
-// time (4 KB of keys and as much of values), once for each KV head and each 16
-// of its query heads; sequences, heads and tiles in that order make one line of
-// tiles. The line is cut into equal shares, one a warp, so that no length leaves
-// a warp idle; a share may begin or end inside a (sequence, head). Those parts
-// are joined by the block after its warps are done, and what the blocks leave
-// open by a second kernel.
+// Tiles and their order: the tokens of a sequence that are seen, 16, 32 or 64 at
+// a time (4 KB of keys and as much of values), once for each KV head and each 8
+// or 16 of its query heads; sequences, heads and tiles in that order make one
+// line. A (sequence, heads) segment counts kBegin on it beside its tiles, for its
+// queries and its result. The line is cut into equal shares, one a warp, so that
+// no length leaves a warp idle; a share may begin or end inside a segment. Those
+// parts are joined by the block after its warps are done, and what the blocks
+// leave open by a second kernel.
 //
 // A warp works alone: its own ring of tiles in shared memory, filled by
 // asynchronous copies ahead of their use, its own running maximum and sum. The
@@ -37,6 +38,8 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxBlocks = 160;
 constexpr int kMaxWarps = 16;
 constexpr float kLazy = 8.f;  // log2 of how far a score may pass the running maximum before that moves
+constexpr int kBegin = 1;   // what a segment costs beside its tiles, in tiles
+constexpr int kRun = 16;    // tokens that are in one page where its size is a multiple
 constexpr float kLn2 = 0.693147180559945f;
 
 // A split (sequence, head): where its last part is (see join).
@@ -69,9 +72,11 @@ struct AttentionParams {
 template <int D, bool FP8>
 struct Shape {
   static constexpr int kRow = FP8 ? D : 2 * D;               // bytes of a token's head
-  static constexpr int kTile = kRow == 256 ? 16 : 32;        // tokens
+  static constexpr int kTile = 4096 / kRow;                  // tokens
   static constexpr int kBytes = kTile * kRow;                // of a tile's keys, or values
-  static constexpr int kStage = 2 * kBytes + (FP8 ? 2 * kTile * 4 : 0);
+  static constexpr int kScales = 2 * kBytes;                 // a stage's scales, {key, value} a token ...
+  static constexpr int kBias = kScales + (FP8 ? 8 * kTile : 0);  // ... and what a score is lowered by
+  static constexpr int kStage = kBias + 4 * kTile;
   static constexpr int E = FP8 && D == 128 ? 16 : 8;         // neighbouring columns of a lane
   static constexpr int H = D / 8 / E;                        // ... and how many such groups
 };
@@ -81,8 +86,8 @@ struct Shape {
 template <int D, bool FP8, int NH>
 struct Layout {
   using S = Shape<D, FP8>;
-  static constexpr int kWarps = S::kStage > 8000 ? 12 : 16;
-  static constexpr int kStages = S::kStage > 8000 ? 2 : 3;
+  static constexpr int kWarps = 12;
+  static constexpr int kStages = 2;
   static constexpr int kRows = 8 * NH;
   static constexpr int kRing = kStages * S::kStage;
   static constexpr int kShared = kWarps * kRing;
@@ -194,45 +199,56 @@ __device__ __forceinline__ Span span_of(const AttentionParams& p, int b) {
   return s;
 }
 
-// A place in the line of tiles.
+// A place in the line; next() returns how far it went.
 template <int TILE>
 struct Cursor {
   Span span;
   int b, chunk, tile;
-  __device__ __forceinline__ void next(const AttentionParams& p) {
-    if (++tile < span.end) return;
+  __device__ __forceinline__ int next(const AttentionParams& p) {
+    if (++tile < span.end) return 1;
     if (++chunk == p.chunks) {
       chunk = 0;
       do {
-        if (++b >= p.B) return;  // (the end of the line)
+        if (++b >= p.B) return 1 + kBegin;  // (the end of the line)
         span = span_of<TILE>(p, b);
       } while (span.first == span.end);
     }
     tile = span.first;
+    return 1 + kBegin;
   }
 };
 
-// What a lane looks up for a tile: its token's page and place there.
-struct Lookup {
-  int page, at, chunk;
-  bool in;
-};
-
+// Where tokens are, in registers across a warp's lanes. Pages of a multiple of
+// kRun tokens: run `first` + lane of the sequence; else the tokens of one tile.
 template <int TILE>
-__device__ __forceinline__ Lookup look_up(const AttentionParams& p, const Cursor<TILE>& c, int lane) {
-  Lookup l;
-  const int token = c.tile * TILE + (lane & (TILE - 1));
-  l.in = token >= c.span.from && token < c.span.len;
-  l.chunk = c.chunk;
-  l.page = 0;
-  l.at = 0;
-  if (l.in) {
-    const uint32_t page = p.page_shift >= 0 ? (uint32_t)token >> p.page_shift : (uint32_t)token / (uint32_t)p.cache.page_size;
-    l.at = token - (int)(page * (uint32_t)p.cache.page_size);
-    l.page = p.table[c.b * p.table_stride + page];
+struct Lookup {
+  static constexpr int N = TILE > 32 ? TILE / 32 : 1;
+  int page[N], at[N];  // -1: not seen
+  int first;
+  __device__ __forceinline__ void find(const AttentionParams& p, const Cursor<TILE>& c, int i, int token) {
+    const uint32_t n = p.page_shift >= 0 ? (uint32_t)token >> p.page_shift : (uint32_t)token / (uint32_t)p.cache.page_size;
+    at[i] = token - (int)(n * (uint32_t)p.cache.page_size);
+    page[i] = p.table[c.b * p.table_stride + n];
   }
-  return l;
-}
+  // `fresh`: another sequence, or the sequence's first tile again.
+  __device__ __forceinline__ void update(const AttentionParams& p, const Cursor<TILE>& c, bool runs, bool fresh, int lane) {
+    if (runs) {
+      const int run = c.tile * (TILE / kRun);
+      if (!fresh && run + TILE / kRun <= first + 32) return;
+      first = run;
+      const int token = (run + lane) * kRun;
+      page[0] = -1, at[0] = 0;
+      if (token < c.span.len) find(p, c, 0, token);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int token = c.tile * TILE + ((32 * i + lane) & (TILE - 1));
+        page[i] = -1, at[i] = 0;
+        if (token >= c.span.from && token < c.span.len) find(p, c, i, token);
+      }
+    }
+  }
+};
 
 template <int D, bool FP8, int NH>
 __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_attention_kernel(const AttentionParams p) {
@@ -240,10 +256,8 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
   using Y = Layout<D, FP8, NH>;
   constexpr int TILE = S::kTile, ROW = S::kRow, E = S::E, H = S::H, TB = TILE / 16, W = Y::kWarps, ROWS = Y::kRows;
   constexpr int THREADS = W * 32;
-  constexpr uint32_t ALL = kFull;  // every token of a tile (of 16: twice)
   extern __shared__ __align__(128) uint8_t shared[];
-  __shared__ int64_t before[THREADS + 1];          // tiles before each thread's sequences
-  __shared__ uint32_t seen[W][Y::kStages];         // a staged tile's tokens that count
+  __shared__ int64_t before[THREADS + 1];          // the line before each thread's sequences, of one chunk
   __shared__ float part_m[W][2][ROWS], part_l[W][2][ROWS];
   __shared__ int seg_a[W], seg_b[W], done_a[W], away_a[W];
   __shared__ int64_t end_b[W];
@@ -252,14 +266,14 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
   afd::pdl_wait();
   afd::pdl_launch_dependents();
 
-  // ---- the line of tiles, and this warp's share of it
+  // ---- the line, and this warp's share of it
   const int each = (p.B + THREADS - 1) / THREADS;
   {
     int64_t mine = 0;
     const int b0 = threadIdx.x * each, b1 = min(p.B, b0 + each);
     for (int b = b0; b < b1; ++b) {
       const Span s = span_of<TILE>(p, b);
-      mine += s.end - s.first;
+      mine += s.end > s.first ? s.end - s.first + kBegin : 0;
     }
     int64_t sum = mine;
 #pragma unroll
@@ -275,7 +289,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
   }
   __syncthreads();
   const int64_t total = before[THREADS] * p.chunks;
-  // A tile a warp at least: of few tiles the first blocks' warps take one each.
+  // About a tile a warp at least: of few tiles the first blocks' warps take one each.
   const int workers = (int)min(total, (int64_t)gridDim.x * W), worker = blockIdx.x * W + warp;
   const bool works = worker < workers;
   const int64_t lo = works ? total * worker / workers : 0, hi = works ? total * (worker + 1) / workers : 0;
@@ -295,10 +309,11 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
   if (lane == 0) seg_a[warp] = seg_b[warp] = -1, done_a[warp] = away_a[warp] = 0, end_b[warp] = 0;
 
   if (lo < hi) {
-    // ---- where the share begins
+    // ---- where the share begins: `place` is that of the next tile on the line
     Cursor<TILE> at;
+    int64_t place = lo;
     {
-      const int64_t line = lo / p.chunks;  // tiles of whole sequences, times the chunks
+      const int64_t line = lo / p.chunks;
       int i = 0;
 #pragma unroll 1
       for (int step = 256; step; step >>= 1)
@@ -307,71 +322,117 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
       at.b = i * each;
       at.span = span_of<TILE>(p, at.b);
       for (;;) {
-        const int64_t n = (int64_t)(at.span.end - at.span.first) * p.chunks;
+        const int64_t n = at.span.end > at.span.first ? (int64_t)(at.span.end - at.span.first + kBegin) * p.chunks : 0;
         if (left < n) break;
         left -= n;
         at.span = span_of<TILE>(p, ++at.b);
       }
-      const int n = at.span.end - at.span.first;
+      const int n = at.span.end - at.span.first + kBegin;
       at.chunk = (int)(left / n);
-      at.tile = at.span.first + (int)(left - (int64_t)at.chunk * n);
+      const int in = (int)(left - (int64_t)at.chunk * n);
+      at.tile = at.span.first + max(in - kBegin, 0);
+      place += max(kBegin - in, 0);
     }
-    const int tiles = (int)(hi - lo);
     const int groups = p.chunks / p.Hkv;  // chunks of a KV head
-    const bool tiled = p.cache.page_size % TILE == 0;  // a tile is in one page
+    const bool runs = p.cache.page_size % kRun == 0;
 
     Cursor<TILE> ahead = at;
-    Lookup next = look_up(p, ahead, lane);
-    ahead.next(p);
+    int64_t ahead_place = place;
+    Lookup<TILE> next;
+    next.update(p, ahead, runs, true, lane);
+    bool whole = true, next_whole = true;  // every token of the staged tile is seen
     // Starts the copies of the tile looked up last, and looks the one after it up.
-    auto issue = [&](int i) {
-      if (i < tiles) {
-        const bool in = next.in && (uint32_t)next.page < (uint32_t)p.cache.pages;
-        const int stage = i % Y::kStages;
-        const uint32_t dst = smem_addr(ring + stage * S::kStage);
-        const uint32_t mask = __ballot_sync(kFull, in);
-        if (lane == 0) seen[warp][stage] = mask;
-        const int head = next.chunk / groups;
-        const int64_t row = (int64_t)head * p.cache.page_size + next.at;
+    auto issue = [&](int stage) {
+      if (ahead_place < hi) {
         constexpr int CH = ROW / 16;  // chunks of a row
-        if (tiled && mask == ALL) {
-          // one run of bytes: the same for every lane but for its own 16
-          const int64_t first = (row - (lane & (TILE - 1))) * ROW + lane * 16;
-          const uint8_t* k = p.cache.k + next.page * p.cache.k_page_bytes + first;
-          const uint8_t* v = p.cache.v + next.page * p.cache.v_page_bytes + first;
+        uint8_t* to = ring + stage * S::kStage;
+        const uint32_t dst = smem_addr(to);
+        const int base = ahead.tile * TILE, head = groups == 1 ? ahead.chunk : ahead.chunk / groups;
+        const int lowest = ahead.span.from - base, end = ahead.span.len - base;  // rows that are seen
+        next_whole = lowest <= 0 && end >= TILE;
+        if (runs) {
+          constexpr int JS = kRun * CH / 32;  // 512-byte steps of a run
+          const int r0 = ahead.tile * (TILE / kRun) - next.first;
+          const uint8_t *k[TILE / kRun], *v[TILE / kRun];
+          bool ok[TILE / kRun];
 #pragma unroll
-          for (int j = 0; j < S::kBytes / 512; ++j) {
-            const uint32_t to = dst + swizzled<ROW>((j * 32 + lane) / CH, (j * 32 + lane) % CH);
-            copy16(to, k + j * 512, true);
-            copy16(to + S::kBytes, v + j * 512, true);
+          for (int r = 0; r < TILE / kRun; ++r) {
+            const int page = __shfl_sync(kFull, next.page[0], r0 + r);
+            const uint32_t row = (uint32_t)(head * p.cache.page_size + __shfl_sync(kFull, next.at[0], r0 + r)) * CH + lane;
+            ok[r] = (uint32_t)page < (uint32_t)p.cache.pages;
+            const uint32_t pg = ok[r] ? (uint32_t)page : 0u;
+            k[r] = p.cache.k + (((uint64_t)pg * p.cache.k_page_units + row) << 4);
+            v[r] = p.cache.v + (((uint64_t)pg * p.cache.v_page_units + row) << 4);
+            next_whole &= ok[r];
+          }
+          if (next_whole) {
+#pragma unroll
+            for (int j = 0; j < S::kBytes / 512; ++j) {
+              const uint32_t d = dst + swizzled<ROW>((j * 32 + lane) / CH, (j * 32 + lane) % CH);
+              copy16(d, k[j / JS] + j % JS * 512, true);
+              copy16(d + S::kBytes, v[j / JS] + j % JS * 512, true);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < S::kBytes / 512; ++j) {
+              const int row = (j * 32 + lane) / CH;
+              const bool in = ok[j / JS] && row >= lowest && row < end;
+              const uint32_t d = dst + swizzled<ROW>(row, (j * 32 + lane) % CH);
+              copy16(d, in ? k[j / JS] + j % JS * 512 : p.cache.k, in);
+              copy16(d + S::kBytes, in ? v[j / JS] + j % JS * 512 : p.cache.v, in);
+            }
+          }
+          if (FP8 || !next_whole) {
+#pragma unroll
+            for (int i = 0; i < Lookup<TILE>::N; ++i) {
+              const int tok = (32 * i + lane) & (TILE - 1);
+              const int page = __shfl_sync(kFull, next.page[0], r0 + tok / kRun);
+              const int row = head * p.cache.page_size + __shfl_sync(kFull, next.at[0], r0 + tok / kRun) + tok % kRun;
+              const bool in = tok >= lowest && tok < end && (uint32_t)page < (uint32_t)p.cache.pages;
+              if (FP8) {
+                const int64_t o = in ? (int64_t)page * p.Hkv * p.cache.page_size + row : 0;
+                copy4(dst + S::kScales + tok * 8, p.cache.k_scale + o, in);
+                copy4(dst + S::kScales + tok * 8 + 4, p.cache.v_scale + o, in);
+              }
+              if (!next_whole) reinterpret_cast<float*>(to + S::kBias)[tok] = in ? 0.f : -INFINITY;
+            }
           }
         } else {
-          const int64_t k_off = in ? next.page * p.cache.k_page_bytes + row * ROW : 0;
-          const int64_t v_off = in ? next.page * p.cache.v_page_bytes + row * ROW : 0;
+#pragma unroll
+          for (int i = 0; i < Lookup<TILE>::N; ++i) {
+            const int tok = (32 * i + lane) & (TILE - 1);
+            const bool in = (uint32_t)next.page[i] < (uint32_t)p.cache.pages;  // (-1: not seen)
+            const uint32_t mask = __ballot_sync(kFull, in);
+            next_whole &= mask == kFull;
+            const uint32_t row = (uint32_t)(head * p.cache.page_size + next.at[i]);
+            const uint32_t pg = in ? (uint32_t)next.page[i] : 0u;
+            const uint64_t k_off = ((uint64_t)pg * p.cache.k_page_units + row * CH) << 4;
+            const uint64_t v_off = ((uint64_t)pg * p.cache.v_page_units + row * CH) << 4;
 #pragma unroll 1
-          for (int j = 0; j < S::kBytes / 512; ++j) {
-            const int r = (j * 32 + lane) / CH, ch = (j * 32 + lane) % CH;
-            const int64_t ko = __shfl_sync(kFull, k_off, r), vo = __shfl_sync(kFull, v_off, r);
-            const bool ok = (mask >> r) & 1u;
-            const uint32_t to = dst + swizzled<ROW>(r, ch);
-            copy16(to, p.cache.k + ko + ch * 16, ok);
-            copy16(to + S::kBytes, p.cache.v + vo + ch * 16, ok);
+            for (int j = 0; j < (TILE < 32 ? TILE : 32) * CH / 32; ++j) {
+              const int r = (j * 32 + lane) / CH, ch = (j * 32 + lane) % CH;
+              const uint64_t ko = __shfl_sync(kFull, k_off, r), vo = __shfl_sync(kFull, v_off, r);
+              const bool ok = (mask >> r) & 1u;
+              const uint32_t d = dst + swizzled<ROW>(32 * i + r, ch);
+              copy16(d, ok ? p.cache.k + ko + ch * 16 : p.cache.k, ok);
+              copy16(d + S::kBytes, ok ? p.cache.v + vo + ch * 16 : p.cache.v, ok);
+            }
+            if (FP8) {
+              const int64_t o = in ? (int64_t)pg * p.Hkv * p.cache.page_size + row : 0;
+              copy4(dst + S::kScales + tok * 8, p.cache.k_scale + o, in);
+              copy4(dst + S::kScales + tok * 8 + 4, p.cache.v_scale + o, in);
+            }
+            reinterpret_cast<float*>(to + S::kBias)[tok] = in ? 0.f : -INFINITY;
           }
         }
-        if (FP8) {
-          const int64_t o = in ? (int64_t)next.page * p.Hkv * p.cache.page_size + row : 0;
-          copy4(dst + 2 * S::kBytes + lane * 4, p.cache.k_scale + o, in);
-          copy4(dst + 2 * S::kBytes + (TILE + lane) * 4, p.cache.v_scale + o, in);
-        }
-        if (i + 1 < tiles) {
-          next = look_up(p, ahead, lane);
-          ahead.next(p);
-        }
+        const int went = ahead.next(p);
+        ahead_place += went;
+        if (ahead_place < hi) next.update(p, ahead, runs, went > 1, lane);
       }
       copies_commit();
     };
-#pragma unroll 1
-    for (int i = 0; i < Y::kStages - 1; ++i) issue(i);
+    static_assert(Y::kStages == 2, "`whole` and `next_whole`");
+    issue(0);
 
     uint32_t qb[NH][D / 16][2];
     float row_scale[NH][2];
@@ -433,17 +494,18 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
     };
 
     bool fresh = true;
+    int stage = 0;
 #pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
-      copies_wait<Y::kStages - 2>();
+    while (place < hi) {  // (a share may hold a segment's beginning alone)
+      copies_wait<0>();
       __syncwarp();
-      issue(i + Y::kStages - 1);  // into the stage that the last tile has left
+      whole = next_whole;
+      issue(stage ^ 1);  // into the stage that the last tile has left
       if (fresh) load_q();
       fresh = false;
-      const int stage = i % Y::kStages;
       const uint8_t* ks = ring + stage * S::kStage;
       const uint8_t* vs = ks + S::kBytes;
-      const uint32_t mask = seen[warp][stage];
+      stage ^= 1;
 
       // ---- scores: token 16 t + g (and + 8), heads 8 n + 2 c (and + 1)
       float s[TB][NH][4];
@@ -490,17 +552,18 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
           const int tok = 16 * t + 8 * y + g;
           float kscale = 1.f, lift = 0.f;
           if (FP8) {
-            kscale = reinterpret_cast<const float*>(vs + S::kBytes)[tok];
-            vscale[t][y] = reinterpret_cast<const float*>(vs + S::kBytes)[TILE + tok];
-            lift = fmaxf(log2_of(vscale[t][y]), -100.f);
+            const float2 two = *reinterpret_cast<const float2*>(ks + S::kScales + tok * 8);
+            kscale = two.x, vscale[t][y] = two.y;
+            lift = fmaxf(log2_of(two.y), -100.f);
           }
+          // (a token that is not seen has a key of zeros)
+          const float bias = whole ? 0.f : reinterpret_cast<const float*>(ks + S::kBias)[tok];
 #pragma unroll
           for (int n = 0; n < NH; ++n)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               float& v = s[t][n][2 * y + x];
-              v *= FP8 ? row_scale[n][x] * kscale : row_scale[n][x];
-              if (mask != ALL) v = (mask >> tok) & 1u ? v : -INFINITY;
+              v = fmaf(v, FP8 ? row_scale[n][x] * kscale : row_scale[n][x], bias);
               top[n][x] = fmaxf(top[n][x], v + lift);
             }
         }
@@ -594,7 +657,8 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
 
       // ---- the end of a segment, or of the share
       const bool ends = at.tile + 1 == at.span.end;
-      if (ends || i + 1 == tiles) {
+      const bool last = place + (ends ? 1 + kBegin : 1) >= hi;
+      if (ends || last) {
 #pragma unroll
         for (int n = 0; n < NH; ++n) l[n][0] = tokens_sum(l[n][0]), l[n][1] = tokens_sum(l[n][1]);
         const int seg = at.b * p.chunks + at.chunk;
@@ -624,7 +688,6 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
           // Left open. What began in an earlier warp's share goes to the warp's own
           // place if more follows; the share's last goes where the ring was.
           const int which = began ? 1 : 0;
-          const bool last = i + 1 == tiles;
           float* to = kept;
           if (last) {
             copies_wait<0>();
@@ -647,14 +710,15 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
               if (g == 0) part_m[warp][which][row] = m[n][x], part_l[warp][which][row] = l[n][x];
             }
           if (lane == 0) {
-            if (which) seg_b[warp] = seg, end_b[warp] = lo + i + (at.span.end - at.tile);
+            if (which) seg_b[warp] = seg, end_b[warp] = place + (at.span.end - at.tile);
             else seg_a[warp] = seg, done_a[warp] = ends, away_a[warp] = !last;
           }
         }
         began = true;
         fresh = true;
       }
-      if (i + 1 < tiles) at.next(p);
+      if (last) break;
+      place += at.next(p);
     }
     copies_wait<0>();
   }

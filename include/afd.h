@@ -604,7 +604,7 @@ typedef struct afd_cache {
   float* k_scale;        /* device FP32 [num_pages][num_kv_heads][page_size] (E4M3), else NULL */
   float* v_scale;        /* not negative; zero or at least 2^-100 */
   int64_t k_page_stride; /* elements from a page to the next (the rest is dense): keys and values may */
-  int64_t v_page_stride; /*   be two halves of one allocation's pages */
+  int64_t v_page_stride; /*   be two halves of one allocation's pages; at most 32 GB */
   int32_t num_pages;
   int32_t page_size;     /* tokens of a page, any number */
   int32_t num_kv_heads;
