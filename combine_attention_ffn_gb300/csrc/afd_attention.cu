@@ -261,6 +261,8 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
   __shared__ float part_m[W][2][ROWS], part_l[W][2][ROWS];
   __shared__ int seg_a[W], seg_b[W], done_a[W], away_a[W];
   __shared__ int64_t end_b[W];
+  __shared__ int4 chains[W + 1];                   // {segment, first warp, end, whole}
+  __shared__ int chain_count;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
 
   afd::pdl_wait();
@@ -304,6 +306,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
       for (int i = threadIdx.x; i < p.Hq; i += THREADS) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
   }
 
+  const int groups = p.chunks / p.Hkv;  // chunks of a KV head
   uint8_t* ring = shared + warp * Y::kRing;
   float* kept = p.kept + (int64_t)worker * ROWS * D;
   if (lane == 0) seg_a[warp] = seg_b[warp] = -1, done_a[warp] = away_a[warp] = 0, end_b[warp] = 0;
@@ -333,7 +336,6 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
       at.tile = at.span.first + max(in - kBegin, 0);
       place += max(kBegin - in, 0);
     }
-    const int groups = p.chunks / p.Hkv;  // chunks of a KV head
     const bool runs = p.cache.page_size % kRun == 0;
 
     Cursor<TILE> ahead = at;
@@ -726,54 +728,62 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
 
   // ---- the block's open parts: a chain begins with the first warp's part of an
   // earlier block's segment, or with a warp's last one, and goes on through the
-  // next warps' first ones.
-  int tail = -1;
-  int64_t tail_end = 0;
-#pragma unroll 1
-  for (int w0 = -1; w0 < W; ++w0) {
-    const int seg = w0 < 0 ? seg_a[0] : seg_b[w0];
-    if (seg < 0) continue;
+  // next warps' first ones. All chains' rows are joined side by side.
+  if (warp == 0) {
+    const int w0 = lane - 1;
+    const int seg = lane > W ? -1 : w0 < 0 ? seg_a[0] : seg_b[w0];
     int w1 = w0 + 1;
     bool done = false;
-    while (w1 < W && seg_a[w1] == seg) done |= done_a[w1] != 0, ++w1;
-    const bool whole = w0 >= 0 && done;
-    if (w0 >= 0 && !done) tail = seg, tail_end = end_b[w0];
-    const int b = seg / p.chunks, chunk = seg % p.chunks, groups = p.chunks / p.Hkv;
-    const int head = chunk / groups, sub = chunk % groups;
-    const int rows = min(p.G - sub * ROWS, ROWS), q0 = head * p.G + sub * ROWS;
-    float* part = p.parts + ((int64_t)blockIdx.x * 2 + (w0 >= 0)) * ROWS * (D + 2);
-    for (int i = threadIdx.x; i < rows * (D / 8); i += THREADS) {
-      const int row = i / (D / 8), col = i % (D / 8) * 8;
-      float most = w0 >= 0 ? part_m[w0][1][row] : -INFINITY;
-      for (int w = w0 + 1; w < w1; ++w) most = fmaxf(most, part_m[w][0][row]);
-      const float minus = most == -INFINITY ? 0.f : most;
-      float sum = 0.f, f[8] = {};
-      for (int w = max(w0, 0); w < w1; ++w) {
-        const int which = w == w0;
-        const float scale = exp2_of(part_m[w][which][row] - minus);
-        const float* from = which || !away_a[w] ? reinterpret_cast<const float*>(shared + w * Y::kRing)
-                                                : p.kept + (int64_t)(blockIdx.x * W + w) * ROWS * D;
-        sum += part_l[w][which][row] * scale;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = fmaf(from[row * D + col + k], scale, f[k]);
-      }
-      if (whole) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] *= inv;
-        *reinterpret_cast<uint4*>(p.out + b * p.out_stride + (int64_t)(q0 + row) * D + col) = afd::float_to_bf16x8(f);
-        if (p.lse && col == 0) p.lse[(int64_t)b * p.Hq + q0 + row] = sum == 0.f ? -INFINITY : most * kLn2 + logf(sum);
-      } else {
-        *reinterpret_cast<float4*>(part + row * D + col) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4*>(part + row * D + col + 4) = make_float4(f[4], f[5], f[6], f[7]);
-        if (col == 0) part[ROWS * D + row] = most, part[ROWS * (D + 1) + row] = sum;
-      }
+    if (seg >= 0)
+      while (w1 < W && seg_a[w1] == seg) done |= done_a[w1] != 0, ++w1;
+    const unsigned found = __ballot_sync(kFull, seg >= 0);
+    if (seg >= 0) {
+      const bool whole = w0 >= 0 && done, tail = w0 >= 0 && !done;
+      chains[__popc(found & ((1u << lane) - 1))] = {seg, w0, w1, whole};
+      if (p.splits && tail) p.splits[blockIdx.x] = {seg, (int)((end_b[w0] * workers - 1) / total / W), {0, 0}};
+    }
+    const bool any = __any_sync(kFull, seg >= 0 && w0 >= 0 && !done);
+    if (lane == 0) {
+      chain_count = __popc(found);
+      if (p.splits && !any) p.splits[blockIdx.x] = {-1, 0, {0, 0}};
     }
   }
-  if (p.splits && threadIdx.x == 0) {
-    // the block with the segment's last tile: its first tile is at or before it
-    const int last = tail < 0 ? 0 : (int)((tail_end * workers - 1) / total / W);
-    p.splits[blockIdx.x] = {tail, last, {0, 0}};
+  __syncthreads();
+  constexpr int ITEMS = ROWS * (D / 8);  // of a chain
+#pragma unroll 1
+  for (int i = threadIdx.x; i < chain_count * ITEMS; i += THREADS) {
+    const int4 chain = chains[i / ITEMS];
+    const int seg = chain.x, w0 = chain.y, w1 = chain.z;
+    const int b = seg / p.chunks, chunk = seg % p.chunks, head = chunk / groups, sub = chunk % groups;
+    const int row = i % ITEMS / (D / 8), col = i % (D / 8) * 8;
+    if (row >= p.G - sub * ROWS) continue;
+    float most = w0 >= 0 ? part_m[w0][1][row] : -INFINITY;
+    for (int w = w0 + 1; w < w1; ++w) most = fmaxf(most, part_m[w][0][row]);
+    const float minus = most == -INFINITY ? 0.f : most;
+    float sum = 0.f, f[8] = {};
+    for (int w = max(w0, 0); w < w1; ++w) {
+      const int which = w == w0;
+      const float scale = exp2_of(part_m[w][which][row] - minus);
+      const float* from = (which || !away_a[w] ? reinterpret_cast<const float*>(shared + w * Y::kRing)
+                                               : p.kept + (int64_t)(blockIdx.x * W + w) * ROWS * D) + row * D + col;
+      const float4 x = *reinterpret_cast<const float4*>(from), y = *reinterpret_cast<const float4*>(from + 4);
+      sum = fmaf(part_l[w][which][row], scale, sum);
+      f[0] = fmaf(x.x, scale, f[0]), f[1] = fmaf(x.y, scale, f[1]), f[2] = fmaf(x.z, scale, f[2]), f[3] = fmaf(x.w, scale, f[3]);
+      f[4] = fmaf(y.x, scale, f[4]), f[5] = fmaf(y.y, scale, f[5]), f[6] = fmaf(y.z, scale, f[6]), f[7] = fmaf(y.w, scale, f[7]);
+    }
+    if (chain.w) {  // the segment is whole
+      const int q = head * p.G + sub * ROWS + row;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] *= inv;
+      *reinterpret_cast<uint4*>(p.out + b * p.out_stride + (int64_t)q * D + col) = afd::float_to_bf16x8(f);
+      if (p.lse && col == 0) p.lse[(int64_t)b * p.Hq + q] = sum == 0.f ? -INFINITY : most * kLn2 + logf(sum);
+    } else {
+      float* part = p.parts + ((int64_t)blockIdx.x * 2 + (w0 >= 0)) * ROWS * (D + 2);
+      *reinterpret_cast<float4*>(part + row * D + col) = make_float4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<float4*>(part + row * D + col + 4) = make_float4(f[4], f[5], f[6], f[7]);
+      if (col == 0) part[ROWS * D + row] = most, part[ROWS * (D + 1) + row] = sum;
+    }
   }
 }
 
