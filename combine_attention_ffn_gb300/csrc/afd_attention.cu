@@ -38,7 +38,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxBlocks = 160;
 constexpr int kMaxWarps = 16;
 constexpr float kLazy = 8.f;  // log2 of how far a score may pass the running maximum before that moves
-constexpr int kBegin = 1;   // what a segment costs beside its tiles, in tiles
+constexpr int kBegin = 2;   // what a segment costs beside its tiles, in tiles
 constexpr int kRun = 16;    // tokens that are in one page where its size is a multiple
 constexpr float kLn2 = 0.693147180559945f;
 
@@ -47,6 +47,13 @@ struct __align__(16) Split {
   int32_t seg;   // sequence * chunks of heads + chunk, or -1
   int32_t last;  // the last block that has a part of it
   int32_t pad[2];
+};
+
+// A segment's parts in a block: the last one of warp w0 (-1: none), the first ones
+// of the warps behind it before w1.
+struct Chain {
+  int32_t w0, w1, rows, whole;
+  int64_t out, lse;  // its first row
 };
 
 struct AttentionParams {
@@ -86,8 +93,12 @@ struct Shape {
 template <int D, bool FP8, int NH>
 struct Layout {
   using S = Shape<D, FP8>;
-  static constexpr int kWarps = 12;
-  static constexpr int kStages = 2;
+#ifndef AFD_W
+#define AFD_W 8
+#define AFD_S 2
+#endif
+  static constexpr int kWarps = AFD_W;
+  static constexpr int kStages = AFD_S;
   static constexpr int kRows = 8 * NH;
   static constexpr int kRing = kStages * S::kStage;
   static constexpr int kShared = kWarps * kRing;
@@ -150,6 +161,9 @@ __device__ __forceinline__ float log2_of(float v) {
   return r;
 }
 
+// The natural logarithm of sum * 2^most; the sum's own, good to 2^-22, by lg2.
+__device__ __forceinline__ float log_sum(float most, float sum) { return (most + log2_of(sum)) * kLn2; }
+
 // Over the eight lanes that hold other tokens of the same heads.
 __device__ __forceinline__ float tokens_max(float v) {
 #pragma unroll
@@ -181,6 +195,12 @@ __device__ __forceinline__ int swizzled(int row, int chunk) {
   if (ROW == 256) return row * 256 + ((chunk & 8) | ((chunk ^ row) & 7)) * 16;
   if (ROW == 128) return row * 128 + ((chunk ^ row) & 7) * 16;
   return row * 64 + ((chunk ^ (row >> 1)) & 3) * 16;
+}
+
+// Quotients of numbers that mostly have 32 bits (a division of 64 takes 200 ns).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
 }
 
 // The tiles [first, end) of a sequence that hold tokens [from, len).
@@ -261,7 +281,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
   __shared__ float part_m[W][2][ROWS], part_l[W][2][ROWS];
   __shared__ int seg_a[W], seg_b[W], done_a[W], away_a[W];
   __shared__ int64_t end_b[W];
-  __shared__ int4 chains[W + 1];                   // {segment, first warp, end, whole}
+  __shared__ Chain chains[W + 1];
   __shared__ int chain_count;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
 
@@ -291,10 +311,10 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
   }
   __syncthreads();
   const int64_t total = before[THREADS] * p.chunks;
-  // About a tile a warp at least: of few tiles the first blocks' warps take one each.
-  const int workers = (int)min(total, (int64_t)gridDim.x * W), worker = blockIdx.x * W + warp;
-  const bool works = worker < workers;
-  const int64_t lo = works ? total * worker / workers : 0, hi = works ? total * (worker + 1) / workers : 0;
+  // Equal shares, but of few tiles the first blocks' warps take one each.
+  const int64_t each_share = max(quotient(total + gridDim.x * W - 1, gridDim.x * W), (int64_t)(1 + kBegin));
+  const int worker = blockIdx.x * W + warp;
+  const int64_t lo = min(each_share * worker, total), hi = min(lo + each_share, total);
 
   // Sequences that see nothing.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -312,18 +332,19 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
   if (lane == 0) seg_a[warp] = seg_b[warp] = -1, done_a[warp] = away_a[warp] = 0, end_b[warp] = 0;
 
   if (lo < hi) {
-    // ---- where the share begins: `place` is that of the next tile on the line
+    // ---- where the share begins: the next tile is `place` behind it on the line
     Cursor<TILE> at;
-    int64_t place = lo;
+    int place = 0;
+    const int share = (int)(hi - lo);
     {
-      const int64_t line = lo / p.chunks;
       int i = 0;
 #pragma unroll 1
       for (int step = 256; step; step >>= 1)
-        if (i + step < THREADS && before[i + step] <= line) i += step;
+        if (i + step < THREADS && before[i + step] * p.chunks <= lo) i += step;
       int64_t left = lo - before[i] * p.chunks;
       at.b = i * each;
       at.span = span_of<TILE>(p, at.b);
+#pragma unroll 1
       for (;;) {
         const int64_t n = at.span.end > at.span.first ? (int64_t)(at.span.end - at.span.first + kBegin) * p.chunks : 0;
         if (left < n) break;
@@ -331,21 +352,31 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
         at.span = span_of<TILE>(p, ++at.b);
       }
       const int n = at.span.end - at.span.first + kBegin;
-      at.chunk = (int)(left / n);
-      const int in = (int)(left - (int64_t)at.chunk * n);
+      at.chunk = (int)quotient(left, n);
+      const int in = (int)(left - (int64_t)at.chunk * n);  // on the segment
       at.tile = at.span.first + max(in - kBegin, 0);
       place += max(kBegin - in, 0);
     }
     const bool runs = p.cache.page_size % kRun == 0;
 
+    // Places in a cache are counted in 64 bytes, which 32 bits hold.
+    const uint8_t *k_lane = p.cache.k + lane * 16, *v_lane = p.cache.v + lane * 16;
+    const uint32_t page_scales = p.Hkv * p.cache.page_size;
+    // A lane's place in the j-th 512 bytes of a stage's keys, or values: the rows of
+    // a step begin at a multiple of their number, so their swizzle is a constant.
+    const uint32_t own = swizzled<ROW>(lane / (ROW / 16), lane % (ROW / 16));
+    auto step_of = [&](int j) {
+      return j * 512 + (own ^ (ROW == 256 ? (j & 3) * 32 : ROW == 128 ? (j & 1) * 64 : 0));
+    };
     Cursor<TILE> ahead = at;
-    int64_t ahead_place = place;
+    int ahead_place = place;
     Lookup<TILE> next;
     next.update(p, ahead, runs, true, lane);
-    bool whole = true, next_whole = true;  // every token of the staged tile is seen
+    bool next_whole = true;   // every token of the tile staged last is seen ...
+    bool whole[Y::kStages];   // ... and of the tiles not taken yet
     // Starts the copies of the tile looked up last, and looks the one after it up.
     auto issue = [&](int stage) {
-      if (ahead_place < hi) {
+      if (ahead_place < share) {
         constexpr int CH = ROW / 16;  // chunks of a row
         uint8_t* to = ring + stage * S::kStage;
         const uint32_t dst = smem_addr(to);
@@ -360,17 +391,17 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
 #pragma unroll
           for (int r = 0; r < TILE / kRun; ++r) {
             const int page = __shfl_sync(kFull, next.page[0], r0 + r);
-            const uint32_t row = (uint32_t)(head * p.cache.page_size + __shfl_sync(kFull, next.at[0], r0 + r)) * CH + lane;
+            const uint32_t row = (uint32_t)(head * p.cache.page_size + __shfl_sync(kFull, next.at[0], r0 + r)) * (ROW / 64);
             ok[r] = (uint32_t)page < (uint32_t)p.cache.pages;
             const uint32_t pg = ok[r] ? (uint32_t)page : 0u;
-            k[r] = p.cache.k + (((uint64_t)pg * p.cache.k_page_units + row) << 4);
-            v[r] = p.cache.v + (((uint64_t)pg * p.cache.v_page_units + row) << 4);
+            k[r] = k_lane + (uint64_t)(pg * p.cache.k_page_units + row) * 64;
+            v[r] = v_lane + (uint64_t)(pg * p.cache.v_page_units + row) * 64;
             next_whole &= ok[r];
           }
           if (next_whole) {
 #pragma unroll
             for (int j = 0; j < S::kBytes / 512; ++j) {
-              const uint32_t d = dst + swizzled<ROW>((j * 32 + lane) / CH, (j * 32 + lane) % CH);
+              const uint32_t d = dst + step_of(j);
               copy16(d, k[j / JS] + j % JS * 512, true);
               copy16(d + S::kBytes, v[j / JS] + j % JS * 512, true);
             }
@@ -379,7 +410,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
             for (int j = 0; j < S::kBytes / 512; ++j) {
               const int row = (j * 32 + lane) / CH;
               const bool in = ok[j / JS] && row >= lowest && row < end;
-              const uint32_t d = dst + swizzled<ROW>(row, (j * 32 + lane) % CH);
+              const uint32_t d = dst + step_of(j);
               copy16(d, in ? k[j / JS] + j % JS * 512 : p.cache.k, in);
               copy16(d + S::kBytes, in ? v[j / JS] + j % JS * 512 : p.cache.v, in);
             }
@@ -389,10 +420,10 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
             for (int i = 0; i < Lookup<TILE>::N; ++i) {
               const int tok = (32 * i + lane) & (TILE - 1);
               const int page = __shfl_sync(kFull, next.page[0], r0 + tok / kRun);
-              const int row = head * p.cache.page_size + __shfl_sync(kFull, next.at[0], r0 + tok / kRun) + tok % kRun;
-              const bool in = tok >= lowest && tok < end && (uint32_t)page < (uint32_t)p.cache.pages;
+              const uint32_t row = head * p.cache.page_size + __shfl_sync(kFull, next.at[0], r0 + tok / kRun) + tok % kRun;
+              const bool in = next_whole || (tok >= lowest && tok < end && (uint32_t)page < (uint32_t)p.cache.pages);
               if (FP8) {
-                const int64_t o = in ? (int64_t)page * p.Hkv * p.cache.page_size + row : 0;
+                const uint32_t o = in ? (uint32_t)page * page_scales + row : 0;
                 copy4(dst + S::kScales + tok * 8, p.cache.k_scale + o, in);
                 copy4(dst + S::kScales + tok * 8 + 4, p.cache.v_scale + o, in);
               }
@@ -408,19 +439,18 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
             next_whole &= mask == kFull;
             const uint32_t row = (uint32_t)(head * p.cache.page_size + next.at[i]);
             const uint32_t pg = in ? (uint32_t)next.page[i] : 0u;
-            const uint64_t k_off = ((uint64_t)pg * p.cache.k_page_units + row * CH) << 4;
-            const uint64_t v_off = ((uint64_t)pg * p.cache.v_page_units + row * CH) << 4;
+            const uint32_t k_off = pg * p.cache.k_page_units + row * (ROW / 64), v_off = pg * p.cache.v_page_units + row * (ROW / 64);
 #pragma unroll 1
             for (int j = 0; j < (TILE < 32 ? TILE : 32) * CH / 32; ++j) {
               const int r = (j * 32 + lane) / CH, ch = (j * 32 + lane) % CH;
-              const uint64_t ko = __shfl_sync(kFull, k_off, r), vo = __shfl_sync(kFull, v_off, r);
+              const uint64_t ko = (uint64_t)__shfl_sync(kFull, k_off, r) * 64, vo = (uint64_t)__shfl_sync(kFull, v_off, r) * 64;
               const bool ok = (mask >> r) & 1u;
               const uint32_t d = dst + swizzled<ROW>(32 * i + r, ch);
               copy16(d, ok ? p.cache.k + ko + ch * 16 : p.cache.k, ok);
               copy16(d + S::kBytes, ok ? p.cache.v + vo + ch * 16 : p.cache.v, ok);
             }
             if (FP8) {
-              const int64_t o = in ? (int64_t)pg * p.Hkv * p.cache.page_size + row : 0;
+              const uint32_t o = in ? pg * page_scales + row : 0;
               copy4(dst + S::kScales + tok * 8, p.cache.k_scale + o, in);
               copy4(dst + S::kScales + tok * 8 + 4, p.cache.v_scale + o, in);
             }
@@ -429,12 +459,15 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
         }
         const int went = ahead.next(p);
         ahead_place += went;
-        if (ahead_place < hi) next.update(p, ahead, runs, went > 1, lane);
+        if (ahead_place < share) next.update(p, ahead, runs, went > 1, lane);
       }
       copies_commit();
     };
-    static_assert(Y::kStages == 2, "`whole` and `next_whole`");
-    issue(0);
+#pragma unroll
+    for (int i = 0; i < Y::kStages - 1; ++i) {
+      issue(i);
+      whole[i] = next_whole;
+    }
 
     uint32_t qb[NH][D / 16][2];
     float row_scale[NH][2];
@@ -498,16 +531,19 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
     bool fresh = true;
     int stage = 0;
 #pragma unroll 1
-    while (place < hi) {  // (a share may hold a segment's beginning alone)
-      copies_wait<0>();
+    while (place < share) {  // (a share may hold a segment's beginning alone)
+      copies_wait<Y::kStages - 2>();
       __syncwarp();
-      whole = next_whole;
-      issue(stage ^ 1);  // into the stage that the last tile has left
+      const bool all = whole[0];
+      issue(stage ? stage - 1 : Y::kStages - 1);  // into the stage that the last tile has left
+#pragma unroll
+      for (int i = 0; i < Y::kStages - 2; ++i) whole[i] = whole[i + 1];
+      whole[Y::kStages - 2] = next_whole;
       if (fresh) load_q();
       fresh = false;
       const uint8_t* ks = ring + stage * S::kStage;
       const uint8_t* vs = ks + S::kBytes;
-      stage ^= 1;
+      stage = stage + 1 == Y::kStages ? 0 : stage + 1;
 
       // ---- scores: token 16 t + g (and + 8), heads 8 n + 2 c (and + 1)
       float s[TB][NH][4];
@@ -559,7 +595,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
             lift = fmaxf(log2_of(two.y), -100.f);
           }
           // (a token that is not seen has a key of zeros)
-          const float bias = whole ? 0.f : reinterpret_cast<const float*>(ks + S::kBias)[tok];
+          const float bias = all ? 0.f : reinterpret_cast<const float*>(ks + S::kBias)[tok];
 #pragma unroll
           for (int n = 0; n < NH; ++n)
 #pragma unroll
@@ -659,7 +695,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
 
       // ---- the end of a segment, or of the share
       const bool ends = at.tile + 1 == at.span.end;
-      const bool last = place + (ends ? 1 + kBegin : 1) >= hi;
+      const bool last = place + (ends ? 1 + kBegin : 1) >= share;
       if (ends || last) {
 #pragma unroll
         for (int n = 0; n < NH; ++n) l[n][0] = tokens_sum(l[n][0]), l[n][1] = tokens_sum(l[n][1]);
@@ -684,7 +720,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
                   for (int k = 0; k < 8; ++k) f[k] = o[(h * E + e + k) / 2][n][2 * (k & 1) + x] * inv;
                   *reinterpret_cast<uint4*>(out + (8 * h + g) * E + e) = afd::float_to_bf16x8(f);
                 }
-              if (p.lse && g == 0) p.lse[(int64_t)at.b * p.Hq + q0 + row] = l[n][x] == 0.f ? -INFINITY : m[n][x] * kLn2 + logf(l[n][x]);
+              if (p.lse && g == 0) p.lse[(int64_t)at.b * p.Hq + q0 + row] = l[n][x] == 0.f ? -INFINITY : log_sum(m[n][x], l[n][x]);
             }
         } else {
           // Left open. What began in an earlier warp's share goes to the warp's own
@@ -712,7 +748,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
               if (g == 0) part_m[warp][which][row] = m[n][x], part_l[warp][which][row] = l[n][x];
             }
           if (lane == 0) {
-            if (which) seg_b[warp] = seg, end_b[warp] = place + (at.span.end - at.tile);
+            if (which) seg_b[warp] = seg, end_b[warp] = lo + place + (at.span.end - at.tile);
             else seg_a[warp] = seg, done_a[warp] = ends, away_a[warp] = !last;
           }
         }
@@ -736,33 +772,38 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
     bool done = false;
     if (seg >= 0)
       while (w1 < W && seg_a[w1] == seg) done |= done_a[w1] != 0, ++w1;
-    const unsigned found = __ballot_sync(kFull, seg >= 0);
+    const bool open = seg >= 0 && w0 >= 0 && !done;
+    const unsigned found = __ballot_sync(kFull, seg >= 0), opens = __ballot_sync(kFull, open);
     if (seg >= 0) {
-      const bool whole = w0 >= 0 && done, tail = w0 >= 0 && !done;
-      chains[__popc(found & ((1u << lane) - 1))] = {seg, w0, w1, whole};
-      if (p.splits && tail) p.splits[blockIdx.x] = {seg, (int)((end_b[w0] * workers - 1) / total / W), {0, 0}};
+      const int b = seg / p.chunks, chunk = seg - b * p.chunks, head = chunk / groups, sub = chunk - head * groups;
+      Chain c;
+      c.w0 = w0, c.w1 = w1, c.rows = min(p.G - sub * ROWS, ROWS), c.whole = w0 >= 0 && done;
+      const int q = head * p.G + sub * ROWS;
+      c.out = b * p.out_stride + (int64_t)q * D;
+      c.lse = (int64_t)b * p.Hq + q;
+      chains[__popc(found & ((1u << lane) - 1))] = c;
     }
-    const bool any = __any_sync(kFull, seg >= 0 && w0 >= 0 && !done);
-    if (lane == 0) {
-      chain_count = __popc(found);
-      if (p.splits && !any) p.splits[blockIdx.x] = {-1, 0, {0, 0}};
-    }
+    // (the one segment that goes on behind the block, if there is one)
+    if (p.splits && (open || (lane == 0 && !opens)))
+      p.splits[blockIdx.x] = {open ? seg : -1, open ? (int)(quotient(end_b[w0] - 1, each_share) / W) : 0, {0, 0}};
+    if (lane == 0) chain_count = __popc(found);
   }
   __syncthreads();
+  // Eight columns of a row a thread. (Code that runs once is fetched from L2 as it
+  // runs: it is kept short.)
   constexpr int ITEMS = ROWS * (D / 8);  // of a chain
 #pragma unroll 1
   for (int i = threadIdx.x; i < chain_count * ITEMS; i += THREADS) {
-    const int4 chain = chains[i / ITEMS];
-    const int seg = chain.x, w0 = chain.y, w1 = chain.z;
-    const int b = seg / p.chunks, chunk = seg % p.chunks, head = chunk / groups, sub = chunk % groups;
+    const Chain& c = chains[i / ITEMS];
     const int row = i % ITEMS / (D / 8), col = i % (D / 8) * 8;
-    if (row >= p.G - sub * ROWS) continue;
-    float most = w0 >= 0 ? part_m[w0][1][row] : -INFINITY;
-    for (int w = w0 + 1; w < w1; ++w) most = fmaxf(most, part_m[w][0][row]);
+    if (row >= c.rows) continue;
+    float most = -INFINITY, sum = 0.f, f[8] = {};
+#pragma unroll 1
+    for (int w = max(c.w0, 0); w < c.w1; ++w) most = fmaxf(most, part_m[w][w == c.w0][row]);
     const float minus = most == -INFINITY ? 0.f : most;
-    float sum = 0.f, f[8] = {};
-    for (int w = max(w0, 0); w < w1; ++w) {
-      const int which = w == w0;
+#pragma unroll 1
+    for (int w = max(c.w0, 0); w < c.w1; ++w) {
+      const int which = w == c.w0;
       const float scale = exp2_of(part_m[w][which][row] - minus);
       const float* from = (which || !away_a[w] ? reinterpret_cast<const float*>(shared + w * Y::kRing)
                                                : p.kept + (int64_t)(blockIdx.x * W + w) * ROWS * D) + row * D + col;
@@ -771,15 +812,14 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
       f[0] = fmaf(x.x, scale, f[0]), f[1] = fmaf(x.y, scale, f[1]), f[2] = fmaf(x.z, scale, f[2]), f[3] = fmaf(x.w, scale, f[3]);
       f[4] = fmaf(y.x, scale, f[4]), f[5] = fmaf(y.y, scale, f[5]), f[6] = fmaf(y.z, scale, f[6]), f[7] = fmaf(y.w, scale, f[7]);
     }
-    if (chain.w) {  // the segment is whole
-      const int q = head * p.G + sub * ROWS + row;
+    if (c.whole) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] *= inv;
-      *reinterpret_cast<uint4*>(p.out + b * p.out_stride + (int64_t)q * D + col) = afd::float_to_bf16x8(f);
-      if (p.lse && col == 0) p.lse[(int64_t)b * p.Hq + q] = sum == 0.f ? -INFINITY : most * kLn2 + logf(sum);
+      *reinterpret_cast<uint4*>(p.out + c.out + row * D + col) = afd::float_to_bf16x8(f);
+      if (p.lse && col == 0) p.lse[c.lse + row] = sum == 0.f ? -INFINITY : log_sum(most, sum);
     } else {
-      float* part = p.parts + ((int64_t)blockIdx.x * 2 + (w0 >= 0)) * ROWS * (D + 2);
+      float* part = p.parts + ((int64_t)blockIdx.x * 2 + (c.w0 >= 0)) * ROWS * (D + 2);
       *reinterpret_cast<float4*>(part + row * D + col) = make_float4(f[0], f[1], f[2], f[3]);
       *reinterpret_cast<float4*>(part + row * D + col + 4) = make_float4(f[4], f[5], f[6], f[7]);
       if (col == 0) part[ROWS * D + row] = most, part[ROWS * (D + 1) + row] = sum;
@@ -829,7 +869,7 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const AttentionParams 
   uint32_t* out = reinterpret_cast<uint32_t*>(p.out + b * p.out_stride + (int64_t)q * D + lane * N);
 #pragma unroll
   for (int k = 0; k < N; k += 2) out[k / 2] = afd::pack_bf16(f[k] * inv, f[k + 1] * inv);
-  if (p.lse && lane == 0) p.lse[(int64_t)b * p.Hq + q] = sum == 0.f ? -INFINITY : most * kLn2 + logf(sum);
+  if (p.lse && lane == 0) p.lse[(int64_t)b * p.Hq + q] = sum == 0.f ? -INFINITY : log_sum(most, sum);
 }
 
 int tile_tokens(int head_dim, bool fp8) { return head_dim == 128 && !fp8 ? 16 : 32; }

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const WriteP
       *reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + head * D + c) = afd::float_to_bf16x8(f);
     } else if (kept) {
       const int64_t row = (int64_t)h * p.cache.page_size + in_page;
-      uint8_t* to = key ? p.cache.k + page * p.cache.k_page_units * 16 : p.cache.v + page * p.cache.v_page_units * 16;
+      uint8_t* to = key ? p.cache.k + page * p.cache.k_page_units * 64 : p.cache.v + page * p.cache.v_page_units * 64;
       if (FP8) {
         *reinterpret_cast<uint2*>(to + row * D + c) = afd::to_e4m3x8(f, 1.f / scale);
         if (c == 0) (key ? p.cache.k_scale : p.cache.v_scale)[page * p.Hkv * p.cache.page_size + row] = scale;

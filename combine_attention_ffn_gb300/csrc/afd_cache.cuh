@@ -10,12 +10,12 @@
 namespace afd {
 
 constexpr int kMaxHeads = 1024;
-constexpr int64_t kMaxPage = (int64_t)1 << 35;  // bytes from a page to the next: 16-byte units, and a page's, in 32 bits
+constexpr int64_t kMaxCacheBytes = (int64_t)1 << 38;  // of keys, or values: places in units of 64 bytes in 32 bits
 
 struct CacheParams {
   uint8_t* k;
   uint8_t* v;
-  uint32_t k_page_units, v_page_units;  // of 16 bytes, from a page to the next
+  uint32_t k_page_units, v_page_units;  // of 64 bytes, from a page to the next
   float* k_scale;  // [pages][heads][page_size], E4M3 only
   float* v_scale;
   int32_t pages, page_size;
@@ -39,9 +39,9 @@ inline afd_status check_cache(const afd_cache* c) {
   }
   if (c->head_dim != 64 && c->head_dim != 128) return AFD_ERR_UNSUPPORTED;
   if (c->num_kv_heads > kMaxHeads || (int64_t)c->num_pages * c->page_size > INT32_MAX) return AFD_ERR_UNSUPPORTED;
-  if (c->num_pages > 0 && (c->k_page_stride > kMaxPage / each || c->v_page_stride > kMaxPage / each ||
-                           c->k_page_stride * each % 16 || c->v_page_stride * each % 16 || !aligned_to(c->k, 16) ||
-                           !aligned_to(c->v, 16)))
+  if (c->num_pages > 0 &&
+      (c->k_page_stride > kMaxCacheBytes / each / c->num_pages || c->v_page_stride > kMaxCacheBytes / each / c->num_pages ||
+       c->k_page_stride * each % 64 || c->v_page_stride * each % 64 || !aligned_to(c->k, 16) || !aligned_to(c->v, 16)))
     return AFD_ERR_UNSUPPORTED;
   return AFD_OK;
 }
@@ -50,7 +50,7 @@ inline afd_status check_cache(const afd_cache* c) {
 inline bool view_cache(const afd_cache* c, CacheParams* out) {
   const int64_t each = c->dtype == AFD_FP8_E4M3 ? 1 : 2;
   *out = {};
-  out->k_page_units = (uint32_t)(c->k_page_stride * each / 16), out->v_page_units = (uint32_t)(c->v_page_stride * each / 16);
+  out->k_page_units = (uint32_t)(c->k_page_stride * each / 64), out->v_page_units = (uint32_t)(c->v_page_stride * each / 64);
   out->pages = c->num_pages, out->page_size = c->page_size;
   if (c->num_pages == 0) return true;
   return device_view(static_cast<uint8_t*>(c->k), &out->k) && device_view(static_cast<uint8_t*>(c->v), &out->v) &&

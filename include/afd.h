@@ -604,9 +604,9 @@ typedef struct afd_cache {
   float* k_scale;        /* device FP32 [num_pages][num_kv_heads][page_size] (E4M3), else NULL */
   float* v_scale;        /* not negative; zero or at least 2^-100 */
   int64_t k_page_stride; /* elements from a page to the next (the rest is dense): keys and values may */
-  int64_t v_page_stride; /*   be two halves of one allocation's pages; at most 32 GB */
-  int32_t num_pages;
-  int32_t page_size;     /* tokens of a page, any number */
+  int64_t v_page_stride; /*   be two halves of one allocation's pages; multiples of 64 bytes */
+  int32_t num_pages;     /* num_pages * page stride at most 256 GB each */
+  int32_t page_size;     /* tokens of a page, any number; multiples of 16 are read fastest */
   int32_t num_kv_heads;
   int32_t head_dim;      /* 64 or 128 */
   int32_t dtype;         /* AFD_BF16 or AFD_FP8_E4M3 */
@@ -632,8 +632,8 @@ typedef struct afd_cache {
  *              tokens with the same slot leave parts of either there.
  *   q_out      device BF16 [num_tokens, num_q_heads, head_dim], row stride
  *              q_out_stride; may be q itself (the same address and stride)
- * Limits: at most 1,024 heads of either kind; q, k, v, q_out, the caches' pages
- * and the strides multiples of 16 bytes; num_pages * page_size below 2^31.
+ * Limits: at most 1,024 heads of either kind; q, k, v, q_out, the caches
+ * and the rows' strides multiples of 16 bytes; num_pages * page_size below 2^31.
  * Buffers may be device, managed or page-locked host memory.
  * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (limits), AFD_ERR_CUDA. */
 AFD_API afd_status afd_cache_write(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
