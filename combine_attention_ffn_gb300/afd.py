@@ -698,7 +698,16 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
 
 
 # -- the source's side of an exchange (afd.h: no context, no state) -----------
-# Forward only, as the experts' side.
+# Forward only, as the experts' side. New tensors need no checks: what the
+# binding spends on a call is more than the GPU does at decode sizes.
+_BF16_T = torch.bfloat16
+
+
+def _grad_of(*tensors) -> bool:
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return True
+    return False
 
 
 class NormRows(NamedTuple):
@@ -729,11 +738,9 @@ def norm_rows(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, resid
     shape = T, H = x.shape
     if H > _INT32:
         raise _too_large(H)
-    if _grad_enabled() and (x.requires_grad or weight.requires_grad
-                            or any(t is not None and t.requires_grad
-                                   for t in (residual, out, residual_out, fp8_out, scale_out))):
+    if _grad_enabled() and _grad_of(x, weight, residual, out, residual_out, fp8_out, scale_out):
         raise _no_backward()
-    bf16 = torch.bfloat16
+    bf16, device = _BF16_T, x.device
     x_stride = _want_rows(x, "x", bf16, shape)
     weight_ptr = _want(weight, "weight", bf16, (H,))
     res_ptr = res_out_ptr = out_ptr = fp8_ptr = scale_ptr = None
@@ -741,23 +748,30 @@ def norm_rows(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, resid
     if residual is not None:
         res_stride, res_ptr = _want_rows(residual, "residual", bf16, shape), residual.data_ptr()
         if residual_out is None:
-            residual_out = _empty(shape, bf16, x.device, stream)
-        res_out_stride, res_out_ptr = _want_rows(residual_out, "residual_out", bf16, shape), residual_out.data_ptr()
+            residual_out, res_out_stride = _empty(shape, bf16, device, stream), H
+        else:
+            res_out_stride = _want_rows(residual_out, "residual_out", bf16, shape)
+        res_out_ptr = residual_out.data_ptr()
     elif residual_out is not None:
         raise AfdError(ERR_ARG, "residual_out needs a residual")
-    if rows or out is not None:
-        if out is None:
-            out = _empty(shape, bf16, x.device, stream)
+    if out is not None:
         out_stride, out_ptr = _want_rows(out, "out", bf16, shape), out.data_ptr()
+    elif rows:
+        out, out_stride = _empty(shape, bf16, device, stream), H
+        out_ptr = out.data_ptr()
     if fp8 or fp8_out is not None or scale_out is not None:
         if H % 128:
             raise AfdError(ERR_ARG, f"float8_e4m3fn rows take a multiple of 128 columns, got {H}")
         if fp8_out is None:
-            fp8_out = _empty(shape, torch.float8_e4m3fn, x.device, stream)
+            fp8_out = _empty(shape, torch.float8_e4m3fn, device, stream)
+            fp8_ptr = fp8_out.data_ptr()
+        else:
+            fp8_ptr = _want(fp8_out, "fp8_out", torch.float8_e4m3fn, shape)
         if scale_out is None:
-            scale_out = _empty((T, H // 128), torch.float32, x.device, stream)
-        fp8_ptr = _want(fp8_out, "fp8_out", torch.float8_e4m3fn, shape)
-        scale_ptr = _want(scale_out, "scale_out", torch.float32, (T, H // 128))
+            scale_out = _empty((T, H // 128), torch.float32, device, stream)
+            scale_ptr = scale_out.data_ptr()
+        else:
+            scale_ptr = _want(scale_out, "scale_out", torch.float32, (T, H // 128))
     _call("afd_norm_rows", x, stream, x.data_ptr(), x_stride, res_ptr, res_stride, weight_ptr, eps, T, H, res_out_ptr,
           res_out_stride, out_ptr, out_stride, fp8_ptr, scale_ptr)
     return NormRows(out, fp8_out, scale_out, residual_out)
@@ -766,42 +780,48 @@ def norm_rows(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, resid
 def _heads(t: torch.Tensor, name: str, tokens: int, dim: int) -> int:
     """Checks a [T, heads, dim] tensor whose rows may be strided; returns the
     row stride in elements."""
-    if t.dim() == 3 and t.dtype is torch.bfloat16 and t.shape[0] == tokens and t.shape[2] == dim:
-        row, head, col = t.stride()
-        heads = t.shape[1]
-        if tokens <= 1:
-            row = heads * dim
-        if col == 1 and (head == dim or heads <= 1) and row >= heads * dim:
-            return row
+    if t.dim() == 3 and t.dtype is _BF16_T:
+        n, heads, d = t.shape
+        if n == tokens and d == dim:
+            row, head, col = t.stride()
+            if tokens <= 1:
+                row = heads * dim
+            if col == 1 and (head == dim or heads <= 1) and row >= heads * dim:
+                return row
     raise AfdError(ERR_ARG, f"{name} must be bfloat16 [{tokens}, heads, {dim}] with dense rows, got {t.dtype} {list(t.shape)}")
+
+
+def _dense_pages(t: torch.Tensor, name: str, pages: int, heads: int, page: int, dim: int) -> int:
+    """Checks that a cache's pages are dense; returns the page stride in elements."""
+    s = t.stride()
+    size = heads * page * dim
+    if (s[3] != 1 and dim > 1) or (s[2] != dim and page > 1) or (s[1] != page * dim and heads > 1):
+        raise AfdError(ERR_ARG, f"{name} must have dense pages, got strides {list(s)}")
+    return s[0] if pages > 1 else size
 
 
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale) -> Cache:
     """The descriptor of a cache."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype \
-            or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+    shape, dtype = k_cache.shape, k_cache.dtype
+    fp8 = dtype is torch.float8_e4m3fn
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not dtype or not (fp8 or dtype is _BF16_T):
         raise AfdError(ERR_ARG, "k_cache and v_cache must be bfloat16 or float8_e4m3fn [pages, KV heads, page size, head size], "
                        f"got {k_cache.dtype} {list(k_cache.shape)} and {v_cache.dtype} {list(v_cache.shape)}")
-    pages, heads, page, dim = k_cache.shape
+    pages, heads, page, dim = shape
     if pages > _INT32 or heads > _INT32 or page > _INT32 or dim > _INT32:
         raise _too_large(pages, heads, page, dim)
-    strides = []
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        s = t.stride()
-        dense = (page * dim, dim, 1)
-        if any(n > 1 and a != b for n, a, b in zip((heads, page, dim), s[1:], dense)):
-            raise AfdError(ERR_ARG, f"{name} must have dense pages, got strides {list(s)}")
-        strides.append(s[0] if pages > 1 else heads * page * dim)
+    k_stride = _dense_pages(k_cache, "k_cache", pages, heads, page, dim)
+    v_stride = _dense_pages(v_cache, "v_cache", pages, heads, page, dim)
     ks = vs = None
-    if k_cache.dtype is torch.float8_e4m3fn:
+    if fp8:
         if k_scale is None or v_scale is None:
             raise AfdError(ERR_ARG, "a float8_e4m3fn cache takes k_scale and v_scale")
         ks = _want(k_scale, "k_scale", torch.float32, (pages, heads, page))
         vs = _want(v_scale, "v_scale", torch.float32, (pages, heads, page))
     elif k_scale is not None or v_scale is not None:
         raise AfdError(ERR_ARG, "a bfloat16 cache takes no scales")
-    return Cache(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, strides[0], strides[1], pages, page, heads, dim,
-                 BF16 if ks is None else FP8_E4M3)
+    return Cache(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, k_stride, v_stride, pages, page, heads, dim,
+                 FP8_E4M3 if fp8 else BF16)
 
 
 def cache_write(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
@@ -823,8 +843,7 @@ def cache_write(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pos
     `v_cache` are [pages, Hkv, page_size, D], bf16, or float8_e4m3fn with
     `k_scale` and `v_scale` float32 [pages, Hkv, page_size]. See
     afd_cache_write in include/afd.h."""
-    if _grad_enabled() and any(t is not None and t.requires_grad for t in
-                               (q, k, v, inv_freq, k_cache, v_cache, k_scale, v_scale, q_out)):
+    if _grad_enabled() and _grad_of(q, k, v, inv_freq, k_cache, v_cache, k_scale, v_scale, q_out):
         raise _no_backward()
     cache = _cache(k_cache, v_cache, k_scale, v_scale)
     dim, heads = cache.head_dim, cache.num_kv_heads
@@ -848,10 +867,11 @@ def cache_write(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pos
         if Hq > _INT32:
             raise _too_large(Hq)
         if q_out is None:
-            q_out = _empty((T, Hq, dim), torch.bfloat16, q.device, stream)
-        out_stride = _heads(q_out, "q_out", T, dim)
-        if q_out.shape[1] != Hq:
-            raise AfdError(ERR_ARG, f"q_out must have {Hq} heads, got {q_out.shape[1]}")
+            q_out, out_stride = _empty((T, Hq, dim), _BF16_T, q.device, stream), Hq * dim
+        else:
+            out_stride = _heads(q_out, "q_out", T, dim)
+            if q_out.shape[1] != Hq:
+                raise AfdError(ERR_ARG, f"q_out must have {Hq} heads, got {q_out.shape[1]}")
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise AfdError(ERR_ARG, "q_out needs q")
@@ -875,7 +895,7 @@ def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     new one counted; with `window` only that many last ones are seen. `scale`
     defaults to D ** -0.5. A sequence that sees nothing gets zeros and an lse of
     -inf. See afd_decode_attention in include/afd.h."""
-    if _grad_enabled() and any(t is not None and t.requires_grad for t in (q, k_cache, v_cache, k_scale, v_scale, out, lse)):
+    if _grad_enabled() and _grad_of(q, k_cache, v_cache, k_scale, v_scale, out, lse):
         raise _no_backward()
     cache = _cache(k_cache, v_cache, k_scale, v_scale)
     dim, heads = cache.head_dim, cache.num_kv_heads
@@ -888,20 +908,25 @@ def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     q_stride = _heads(q, "q", B, dim)
     table_stride = _want_rows(page_table, "page_table", torch.int32, (B, width))
     lengths_ptr = _want(lengths, "lengths", torch.int32, (B,))
+    device = q.device
     if out is None:
-        out = _empty((B, Hq, dim), torch.bfloat16, q.device, stream)
-    out_stride = _heads(out, "out", B, dim)
-    if out.shape[1] != Hq:
-        raise AfdError(ERR_ARG, f"out must have {Hq} heads, got {out.shape[1]}")
-    if lse is None and return_lse:
-        lse = _empty((B, Hq), torch.float32, q.device, stream)
-    lse_ptr = None if lse is None else _want(lse, "lse", torch.float32, (B, Hq))
+        out, out_stride = _empty((B, Hq, dim), _BF16_T, device, stream), Hq * dim
+    else:
+        out_stride = _heads(out, "out", B, dim)
+        if out.shape[1] != Hq:
+            raise AfdError(ERR_ARG, f"out must have {Hq} heads, got {out.shape[1]}")
+    lse_ptr = workspace_ptr = None
+    if lse is not None:
+        lse_ptr = _want(lse, "lse", torch.float32, (B, Hq))
+    elif return_lse:
+        lse = _empty((B, Hq), torch.float32, device, stream)
+        lse_ptr = lse.data_ptr()
     size = (_lib or load_library()).afd_decode_workspace_bytes(B, Hq, heads, dim, width, cache.page_size)
-    workspace = None
     if size > 0:
-        on = q.device if q.is_cuda else torch.device("cuda", _current_device())
+        on = device if q.is_cuda else torch.device("cuda", _current_device())
         workspace = _empty(size, torch.uint8, on, stream)
+        workspace_ptr = workspace.data_ptr()
     _call("afd_decode_attention", q, stream, q.data_ptr(), q_stride, cache, page_table.data_ptr(), table_stride, width,
           lengths_ptr, B, Hq, dim ** -0.5 if scale is None else scale, window, out.data_ptr(), out_stride, lse_ptr,
-          None if workspace is None else workspace.data_ptr(), size)
+          workspace_ptr, size)
     return (out, lse) if lse is not None else out

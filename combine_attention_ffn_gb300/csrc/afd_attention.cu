@@ -36,9 +36,13 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxBlocks = 160;
-constexpr int kMaxWarps = 16;
+constexpr int kWarps = 8;         // of a block
+constexpr int kStages = 2;        // tiles of a warp's ring
+constexpr int kSoloBlocks = 148;  // no more than SMs
 constexpr float kLazy = 8.f;  // log2 of how far a score may pass the running maximum before that moves
 constexpr int kBegin = 2;   // what a segment costs beside its tiles, in tiles
+constexpr int kSolo = 4;    // tiles a warp up to which a block takes a whole segment
+constexpr int kDry = 8;     // places up to which a share begins with a dry pass
 constexpr int kRun = 16;    // tokens that are in one page where its size is a multiple
 constexpr float kLn2 = 0.693147180559945f;
 
@@ -66,6 +70,7 @@ struct AttentionParams {
   const int32_t* lengths;
   int32_t B, Hq, Hkv, G, chunks;  // chunks: of at most 8 or 16 query heads, all KV heads'
   int32_t page_shift;             // log2 of the page size, or -1
+  int32_t solo;                   // every segment has a block of its own, whatever the lengths are
   float scale_log2;
   int32_t window;
   uint16_t* out;
@@ -88,22 +93,14 @@ struct Shape {
   static constexpr int H = D / 8 / E;                        // ... and how many such groups
 };
 
-// Warps of a block and stages of a warp's ring; NH: query heads of a chunk, in
-// eights.
+// NH: query heads of a chunk, in eights.
 template <int D, bool FP8, int NH>
 struct Layout {
   using S = Shape<D, FP8>;
-#ifndef AFD_W
-#define AFD_W 8
-#define AFD_S 2
-#endif
-  static constexpr int kWarps = AFD_W;
-  static constexpr int kStages = AFD_S;
   static constexpr int kRows = 8 * NH;
   static constexpr int kRing = kStages * S::kStage;
   static constexpr int kShared = kWarps * kRing;
   static_assert(kStages >= 2 && kRing >= kRows * D * 4, "a part goes where the ring was");
-  static_assert(kWarps <= kMaxWarps);
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -271,10 +268,10 @@ struct Lookup {
 };
 
 template <int D, bool FP8, int NH>
-__global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_attention_kernel(const AttentionParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const AttentionParams p) {
   using S = Shape<D, FP8>;
   using Y = Layout<D, FP8, NH>;
-  constexpr int TILE = S::kTile, ROW = S::kRow, E = S::E, H = S::H, TB = TILE / 16, W = Y::kWarps, ROWS = Y::kRows;
+  constexpr int TILE = S::kTile, ROW = S::kRow, E = S::E, H = S::H, TB = TILE / 16, W = kWarps, ROWS = Y::kRows;
   constexpr int THREADS = W * 32;
   extern __shared__ __align__(128) uint8_t shared[];
   __shared__ int64_t before[THREADS + 1];          // the line before each thread's sequences, of one chunk
@@ -290,12 +287,15 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
 
   // ---- the line, and this warp's share of it
   const int each = (p.B + THREADS - 1) / THREADS;
-  {
+  bool solo = p.solo;
+  if (!solo) {
     int64_t mine = 0;
+    int longest = 0;
     const int b0 = threadIdx.x * each, b1 = min(p.B, b0 + each);
     for (int b = b0; b < b1; ++b) {
       const Span s = span_of<TILE>(p, b);
       mine += s.end > s.first ? s.end - s.first + kBegin : 0;
+      longest = max(longest, s.end - s.first);
     }
     int64_t sum = mine;
 #pragma unroll
@@ -304,39 +304,31 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
       if (lane >= d) sum += o;
     }
     if (lane == 31) end_b[warp] = sum;
-    __syncthreads();
+    // Short sequences, and a block for each: nothing is left for the second kernel.
+    solo = __syncthreads_and(longest <= kSolo * W && p.B * p.chunks <= gridDim.x);
     for (int w = 0; w < warp; ++w) sum += end_b[w];
     before[threadIdx.x + 1] = sum;
     if (threadIdx.x == 0) before[0] = 0;
+    __syncthreads();
   }
-  __syncthreads();
-  const int64_t total = before[THREADS] * p.chunks;
-  // Equal shares, but of few tiles the first blocks' warps take one each.
-  const int64_t each_share = max(quotient(total + gridDim.x * W - 1, gridDim.x * W), (int64_t)(1 + kBegin));
-  const int worker = blockIdx.x * W + warp;
-  const int64_t lo = min(each_share * worker, total), hi = min(lo + each_share, total);
-
-  // Sequences that see nothing.
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const Span s = span_of<TILE>(p, b);
-    if (s.first != s.end) continue;
-    for (int i = threadIdx.x; i < p.Hq * (D / 8); i += THREADS)
-      *reinterpret_cast<uint4*>(p.out + b * p.out_stride + i * 8) = make_uint4(0, 0, 0, 0);
-    if (p.lse)
-      for (int i = threadIdx.x; i < p.Hq; i += THREADS) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
-  }
-
-  const int groups = p.chunks / p.Hkv;  // chunks of a KV head
-  uint8_t* ring = shared + warp * Y::kRing;
-  float* kept = p.kept + (int64_t)worker * ROWS * D;
-  if (lane == 0) seg_a[warp] = seg_b[warp] = -1, done_a[warp] = away_a[warp] = 0, end_b[warp] = 0;
-
-  if (lo < hi) {
-    // ---- where the share begins: the next tile is `place` behind it on the line
-    Cursor<TILE> at;
-    int place = 0;
-    const int share = (int)(hi - lo);
-    {
+  Cursor<TILE> at;
+  int64_t lo = 0, each_share = 1;  // this warp's first place on the line, and those of a warp
+  int share = 0, place = 0;        // places it has; where its next tile is behind the first
+  if (solo) {
+    const int seg = min((int)blockIdx.x, p.B * p.chunks - 1);
+    at.b = seg / p.chunks, at.chunk = seg - at.b * p.chunks;
+    at.span = span_of<TILE>(p, at.b);
+    const int n = (int)blockIdx.x == seg ? at.span.end - at.span.first : 0, per = (n + W - 1) / W;
+    const int first = min(per * warp, n);
+    at.tile = at.span.first + first;
+    share = min(per, n - first);
+  } else {
+    // Equal shares, but of few tiles the first blocks' warps take one each.
+    const int64_t total = before[THREADS] * p.chunks;
+    each_share = max(quotient(total + gridDim.x * W - 1, gridDim.x * W), (int64_t)(1 + kBegin));
+    lo = min(each_share * (blockIdx.x * W + warp), total);
+    share = (int)min(each_share, total - lo);
+    if (share > 0) {
       int i = 0;
 #pragma unroll 1
       for (int step = 256; step; step >>= 1)
@@ -355,8 +347,26 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
       at.chunk = (int)quotient(left, n);
       const int in = (int)(left - (int64_t)at.chunk * n);  // on the segment
       at.tile = at.span.first + max(in - kBegin, 0);
-      place += max(kBegin - in, 0);
+      place = max(kBegin - in, 0);
     }
+  }
+
+  // Sequences that see nothing.
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const Span s = span_of<TILE>(p, b);
+    if (s.first != s.end) continue;
+    for (int i = threadIdx.x; i < p.Hq * (D / 8); i += THREADS)
+      *reinterpret_cast<uint4*>(p.out + b * p.out_stride + i * 8) = make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (int i = threadIdx.x; i < p.Hq; i += THREADS) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
+  }
+
+  const int groups = p.chunks / p.Hkv;  // chunks of a KV head
+  uint8_t* ring = shared + warp * Y::kRing;
+  float* kept = p.kept + (int64_t)(blockIdx.x * W + warp) * ROWS * D;
+  if (lane == 0) seg_a[warp] = seg_b[warp] = -1, done_a[warp] = away_a[warp] = 0, end_b[warp] = 0;
+
+  if (place < share) {
     const bool runs = p.cache.page_size % kRun == 0;
 
     // Places in a cache are counted in 64 bytes, which 32 bits hold.
@@ -373,7 +383,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
     Lookup<TILE> next;
     next.update(p, ahead, runs, true, lane);
     bool next_whole = true;   // every token of the tile staged last is seen ...
-    bool whole[Y::kStages];   // ... and of the tiles not taken yet
+    bool whole[kStages];   // ... and of the tiles not taken yet
     // Starts the copies of the tile looked up last, and looks the one after it up.
     auto issue = [&](int stage) {
       if (ahead_place < share) {
@@ -464,7 +474,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
       copies_commit();
     };
 #pragma unroll
-    for (int i = 0; i < Y::kStages - 1; ++i) {
+    for (int i = 0; i < kStages - 1; ++i) {
       issue(i);
       whole[i] = next_whole;
     }
@@ -528,22 +538,27 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
       }
     };
 
-    bool fresh = true;
+    // The first pass takes what the first stage happens to hold, while the copies
+    // into it are on their way, and its result is dropped: it is there to fetch the
+    // code, which takes longer than a tile does (one sequence of 200 tokens: 7.4 us,
+    // without it 9.6). Of long shares it is no gain (batches lose 1 us).
+    bool fresh = true, dry = share <= kDry;
     int stage = 0;
 #pragma unroll 1
     while (place < share) {  // (a share may hold a segment's beginning alone)
-      copies_wait<Y::kStages - 2>();
-      __syncwarp();
       const bool all = whole[0];
-      issue(stage ? stage - 1 : Y::kStages - 1);  // into the stage that the last tile has left
+      if (!dry) {
+        copies_wait<kStages - 2>();
+        __syncwarp();
+        issue(stage ? stage - 1 : kStages - 1);  // into the stage that the last tile has left
 #pragma unroll
-      for (int i = 0; i < Y::kStages - 2; ++i) whole[i] = whole[i + 1];
-      whole[Y::kStages - 2] = next_whole;
+        for (int i = 0; i < kStages - 2; ++i) whole[i] = whole[i + 1];
+        whole[kStages - 2] = next_whole;
+      }
       if (fresh) load_q();
       fresh = false;
       const uint8_t* ks = ring + stage * S::kStage;
       const uint8_t* vs = ks + S::kBytes;
-      stage = stage + 1 == Y::kStages ? 0 : stage + 1;
 
       // ---- scores: token 16 t + g (and + 8), heads 8 n + 2 c (and + 1)
       float s[TB][NH][4];
@@ -693,6 +708,12 @@ __global__ void __launch_bounds__(Layout<D, FP8, NH>::kWarps * 32, 1) decode_att
         }
       }
 
+      if (dry) {
+        dry = false;
+        fresh = true;
+        continue;
+      }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
       // ---- the end of a segment, or of the share
       const bool ends = at.tile + 1 == at.span.end;
       const bool last = place + (ends ? 1 + kBegin : 1) >= share;
@@ -843,27 +864,45 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const AttentionParams 
   if (row >= min(p.G - sub * ROWS, ROWS)) return;
   constexpr int64_t kPart = ROWS * (D + 2);
   auto part = [&](int i) { return p.parts + ((int64_t)i * 2 + (i == from)) * kPart; };
-  float most = -INFINITY;
-  for (int i = from + lane; i <= split.last; i += 32) most = fmaxf(most, part(i)[ROWS * D + row]);
+  // 32 parts at a time, their maxima and sums one a lane; kAhead of them in flight.
+  constexpr int N = D / 32, kAhead = 8;
+  float most = -INFINITY, sum = 0.f, f[N] = {};
+  for (int i0 = from; i0 <= split.last; i0 += 32) {
+    const int n = min(split.last + 1 - i0, 32);
+    const float* mine = part(i0 + min(lane, n - 1));
+    const float m = lane < n ? mine[ROWS * D + row] : -INFINITY, l = lane < n ? mine[ROWS * (D + 1) + row] : 0.f;
+    float top = fmaxf(m, most);
 #pragma unroll
-  for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, d));
-  const float minus = most == -INFINITY ? 0.f : most;
-  constexpr int N = D / 32;
-  float sum = 0.f, f[N] = {};
-#pragma unroll 4
-  for (int i = from; i <= split.last; ++i) {
-    const float* q = part(i);
-    const float scale = exp2_of(q[ROWS * D + row] - minus);
-    sum = fmaf(q[ROWS * (D + 1) + row], scale, sum);
-    if constexpr (N == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(q + row * D + lane * 4);
-      f[0] = fmaf(v.x, scale, f[0]), f[1] = fmaf(v.y, scale, f[1]);
-      f[2] = fmaf(v.z, scale, f[2]), f[3] = fmaf(v.w, scale, f[3]);
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(q + row * D + lane * 2);
-      f[0] = fmaf(v.x, scale, f[0]), f[1] = fmaf(v.y, scale, f[1]);
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+    const float minus = top == -INFINITY ? 0.f : top, before = exp2_of(most - minus), weight = exp2_of(m - minus);
+    most = top;
+    sum = fmaf(sum, before, l * weight);  // (each lane's own parts)
+#pragma unroll
+    for (int k = 0; k < N; ++k) f[k] *= before;
+    for (int j = 0; j < n; j += kAhead) {
+      float v[kAhead][N];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float* q = part(i0 + min(j + u, n - 1)) + row * D + lane * N;
+        if constexpr (N == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(q);
+          v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(q);
+          v[u][0] = x.x, v[u][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float w = __shfl_sync(kFull, weight, min(j + u, 31));
+        if (j + u < n)
+#pragma unroll
+          for (int k = 0; k < N; ++k) f[k] = fmaf(v[u][k], w, f[k]);
+      }
     }
   }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int q = head * p.G + sub * ROWS + row;
   uint32_t* out = reinterpret_cast<uint32_t*>(p.out + b * p.out_stride + (int64_t)q * D + lane * N);
@@ -872,22 +911,25 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const AttentionParams 
   if (p.lse && lane == 0) p.lse[(int64_t)b * p.Hq + q] = sum == 0.f ? -INFINITY : log_sum(most, sum);
 }
 
-int tile_tokens(int head_dim, bool fp8) { return head_dim == 128 && !fp8 ? 16 : 32; }
+int tile_tokens(int head_dim, bool fp8) { return 4096 / (head_dim * (fp8 ? 1 : 2)); }
+int smallest_tile(int head_dim) { return tile_tokens(head_dim, false); }
 
 int chunk_rows(int group) { return group > 8 ? 16 : 8; }
 
 int64_t parts_of(int head_dim, int rows) { return kMaxBlocks * (int64_t)2 * rows * (head_dim + 2); }
 int64_t workspace_of(int head_dim, int rows) {
   return kMaxBlocks * (int64_t)sizeof(Split) +
-         (parts_of(head_dim, rows) + kMaxBlocks * (int64_t)kMaxWarps * rows * head_dim) * (int64_t)sizeof(float);
+         (parts_of(head_dim, rows) + kMaxBlocks * (int64_t)kWarps * rows * head_dim) * (int64_t)sizeof(float);
 }
 
-// The most tiles there can be: those of full tables.
-int64_t most_tiles(int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t tokens, int tile) {
-  const int64_t rows = chunk_rows((int)(q_heads / kv_heads));
-  const int64_t chunks = kv_heads * ((q_heads / kv_heads + rows - 1) / rows);
-  const int64_t tiles = (tokens + tile - 1) / tile;
-  return tiles == 0 ? 0 : seqs * chunks > INT64_MAX / tiles ? INT64_MAX : seqs * chunks * tiles;
+int64_t segments(int64_t seqs, int64_t q_heads, int64_t kv_heads) {
+  const int64_t group = q_heads / kv_heads, rows = chunk_rows((int)group);
+  return seqs * kv_heads * ((group + rows - 1) / rows);
+}
+
+// Whether a block for each segment does even where all tables are full.
+bool is_solo(int64_t segments, int64_t tokens, int tile) {
+  return segments <= kSoloBlocks && tokens <= (int64_t)kSolo * kWarps * tile;
 }
 
 template <int D, bool FP8, int NH>
@@ -896,10 +938,10 @@ cudaError_t launch_attention(const AttentionParams& p, int64_t tiles, int device
   static std::atomic<uint64_t> done{0};
   cudaError_t e = afd::allow_shared(decode_attention_kernel<D, FP8, NH>, Y::kShared, device, done);
   if (e != cudaSuccess) return e;
-  const int64_t want = tiles / Y::kWarps + (tiles % Y::kWarps != 0), most = sms < kMaxBlocks ? sms : kMaxBlocks;
-  const int blocks = (int)(want < 1 ? 1 : want < most ? want : most);
-  e = afd::launch_dependent(decode_attention_kernel<D, FP8, NH>, blocks, Y::kWarps * 32, Y::kShared, stream, p);
-  if (e != cudaSuccess || blocks == 1) return e;
+  const int64_t most = sms < kMaxBlocks ? sms : kMaxBlocks, want = p.solo ? p.B * p.chunks : tiles;
+  const int blocks = (int)(tiles == 0 || (want > most && !p.solo) ? most : want);
+  e = afd::launch_dependent(decode_attention_kernel<D, FP8, NH>, blocks, kWarps * 32, Y::kShared, stream, p);
+  if (e != cudaSuccess || p.solo) return e;
   return afd::launch_dependent(decode_join_kernel<D, NH>, blocks * NH, 256, 0, stream, p);
 }
 
@@ -923,9 +965,9 @@ AFD_API int64_t afd_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads
   if (num_seqs < 0 || num_kv_heads < 1 || num_q_heads < 1 || num_q_heads % num_kv_heads || max_pages < 0 || page_size < 1 ||
       (head_dim != 64 && head_dim != 128))
     return -1;
-  // (of the two types' tiles the smaller, so the larger number of them)
-  const int64_t tiles = most_tiles(num_seqs, num_q_heads, num_kv_heads, (int64_t)max_pages * page_size, 16);
-  return tiles <= 1 ? 0 : workspace_of(head_dim, chunk_rows(num_q_heads / num_kv_heads));
+  const int64_t tokens = (int64_t)max_pages * page_size;
+  if (tokens == 0 || is_solo(segments(num_seqs, num_q_heads, num_kv_heads), tokens, smallest_tile(head_dim))) return 0;
+  return workspace_of(head_dim, chunk_rows(num_q_heads / num_kv_heads));
 }
 
 AFD_API afd_status afd_decode_attention(const void* q, int64_t q_stride, const afd_cache* cache,
@@ -969,7 +1011,9 @@ AFD_API afd_status afd_decode_attention(const void* q, int64_t q_stride, const a
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return AFD_ERR_CUDA;
   const bool fp8 = cache->dtype == AFD_FP8_E4M3;
-  const int64_t tiles = most_tiles(num_seqs, num_q_heads, Hkv, tokens, tile_tokens(D, fp8));
+  // (of the two types' tiles the smaller decides, as for the workspace)
+  p.solo = need == 0;
+  const int64_t tiles = (tokens + tile_tokens(D, fp8) - 1) / tile_tokens(D, fp8) * num_seqs * p.chunks;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = D == 64 ? launch_of<64>(p, fp8, tiles, dev, sms, s) : launch_of<128>(p, fp8, tiles, dev, sms, s);
   return e == cudaSuccess ? AFD_OK : AFD_ERR_CUDA;

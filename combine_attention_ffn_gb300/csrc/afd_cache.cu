@@ -5,11 +5,12 @@
 //   or 2i and 2i + 1): (a cos - b sin, b cos + a sin) * factor
 //
 // Angles are products and remainders in FP64 (a position of a million leaves
-// FP32 two digits of the angle), once for each token and pair of a block; sine
-// and cosine of the remainder, at most pi, and the rotation are FP32. A block
-// takes some of a token's heads, a thread eight columns of one at a time. What
-// bounds many tokens is the traffic: queries read and written, keys and values
-// read and written once.
+// FP32 two digits of the angle), once for each token and pair; sine and cosine of
+// the remainder, at most pi, and the rotation are FP32. A block takes some tokens,
+// or some of a token's heads where there are few; a thread has eight columns of
+// every so many heads, so it holds its sines and cosines in registers through a
+// token. What bounds many tokens is the traffic: queries read and written, keys and
+// values read and written once; a decode step is a chain of latencies.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -35,13 +36,19 @@ struct WriteParams {
   const float* inv_freq;
   int32_t pairs, interleaved;
   float factor;
-  int32_t T, Hq, Hkv, splits;
+  int32_t T, Hq, Hkv;
+  int32_t blocks;        // that share the tokens
+  int32_t splits, each;  // blocks that share a token's heads, and the heads of each
   afd::CacheParams cache;
   uint16_t* q_out;
   int64_t q_out_stride;
 };
 
-constexpr int kWriteThreads = 256;
+constexpr int kWriteThreads = 256;  // of a block at most
+constexpr int kWriteBlocks = 4;     // of an SM, of many tokens
+constexpr int kAhead = 4;           // groups of eight columns of a thread in flight
+constexpr int kMaxTokens = 8;       // whose sines and cosines a block finds in one go
+constexpr uint32_t kNowhere = 0xffffffffu;
 constexpr int kMaxPairs = 64;
 
 // Sine and cosine of position * freq.
@@ -55,81 +62,149 @@ __device__ __forceinline__ float2 rotation(int64_t position, float freq, float f
   return make_float2(c * factor, s * factor);
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const WriteParams p) {
-  __shared__ float2 turn[kMaxPairs];
+// How a head's columns turn: not at all, (2i, 2i + 1) with a multiple of four
+// pairs, (i, pairs + i) with one of eight, or either with another number of them.
+enum { kStill, kInterleaved, kHalves, kUneven };
+
+// Eight columns of a head turned. `raw` are the columns as they lie there, `from`
+// the head's address, `partner` the lane that has their partners (kHalves).
+template <int MODE>
+__device__ __forceinline__ void turn_columns(const uint4& raw, const uint16_t* from, int c, int pairs, bool interleaved,
+                                             int partner, const float (&cosine)[8], const float (&sine)[8], float (&f)[8]) {
+  afd::bf16x8_to_float(raw, f);
+  if (MODE == kStill) return;
+  float other[8] = {};
+  if (MODE == kInterleaved) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) other[e] = f[e ^ 1];
+  } else if (MODE == kHalves) {
+    afd::bf16x8_to_float(make_uint4(__shfl_sync(0xffffffffu, raw.x, partner), __shfl_sync(0xffffffffu, raw.y, partner),
+                                    __shfl_sync(0xffffffffu, raw.z, partner), __shfl_sync(0xffffffffu, raw.w, partner)), other);
+  } else if (from) {
+#pragma unroll 1
+    for (int e = 0; e < 8 && c + e < 2 * pairs; ++e) {
+      const int col = c + e;
+      other[e] = __uint_as_float((uint32_t)from[interleaved ? col ^ 1 : col < pairs ? col + pairs : col - pairs] << 16);
+    }
+  }
+  if (c >= 2 * pairs) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float y = f[e] * cosine[e] + other[e] * sine[e];
+    f[e] = MODE == kUneven && c + e >= 2 * pairs ? f[e] : y;
+  }
+}
+
+template <int D, bool FP8, int MODE>
+__global__ void __launch_bounds__(kWriteThreads, kWriteBlocks) cache_write_kernel(const WriteParams p) {
+  __shared__ float2 turn[kMaxTokens][kMaxPairs];
+  __shared__ uint32_t page_of[kMaxTokens], place_of[kMaxTokens];  // kNowhere: not kept
   constexpr int L = D / 8;  // lanes of a head
   afd::pdl_wait();
   afd::pdl_launch_dependents();
-  const int t = blockIdx.x / p.splits, part = blockIdx.x % p.splits;
-  const int heads = p.Hq + 2 * p.Hkv;
-  const int vecs = heads * L;
-  // a whole number of warps' worth of a token's groups each
-  const int each = ((vecs + p.splits - 1) / p.splits + 31) & ~31;
-  const int lo = part * each, hi = min(vecs, lo + each);
-  if (lo >= hi) return;
-  const int64_t slot = p.slots[t];
-  const bool kept = slot >= 0 && slot < (int64_t)p.cache.pages * p.cache.page_size;
-  const int64_t page = kept ? (uint32_t)slot / (uint32_t)p.cache.page_size : 0;
-  const int in_page = kept ? (int)((uint32_t)slot % (uint32_t)p.cache.page_size) : 0;
-  if ((int)threadIdx.x < p.pairs) turn[threadIdx.x] = rotation(p.positions[t], p.inv_freq[threadIdx.x], p.factor);
-  __syncthreads();
-  for (int i0 = lo; i0 < hi; i0 += kWriteThreads) {
-    const int i = i0 + threadIdx.x;
-    const bool in = i < hi;
-    const int head = in ? i / L : 0, c = i % L * 8;
-    const uint16_t* from = head < p.Hq ? p.q + t * p.q_stride + head * D
-                           : head < p.Hq + p.Hkv ? p.k + t * p.k_stride + (head - p.Hq) * D
-                                                 : p.v + t * p.v_stride + (head - p.Hq - p.Hkv) * D;
-    const bool turned = head < p.Hq + p.Hkv && c < 2 * p.pairs;
-    float f[8] = {};
-    if (in) {
-      afd::bf16x8_to_float(afd::ld_before_write(reinterpret_cast<const uint4*>(from + c)), f);  // (q_out may be q)
-      if (turned) {
-        if (p.interleaved) {
+  const int block = blockIdx.x / p.splits, part = blockIdx.x - block * p.splits;
+  const int t0 = (int)((int64_t)p.T * block / p.blocks), t1 = (int)((int64_t)p.T * (block + 1) / p.blocks);
+  // The block's heads, counted through queries, keys and values.
+  const int h0 = part * p.each, h1 = min(p.Hq + 2 * p.Hkv, h0 + p.each);
+  const int q1 = min(h1, p.Hq), kv0 = max(h0, p.Hq);
+  const int c = threadIdx.x % L * 8, mine = threadIdx.x / L;
+  const int step = blockDim.x / L;  // heads that the block takes at a time
+  const int partner = (threadIdx.x & 31) + (c < p.pairs ? p.pairs : -p.pairs) / 8;
+#pragma unroll 1
+  for (int t = t0; t < t1; ++t) {
+    const int at = (t - t0) % kMaxTokens;
+    // The first rows are on their way while the block finds its sines and cosines.
+    const uint16_t* q = p.q + t * p.q_stride + (h0 + mine) * D + c;
+    uint4 raw[kAhead], kv = make_uint4(0, 0, 0, 0);
+    auto fetch = [&](int r0) {
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int pair = (c + e) / 2;
-            if (pair < p.pairs) {
-              const float2 w = turn[pair];
-              const float a = f[e], b = f[e + 1];
-              f[e] = a * w.x - b * w.y;
-              f[e + 1] = b * w.x + a * w.y;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int col = c + e;
-            if (col < 2 * p.pairs) {
-              const bool first = col < p.pairs;
-              const float2 w = turn[first ? col : col - p.pairs];
-              const float other = __uint_as_float((uint32_t)from[first ? col + p.pairs : col - p.pairs] << 16);
-              f[e] = f[e] * w.x + (first ? -other : other) * w.y;
-            }
-          }
+      for (int u = 0; u < kAhead; ++u)
+        raw[u] = r0 + u * step + mine < q1 ? afd::ld_before_write(reinterpret_cast<const uint4*>(q + u * step * D))
+                                           : make_uint4(0, 0, 0, 0);  // (q_out may be q)
+    };
+    auto kv_source = [&](int head) {
+      return head < p.Hq + p.Hkv ? p.k + t * p.k_stride + (head - p.Hq) * D : p.v + t * p.v_stride + (head - p.Hq - p.Hkv) * D;
+    };
+    fetch(h0);
+    if (kv0 + mine < h1) kv = afd::ld_once(reinterpret_cast<const uint4*>(kv_source(kv0 + mine) + c));
+    if (at == 0) {
+      const int tokens = min(t1 - t, kMaxTokens);
+      __syncthreads();  // (the last tokens' have been read)
+      for (int i = threadIdx.x; i < tokens; i += blockDim.x) {
+        const int64_t slot = p.slots[t + i];
+        const bool kept = slot >= 0 && slot < (int64_t)p.cache.pages * p.cache.page_size;
+        const uint32_t page = kept ? (uint32_t)slot / (uint32_t)p.cache.page_size : kNowhere;
+        page_of[i] = page;
+        place_of[i] = kept ? (uint32_t)slot - page * (uint32_t)p.cache.page_size : 0;
+      }
+      if (MODE != kStill)
+        for (int i = threadIdx.x; i < tokens * p.pairs; i += blockDim.x) {
+          const int tok = i / p.pairs, pair = i - tok * p.pairs;
+          turn[tok][pair] = rotation(p.positions[t + tok], p.inv_freq[pair], p.factor);
         }
+      __syncthreads();
+    }
+    float cosine[8], sine[8];  // of this thread's columns, sines with their signs
+    if (MODE != kStill) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int col = c + e;
+        const bool paired = MODE == kInterleaved || (MODE == kUneven && p.interleaved);
+        const bool second = paired ? e & 1 : col >= p.pairs;
+        const int pair = paired ? col / 2 : second ? col - p.pairs : col;
+        const float2 w = turn[at][min(pair, p.pairs - 1)];
+        cosine[e] = w.x, sine[e] = second ? w.y : -w.y;
       }
     }
-    __syncwarp();  // the warp has read the heads that it now writes
-    const bool key = head >= p.Hq && head < p.Hq + p.Hkv;
-    const int h = key ? head - p.Hq : head - p.Hq - p.Hkv;
-    float scale = 1.f;
-    if (FP8) scale = afd::block_scale(afd::lanes_absmax<L>(afd::absmax8(f)));
-    if (!in) continue;
-    if (head < p.Hq) {
-      *reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + head * D + c) = afd::float_to_bf16x8(f);
-    } else if (kept) {
-      const int64_t row = (int64_t)h * p.cache.page_size + in_page;
-      uint8_t* to = key ? p.cache.k + page * p.cache.k_page_units * 64 : p.cache.v + page * p.cache.v_page_units * 64;
+    uint16_t* out = p.q_out + t * p.q_out_stride + (h0 + mine) * D + c;
+#pragma unroll 1
+    for (int r0 = h0; r0 < q1;) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (r0 + u * step >= q1) break;  // (the whole block)
+        float f[8];
+        const bool in = r0 + u * step + mine < q1;
+        turn_columns<MODE>(raw[u], in ? q - c + u * step * D : nullptr, c, p.pairs, p.interleaved, partner, cosine, sine, f);
+        if (MODE == kUneven) __syncwarp();  // the warp has read the heads that it now writes
+        if (in) *reinterpret_cast<uint4*>(out + u * step * D) = afd::float_to_bf16x8(f);
+      }
+      r0 += kAhead * step;
+      if (r0 >= q1) break;
+      q += kAhead * step * D, out += kAhead * step * D;
+      fetch(r0);
+    }
+#pragma unroll 1
+    for (int r0 = kv0; r0 < h1; r0 += step) {
+      const int head = r0 + mine;
+      const bool in = head < h1, key = head < p.Hq + p.Hkv;
+      if (r0 > kv0) kv = in ? afd::ld_once(reinterpret_cast<const uint4*>(kv_source(head) + c)) : make_uint4(0, 0, 0, 0);
+      float f[8], still[8];
+      turn_columns<MODE>(kv, in && key ? kv_source(head) : nullptr, c, p.pairs, p.interleaved, partner, cosine, sine, f);
+      afd::bf16x8_to_float(kv, still);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = key ? f[e] : still[e];
+      float scale = 1.f;
+      if (FP8) scale = afd::block_scale(afd::lanes_absmax<L>(afd::absmax8(f)));
+      const uint32_t page = page_of[at];
+      if (!in || page == kNowhere) continue;
+      const int64_t row = (int64_t)(head - p.Hq - (key ? 0 : p.Hkv)) * p.cache.page_size + place_of[at];
+      uint8_t* to = key ? p.cache.k + (uint64_t)page * p.cache.k_page_units * 64 : p.cache.v + (uint64_t)page * p.cache.v_page_units * 64;
       if (FP8) {
         *reinterpret_cast<uint2*>(to + row * D + c) = afd::to_e4m3x8(f, 1.f / scale);
-        if (c == 0) (key ? p.cache.k_scale : p.cache.v_scale)[page * p.Hkv * p.cache.page_size + row] = scale;
+        if (c == 0) (key ? p.cache.k_scale : p.cache.v_scale)[(int64_t)page * p.Hkv * p.cache.page_size + row] = scale;
       } else {
         *reinterpret_cast<uint4*>(to + (row * D + c) * 2) = afd::float_to_bf16x8(f);
       }
     }
   }
+}
+
+template <int D, bool FP8>
+cudaError_t launch_write(const WriteParams& p, int64_t grid, int threads, cudaStream_t s) {
+  auto kernel = p.pairs == 0 ? cache_write_kernel<D, FP8, kStill>
+                : p.pairs % (p.interleaved ? 4 : 8) ? cache_write_kernel<D, FP8, kUneven>
+                : p.interleaved ? cache_write_kernel<D, FP8, kInterleaved> : cache_write_kernel<D, FP8, kHalves>;
+  return afd::launch_dependent(kernel, grid, threads, 0, s, p);
 }
 
 }  // namespace
@@ -168,16 +243,19 @@ extern "C" AFD_API afd_status afd_cache_write(const void* q, int64_t q_stride, c
   int dev = -1, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return AFD_ERR_CUDA;
-  // Few tokens: several blocks share a token, so that no thread takes its
-  // groups of columns in turn while SMs are idle.
-  const int rounds = ((Hq + 2 * Hkv) * (D / 8) + kWriteThreads - 1) / kWriteThreads;
-  const int64_t spread = (2 * (int64_t)sms + p.T - 1) / p.T;
-  p.splits = (int32_t)(spread < rounds ? spread : rounds);
-  const int64_t grid = (int64_t)p.T * p.splits;
-  if (grid > INT32_MAX) return AFD_ERR_UNSUPPORTED;
+  // Many tokens: as many blocks as there is room for, with the same number each.
+  // Few: several blocks share a token, so that no head waits for another while SMs
+  // are idle.
+  const int heads = Hq + 2 * Hkv, L = D / 8;
+  p.blocks = (int32_t)(p.T < kWriteBlocks * (int64_t)sms ? p.T : kWriteBlocks * (int64_t)sms);
+  const int spread = (2 * sms + p.blocks - 1) / p.blocks, most = (heads * L + 127) / 128;
+  p.splits = spread < most ? spread : most;
+  p.each = (heads + p.splits - 1) / p.splits;
+  const int need = (p.each * L + 31) & ~31, threads = need < kWriteThreads ? need : kWriteThreads;
+  const int64_t grid = (int64_t)p.blocks * p.splits;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool fp8 = cache->dtype == AFD_FP8_E4M3;
-  auto kernel = D == 64 ? (fp8 ? cache_write_kernel<64, true> : cache_write_kernel<64, false>)
-                        : (fp8 ? cache_write_kernel<128, true> : cache_write_kernel<128, false>);
-  return afd::launch_dependent(kernel, grid, kWriteThreads, 0, s, p) == cudaSuccess ? AFD_OK : AFD_ERR_CUDA;
+  const cudaError_t e = D == 64 ? (fp8 ? launch_write<64, true>(p, grid, threads, s) : launch_write<64, false>(p, grid, threads, s))
+                                : (fp8 ? launch_write<128, true>(p, grid, threads, s) : launch_write<128, false>(p, grid, threads, s));
+  return e == cudaSuccess ? AFD_OK : AFD_ERR_CUDA;
 }
