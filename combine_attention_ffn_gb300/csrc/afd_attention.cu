@@ -7,7 +7,7 @@
 // Tiles and their order: the tokens of a sequence that are seen, 16, 32 or 64 at
 // a time (4 KB of keys and as much of values), once for each KV head and each 8
 // or 16 of its query heads; sequences, heads and tiles in that order make one
-// line. A (sequence, heads) segment counts kBegin on it beside its tiles, for its
+// line. A (sequence, heads) segment counts a tile or two more on it, for its
 // queries and its result. The line is cut into equal shares, one a warp, so that
 // no length leaves a warp idle; a share may begin or end inside a segment. Those
 // parts are joined by the block after its warps are done, and what the blocks
@@ -36,13 +36,14 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxBlocks = 160;
-constexpr int kWarps = 8;         // of a block
-constexpr int kStages = 2;        // tiles of a warp's ring
+// Warps of a block, each with two stages of 8 KB. Three or four stages are slower:
+// 128 sequences (BF16) 218 us with three, 209 with two; twelve warps take 212, six
+// with three stages 217, seven with two 209.5, nine 205.5, ten 206.6 against 205.6
+// for eight; 64 sequences (E4M3, 16 heads a KV head) 75, 93 and 86 against 70.8.
+constexpr int kWarps = 8;
 constexpr int kSoloBlocks = 148;  // no more than SMs
 constexpr float kLazy = 8.f;  // log2 of how far a score may pass the running maximum before that moves
-constexpr int kBegin = 2;   // what a segment costs beside its tiles, in tiles
 constexpr int kSolo = 4;    // tiles a warp up to which a block takes a whole segment
-constexpr int kDry = 8;     // places up to which a share begins with a dry pass
 constexpr int kRun = 16;    // tokens that are in one page where its size is a multiple
 constexpr float kLn2 = 0.693147180559945f;
 
@@ -91,6 +92,10 @@ struct Shape {
   static constexpr int kStage = kBias + 4 * kTile;
   static constexpr int E = FP8 && D == 128 ? 16 : 8;         // neighbouring columns of a lane
   static constexpr int H = D / 8 / E;                        // ... and how many such groups
+  // What a segment counts beside its tiles, in tiles. With 0, 1/2, 1, 3/2 and 2:
+  // 64 unlike sequences (E4M3, 128 columns) 79.6, 77.5, 74.3, 73.4, 72.0 us; 250
+  // short ones (BF16, 64 columns) 43.7, 38.4, 36.6, 37.2, 37.5.
+  static constexpr int kBegin = FP8 && D == 128 ? 2 : 1;
 };
 
 // NH: query heads of a chunk, in eights.
@@ -98,9 +103,9 @@ template <int D, bool FP8, int NH>
 struct Layout {
   using S = Shape<D, FP8>;
   static constexpr int kRows = 8 * NH;
-  static constexpr int kRing = kStages * S::kStage;
+  static constexpr int kRing = 2 * S::kStage;  // one tile is taken while the next one comes
   static constexpr int kShared = kWarps * kRing;
-  static_assert(kStages >= 2 && kRing >= kRows * D * 4, "a part goes where the ring was");
+  static_assert(kRing >= kRows * D * 4, "a part goes where the ring was");
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -217,7 +222,7 @@ __device__ __forceinline__ Span span_of(const AttentionParams& p, int b) {
 }
 
 // A place in the line; next() returns how far it went.
-template <int TILE>
+template <int TILE, int BEGIN>
 struct Cursor {
   Span span;
   int b, chunk, tile;
@@ -226,12 +231,12 @@ struct Cursor {
     if (++chunk == p.chunks) {
       chunk = 0;
       do {
-        if (++b >= p.B) return 1 + kBegin;  // (the end of the line)
+        if (++b >= p.B) return 1 + BEGIN;  // (the end of the line)
         span = span_of<TILE>(p, b);
       } while (span.first == span.end);
     }
     tile = span.first;
-    return 1 + kBegin;
+    return 1 + BEGIN;
   }
 };
 
@@ -242,13 +247,15 @@ struct Lookup {
   static constexpr int N = TILE > 32 ? TILE / 32 : 1;
   int page[N], at[N];  // -1: not seen
   int first;
-  __device__ __forceinline__ void find(const AttentionParams& p, const Cursor<TILE>& c, int i, int token) {
+  template <typename C>
+  __device__ __forceinline__ void find(const AttentionParams& p, const C& c, int i, int token) {
     const uint32_t n = p.page_shift >= 0 ? (uint32_t)token >> p.page_shift : (uint32_t)token / (uint32_t)p.cache.page_size;
     at[i] = token - (int)(n * (uint32_t)p.cache.page_size);
     page[i] = p.table[c.b * p.table_stride + n];
   }
   // `fresh`: another sequence, or the sequence's first tile again.
-  __device__ __forceinline__ void update(const AttentionParams& p, const Cursor<TILE>& c, bool runs, bool fresh, int lane) {
+  template <typename C>
+  __device__ __forceinline__ void update(const AttentionParams& p, const C& c, bool runs, bool fresh, int lane) {
     if (runs) {
       const int run = c.tile * (TILE / kRun);
       if (!fresh && run + TILE / kRun <= first + 32) return;
@@ -272,7 +279,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
   using S = Shape<D, FP8>;
   using Y = Layout<D, FP8, NH>;
   constexpr int TILE = S::kTile, ROW = S::kRow, E = S::E, H = S::H, TB = TILE / 16, W = kWarps, ROWS = Y::kRows;
-  constexpr int THREADS = W * 32;
+  constexpr int THREADS = W * 32, kBegin = S::kBegin;
   extern __shared__ __align__(128) uint8_t shared[];
   __shared__ int64_t before[THREADS + 1];          // the line before each thread's sequences, of one chunk
   __shared__ float part_m[W][2][ROWS], part_l[W][2][ROWS];
@@ -311,7 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
     if (threadIdx.x == 0) before[0] = 0;
     __syncthreads();
   }
-  Cursor<TILE> at;
+  Cursor<TILE, kBegin> at;
   int64_t lo = 0, each_share = 1;  // this warp's first place on the line, and those of a warp
   int share = 0, place = 0;        // places it has; where its next tile is behind the first
   if (solo) {
@@ -378,12 +385,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
     auto step_of = [&](int j) {
       return j * 512 + (own ^ (ROW == 256 ? (j & 3) * 32 : ROW == 128 ? (j & 1) * 64 : 0));
     };
-    Cursor<TILE> ahead = at;
+    Cursor<TILE, kBegin> ahead = at;
     int ahead_place = place;
     Lookup<TILE> next;
     next.update(p, ahead, runs, true, lane);
-    bool next_whole = true;   // every token of the tile staged last is seen ...
-    bool whole[kStages];   // ... and of the tiles not taken yet
+    bool next_whole = true;  // every token of the tile staged last is seen
     // Starts the copies of the tile looked up last, and looks the one after it up.
     auto issue = [&](int stage) {
       if (ahead_place < share) {
@@ -473,11 +479,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
       }
       copies_commit();
     };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      issue(i);
-      whole[i] = next_whole;
-    }
+    issue(0);
 
     uint32_t qb[NH][D / 16][2];
     float row_scale[NH][2];
@@ -538,23 +540,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
       }
     };
 
-    // The first pass takes what the first stage happens to hold, while the copies
-    // into it are on their way, and its result is dropped: it is there to fetch the
-    // code, which takes longer than a tile does (one sequence of 200 tokens: 7.4 us,
-    // without it 9.6). Of long shares it is no gain (batches lose 1 us).
-    bool fresh = true, dry = share <= kDry;
+    bool fresh = true;
     int stage = 0;
 #pragma unroll 1
     while (place < share) {  // (a share may hold a segment's beginning alone)
-      const bool all = whole[0];
-      if (!dry) {
-        copies_wait<kStages - 2>();
-        __syncwarp();
-        issue(stage ? stage - 1 : kStages - 1);  // into the stage that the last tile has left
-#pragma unroll
-        for (int i = 0; i < kStages - 2; ++i) whole[i] = whole[i + 1];
-        whole[kStages - 2] = next_whole;
-      }
+      const bool all = next_whole;
+      copies_wait<0>();
+      __syncwarp();
+      issue(stage ^ 1);  // into the stage that the last tile has left
       if (fresh) load_q();
       fresh = false;
       const uint8_t* ks = ring + stage * S::kStage;
@@ -708,12 +701,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
         }
       }
 
-      if (dry) {
-        dry = false;
-        fresh = true;
-        continue;
-      }
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      stage ^= 1;
       // ---- the end of a segment, or of the share
       const bool ends = at.tile + 1 == at.span.end;
       const bool last = place + (ends ? 1 + kBegin : 1) >= share;
