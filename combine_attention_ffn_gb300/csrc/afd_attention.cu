@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
 
     // Places in a cache are counted in 64 bytes, which 32 bits hold.
     const uint8_t *k_lane = p.cache.k + lane * 16, *v_lane = p.cache.v + lane * 16;
-    const uint32_t page_scales = p.Hkv * p.cache.page_size;
+    const uint32_t page_scales = (uint32_t)p.Hkv * (uint32_t)p.cache.page_size;
     // A lane's place in the j-th 512 bytes of a stage's keys, or values: the rows of
     // a step begin at a multiple of their number, so their swizzle is a constant.
     const uint32_t own = swizzled<ROW>(lane / (ROW / 16), lane % (ROW / 16));
@@ -396,7 +396,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
         constexpr int CH = ROW / 16;  // chunks of a row
         uint8_t* to = ring + stage * S::kStage;
         const uint32_t dst = smem_addr(to);
-        const int base = ahead.tile * TILE, head = groups == 1 ? ahead.chunk : ahead.chunk / groups;
+        const int base = ahead.tile * TILE;
+        const uint32_t head_row = (uint32_t)(groups == 1 ? ahead.chunk : ahead.chunk / groups) * (uint32_t)p.cache.page_size;
         const int lowest = ahead.span.from - base, end = ahead.span.len - base;  // rows that are seen
         next_whole = lowest <= 0 && end >= TILE;
         if (runs) {
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
 #pragma unroll
           for (int r = 0; r < TILE / kRun; ++r) {
             const int page = __shfl_sync(kFull, next.page[0], r0 + r);
-            const uint32_t row = (uint32_t)(head * p.cache.page_size + __shfl_sync(kFull, next.at[0], r0 + r)) * (ROW / 64);
+            const uint32_t row = (head_row + __shfl_sync(kFull, next.at[0], r0 + r)) * (ROW / 64);
             ok[r] = (uint32_t)page < (uint32_t)p.cache.pages;
             const uint32_t pg = ok[r] ? (uint32_t)page : 0u;
             k[r] = k_lane + (uint64_t)(pg * p.cache.k_page_units + row) * 64;
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
             for (int i = 0; i < Lookup<TILE>::N; ++i) {
               const int tok = (32 * i + lane) & (TILE - 1);
               const int page = __shfl_sync(kFull, next.page[0], r0 + tok / kRun);
-              const uint32_t row = head * p.cache.page_size + __shfl_sync(kFull, next.at[0], r0 + tok / kRun) + tok % kRun;
+              const uint32_t row = head_row + __shfl_sync(kFull, next.at[0], r0 + tok / kRun) + tok % kRun;
               const bool in = next_whole || (tok >= lowest && tok < end && (uint32_t)page < (uint32_t)p.cache.pages);
               if (FP8) {
                 const uint32_t o = in ? (uint32_t)page * page_scales + row : 0;
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
             const bool in = (uint32_t)next.page[i] < (uint32_t)p.cache.pages;  // (-1: not seen)
             const uint32_t mask = __ballot_sync(kFull, in);
             next_whole &= mask == kFull;
-            const uint32_t row = (uint32_t)(head * p.cache.page_size + next.at[i]);
+            const uint32_t row = head_row + next.at[i];
             const uint32_t pg = in ? (uint32_t)next.page[i] : 0u;
             const uint32_t k_off = pg * p.cache.k_page_units + row * (ROW / 64), v_off = pg * p.cache.v_page_units + row * (ROW / 64);
 #pragma unroll 1
