@@ -858,18 +858,8 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const AttentionParams 
   float most = -INFINITY, sum = 0.f, f[N] = {};
   for (int i0 = from; i0 <= split.last; i0 += 32) {
     const int n = min(split.last + 1 - i0, 32);
-    const float* mine = part(i0 + min(lane, n - 1));
-    const float m = lane < n ? mine[ROWS * D + row] : -INFINITY, l = lane < n ? mine[ROWS * (D + 1) + row] : 0.f;
-    float top = fmaxf(m, most);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-    const float minus = top == -INFINITY ? 0.f : top, before = exp2_of(most - minus), weight = exp2_of(m - minus);
-    most = top;
-    sum = fmaf(sum, before, l * weight);  // (each lane's own parts)
-#pragma unroll
-    for (int k = 0; k < N; ++k) f[k] *= before;
-    for (int j = 0; j < n; j += kAhead) {
-      float v[kAhead][N];
+    float v[kAhead][N];
+    auto fetch = [&](int j) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const float* q = part(i0 + min(j + u, n - 1)) + row * D + lane * N;
@@ -881,6 +871,19 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const AttentionParams 
           v[u][0] = x.x, v[u][1] = x.y;
         }
       }
+    };
+    const float* mine = part(i0 + min(lane, n - 1));
+    const float m = lane < n ? mine[ROWS * D + row] : -INFINITY, l = lane < n ? mine[ROWS * (D + 1) + row] : 0.f;
+    fetch(0);
+    float top = fmaxf(m, most);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+    const float minus = top == -INFINITY ? 0.f : top, before = exp2_of(most - minus), weight = exp2_of(m - minus);
+    most = top;
+    sum = fmaf(sum, before, l * weight);  // (each lane's own parts)
+#pragma unroll
+    for (int k = 0; k < N; ++k) f[k] *= before;
+    for (int j = 0;;) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const float w = __shfl_sync(kFull, weight, min(j + u, 31));
@@ -888,6 +891,9 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const AttentionParams 
 #pragma unroll
           for (int k = 0; k < N; ++k) f[k] = fmaf(v[u][k], w, f[k]);
       }
+      j += kAhead;
+      if (j >= n) break;
+      fetch(j);
     }
   }
 #pragma unroll
