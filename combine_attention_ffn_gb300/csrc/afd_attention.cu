@@ -295,28 +295,36 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
   // ---- the line, and this warp's share of it
   const int each = (p.B + THREADS - 1) / THREADS;
   bool solo = p.solo;
+  // (Up to 32 sequences every warp has them in its lanes and waits for no other:
+  // 0.6 us less, and 0.2 more with more of them.)
+  const bool few = p.B <= 32;
+  int64_t mine = 0, sum = 0;
   if (!solo) {
-    int64_t mine = 0;
     int longest = 0;
-    const int b0 = threadIdx.x * each, b1 = min(p.B, b0 + each);
+    const int b0 = few ? lane : threadIdx.x * each, b1 = min(p.B, b0 + (few ? 1 : each));
     for (int b = b0; b < b1; ++b) {
       const Span s = span_of<TILE>(p, b);
       mine += s.end > s.first ? s.end - s.first + kBegin : 0;
       longest = max(longest, s.end - s.first);
     }
-    int64_t sum = mine;
+    sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t o = __shfl_up_sync(kFull, sum, d);
       if (lane >= d) sum += o;
     }
-    if (lane == 31) end_b[warp] = sum;
     // Short sequences, and a block for each: nothing is left for the second kernel.
-    solo = __syncthreads_and(longest <= kSolo * W && p.B * p.chunks <= gridDim.x);
-    for (int w = 0; w < warp; ++w) sum += end_b[w];
-    before[threadIdx.x + 1] = sum;
-    if (threadIdx.x == 0) before[0] = 0;
-    __syncthreads();
+    const bool short_all = longest <= kSolo * W && p.B * p.chunks <= gridDim.x;
+    if (few) {
+      solo = __all_sync(kFull, short_all);
+    } else {
+      if (lane == 31) end_b[warp] = sum;
+      solo = __syncthreads_and(short_all);
+      for (int w = 0; w < warp; ++w) sum += end_b[w];
+      before[threadIdx.x + 1] = sum;
+      if (threadIdx.x == 0) before[0] = 0;
+      __syncthreads();
+    }
   }
   Cursor<TILE, kBegin> at;
   int64_t lo = 0, each_share = 1;  // this warp's first place on the line, and those of a warp
@@ -331,17 +339,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
     share = min(per, n - first);
   } else {
     // Equal shares, but of few tiles the first blocks' warps take one each.
-    const int64_t total = before[THREADS] * p.chunks;
+    const int64_t total = (few ? __shfl_sync(kFull, sum, 31) : before[THREADS]) * p.chunks;
     each_share = max(quotient(total + gridDim.x * W - 1, gridDim.x * W), (int64_t)(1 + kBegin));
     lo = min(each_share * (blockIdx.x * W + warp), total);
     share = (int)min(each_share, total - lo);
     if (share > 0) {
-      int i = 0;
+      int64_t left;
+      if (few) {
+        const int i = __popc(__ballot_sync(kFull, sum * p.chunks <= lo));
+        left = lo - __shfl_sync(kFull, sum - mine, i) * p.chunks;
+        at.b = i;
+      } else {
+        int i = 0;
 #pragma unroll 1
-      for (int step = 256; step; step >>= 1)
-        if (i + step < THREADS && before[i + step] * p.chunks <= lo) i += step;
-      int64_t left = lo - before[i] * p.chunks;
-      at.b = i * each;
+        for (int step = 256; step; step >>= 1)
+          if (i + step < THREADS && before[i + step] * p.chunks <= lo) i += step;
+        left = lo - before[i] * p.chunks;
+        at.b = i * each;
+      }
       at.span = span_of<TILE>(p, at.b);
 #pragma unroll 1
       for (;;) {
@@ -356,16 +371,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
       at.tile = at.span.first + max(in - kBegin, 0);
       place = max(kBegin - in, 0);
     }
-  }
-
-  // Sequences that see nothing.
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const Span s = span_of<TILE>(p, b);
-    if (s.first != s.end) continue;
-    for (int i = threadIdx.x; i < p.Hq * (D / 8); i += THREADS)
-      *reinterpret_cast<uint4*>(p.out + b * p.out_stride + i * 8) = make_uint4(0, 0, 0, 0);
-    if (p.lse)
-      for (int i = threadIdx.x; i < p.Hq; i += THREADS) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
   }
 
   const int groups = p.chunks / p.Hkv;  // chunks of a KV head
@@ -769,6 +774,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
       place += at.next(p);
     }
     copies_wait<0>();
+  }
+  // Sequences that see nothing.
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const Span s = span_of<TILE>(p, b);
+    if (s.first != s.end) continue;
+    for (int i = threadIdx.x; i < p.Hq * (D / 8); i += THREADS)
+      *reinterpret_cast<uint4*>(p.out + b * p.out_stride + i * 8) = make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (int i = threadIdx.x; i < p.Hq; i += THREADS) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
   }
   __syncthreads();
 
