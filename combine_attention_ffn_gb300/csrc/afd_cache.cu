@@ -11,8 +11,8 @@
 // every so many heads, so it holds its sines and cosines in registers through a
 // token (looked up and chosen for every group of columns, 8,192 tokens took 83 us).
 // What bounds many tokens is the traffic, queries read and written, keys and values
-// read and written once, with half of the issue slots: 314 MB in 55.9 us, 5.6 TB/s.
-// A decode step is a chain of latencies: 2.4 us for a token, 4.2 for 128.
+// read and written once, with half of the issue slots: 314 MB in 57 us, 5.5 TB/s.
+// A decode step is a chain of latencies: 2.4 us for a token, 4.4 for 128.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -49,7 +49,8 @@ struct WriteParams {
 constexpr int kWriteThreads = 256;  // of a block at most
 // Blocks of an SM, of many tokens, and of all SMs two of few. 8,192 tokens (64 query
 // heads, 8 KV heads, E4M3): 55.9 us; four 55.3, five 56.8, six 57.9; 128 tokens,
-// where registers and not their number count: 4.2, 4.8, 6.0 and 6.3.
+// where registers and not their number count: 4.2, 4.8, 6.0 and 6.3 (all before the
+// values were divided by their scale, which takes 1 and 0.2 us more).
 constexpr int kWriteBlocks = 3;
 constexpr int kAhead = 4;           // groups of eight columns of a thread in flight
 constexpr int kMaxTokens = 8;       // whose sines and cosines a block finds in one go
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kWriteThreads, kWriteBlocks) cache_write_kerne
       const int64_t row = (int64_t)(head - p.Hq - (key ? 0 : p.Hkv)) * p.cache.page_size + place_of[at];
       uint8_t* to = key ? p.cache.k + (uint64_t)page * p.cache.k_page_units * 64 : p.cache.v + (uint64_t)page * p.cache.v_page_units * 64;
       if (FP8) {
-        *reinterpret_cast<uint2*>(to + row * D + c) = afd::to_e4m3x8(f, 1.f / scale);
+        *reinterpret_cast<uint2*>(to + row * D + c) = afd::divided_e4m3x8(f, scale);
         if (c == 0) (key ? p.cache.k_scale : p.cache.v_scale)[(int64_t)page * p.Hkv * p.cache.page_size + row] = scale;
       } else {
         *reinterpret_cast<uint4*>(to + (row * D + c) * 2) = afd::float_to_bf16x8(f);

@@ -3,9 +3,7 @@
 //
 // The floor keeps the scale and its reciprocal normal numbers, and the scale of
 // a vector of zeros small beside any other. A vector that holds an infinity or
-// a NaN gets that as its scale, so all of it decodes to NaN. v / scale is
-// taken as v * (1 / scale), at most 2^-23 off, which moves one value in a
-// million or so to the E4M3 neighbour on the other side of a tie.
+// a NaN gets that as its scale, so all of it decodes to NaN.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -32,8 +30,9 @@ __device__ __forceinline__ uint32_t lanes_absmax(uint32_t m) {
   return m;
 }
 
+// (A product with 1 / 448: at most a step of FP32 from the quotient.)
 __device__ __forceinline__ float block_scale(uint32_t absmax) {
-  const float s = __uint_as_float(absmax) / kE4m3Max;
+  const float s = __uint_as_float(absmax) * (1.f / kE4m3Max);
   return s < kSmallestScale ? kSmallestScale : s;  // (a NaN stays)
 }
 
@@ -44,9 +43,17 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
   return r;
 }
 
+// v / scale as v * (1 / scale), at most 2^-23 off. That moves a value in a hundred
+// thousand to its E4M3 neighbour, for values that are FP32 results; quotients of
+// BF16 values often lie on a tie (one in a few hundred), so those are divided.
 __device__ __forceinline__ uint2 to_e4m3x8(const float (&v)[8], float inv) {
   return make_uint2(pack_e4m3(v[0] * inv, v[1] * inv) | pack_e4m3(v[2] * inv, v[3] * inv) << 16,
                     pack_e4m3(v[4] * inv, v[5] * inv) | pack_e4m3(v[6] * inv, v[7] * inv) << 16);
+}
+
+__device__ __forceinline__ uint2 divided_e4m3x8(const float (&v)[8], float scale) {
+  return make_uint2(pack_e4m3(v[0] / scale, v[1] / scale) | pack_e4m3(v[2] / scale, v[3] / scale) << 16,
+                    pack_e4m3(v[4] / scale, v[5] / scale) | pack_e4m3(v[6] / scale, v[7] / scale) << 16);
 }
 
 }  // namespace afd

@@ -566,7 +566,7 @@ AFD_API int64_t afd_adapter_workspace_bytes(int64_t num_rows, int32_t num_tokens
  * They take at most 2^31 - 2^20 - 1 rows or tokens.
  * Where values go to E4M3, a vector of them shares one FP32 scale,
  *   scale = max(max |v| / 448, 2^-100), value = e4m3(v / scale),
- * rounded to nearest even; all of a vector with an infinity or a NaN decodes to
+ * the scale to a step of FP32, values rounded to nearest even; all of a vector with an infinity or a NaN decodes to
  * NaN. */
 
 /* The rows a source dispatches, from its residual stream:

@@ -551,3 +551,18 @@ def test_refusals_on_the_gpu():
         with pytest.raises(afd.AfdError) as e:
             call()
         assert e.value.status == afd.ERR_ARG, i
+
+
+def test_write_ties_go_where_the_division_puts_them():
+    """BF16 values whose quotients by the scale lie on ties of E4M3: bit for bit what
+    the division by the scale gives in FP32 (the scale: a product with FP32's 1 / 448)."""
+    s = _write_case(300, 1, 4, 128, 16, 0, True, 24)
+    s["slots"][:] = torch.arange(300, device="cuda")
+    s["v"].copy_(torch.randint(-14, 15, s["v"].shape, generator=_gen(25), device="cuda").float())
+    _write(s)
+    for name in ("k", "v"):
+        t = s[name].float()
+        scale = t.abs().amax(-1) * torch.tensor(1 / 448, device="cuda")
+        assert torch.equal(_flat(s[name + "_scale"])[:300], scale)
+        want = (t / scale[..., None]).to(FP8)
+        assert torch.equal(_flat(s[name + "_cache"])[:300].view(torch.uint8), want.view(torch.uint8))
