@@ -50,7 +50,12 @@ constexpr int kMaxBlocks = 160;
 constexpr int kWarps = 8;
 constexpr int kSoloBlocks = 148;  // no more than SMs
 constexpr float kLazy = 8.f;  // log2 of how far a score may pass the running maximum before that moves
-constexpr int kSolo = 4;    // tiles a warp up to which a block takes a whole segment
+// Tiles a warp up to which a block takes a whole segment: where the lengths say so,
+// and where full tables would (then in one launch). One sequence, 8 KV heads, us, a
+// block for each segment against shares: BF16, 128 columns, 500 tokens 8.7 / 10.0, 800
+// 10.7 / 10.1; E4M3, 1,000 10.1 / 11.9, 1,500 12.2 / 12.0; 64 columns, 1,000 8.4 / 9.4,
+// 1,500 10.1 / 9.5. By the lengths, beside a second launch: 300 8.5 / 9.9, 500 10.3 / 10.0.
+constexpr int kSolo = 4, kSoloFull = 6;
 constexpr int kRun = 16;    // tokens that are in one page where its size is a multiple
 constexpr float kLn2 = 0.693147180559945f;
 
@@ -945,7 +950,7 @@ int64_t segments(int64_t seqs, int64_t q_heads, int64_t kv_heads) {
 
 // Whether a block for each segment does even where all tables are full.
 bool is_solo(int64_t segments, int64_t tokens, int tile) {
-  return segments <= kSoloBlocks && tokens <= (int64_t)kSolo * kWarps * tile;
+  return segments <= kSoloBlocks && tokens <= (int64_t)kSoloFull * kWarps * tile;
 }
 
 template <int D, bool FP8, int NH>

@@ -120,8 +120,8 @@ def test_attention_workspace(lib):
     size = lib.afd_decode_workspace_bytes
     for B, Hq, Hkv, D, pages, page in ((1, 8, 8, 128, 8, 16), (64, 64, 4, 64, 1000, 64), (1, 40, 1, 128, 1 << 26, 1)):
         assert size(B, Hq, Hkv, D, 8 * pages, page) == size(B, Hq, Hkv, D, 16 * pages, page) > 0
-    assert size(1, 1, 1, 128, 1, 16) == size(1, 64, 4, 128, 32, 16) == size(148, 8, 1, 64, 4, 256) == 0
-    assert size(1, 64, 4, 128, 33, 16) > 0 and size(149, 8, 1, 64, 4, 256) > 0 and size(1, 256, 8, 64, 5, 256) > 0
+    assert size(1, 1, 1, 128, 1, 16) == size(1, 64, 4, 128, 48, 16) == size(148, 8, 1, 64, 6, 256) == 0
+    assert size(1, 64, 4, 128, 49, 16) > 0 and size(149, 8, 1, 64, 6, 256) > 0 and size(1, 256, 8, 64, 7, 256) > 0
     assert size(0, 8, 8, 128, 8, 16) == 0 and size(4, 8, 8, 128, 0, 16) == 0
     for bad in ((-1, 8, 8, 128, 8, 16), (1, 8, 3, 128, 8, 16), (1, 0, 1, 128, 8, 16), (1, 8, 0, 128, 8, 16), (1, 8, 8, 96, 8, 16),
                 (1, 8, 8, 128, -1, 16), (1, 8, 8, 128, 8, 0)):
