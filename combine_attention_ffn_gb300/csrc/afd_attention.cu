@@ -474,7 +474,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
             const uint32_t row = head_row + next.at[i];
             const uint32_t pg = in ? (uint32_t)next.page[i] : 0u;
             const uint32_t k_off = pg * p.cache.k_page_units + row * (ROW / 64), v_off = pg * p.cache.v_page_units + row * (ROW / 64);
-#pragma unroll 1
+            // (As a loop: 64 sequences of up to 4,096 tokens, pages of 1 80.7 us, of 24
+            // 70.2; unrolled 71.2 and 65.5, where pages of 16 take 63.1.)
+#pragma unroll
             for (int j = 0; j < (TILE < 32 ? TILE : 32) * CH / 32; ++j) {
               const int r = (j * 32 + lane) / CH, ch = (j * 32 + lane) % CH;
               const uint64_t ko = (uint64_t)__shfl_sync(kFull, k_off, r) * 64, vo = (uint64_t)__shfl_sync(kFull, v_off, r) * 64;
