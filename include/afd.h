@@ -657,6 +657,8 @@ AFD_API afd_status afd_cache_write(const void* q, int64_t q_stride, const void* 
  * FP16, weighted by the values' scales first). Which tokens are summed together depends
  * on all lengths of the call, so the last bits of a sequence's result may change
  * with what it is batched with; the same call gives the same bits.
+ * A column with an infinity among the values that are seen may come out as NaN
+ * (its weight's second part may be zero or negative).
  *   q           device BF16 [num_seqs, num_q_heads, head_dim], row stride q_stride
  *   page_table  device int32 [num_seqs, max_pages], row stride table_stride
  *   lengths     device int32 [num_seqs]
