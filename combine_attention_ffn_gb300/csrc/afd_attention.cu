@@ -175,6 +175,26 @@ __device__ __forceinline__ float log2_of(float v) {
   return r;
 }
 
+// A token's values weigh p * their scale, so E4M3 caches raise the running maximum
+// by the scale's logarithm, within these bounds. A sum of exponentials then ends up to
+// 2^100 (with values of zero) or down to 2^-80 where the largest score is: the tokens
+// that leave FP32's range below that are 2^-46 of it each. Above 2^80 a weight passes
+// FP16 and the result becomes infinite or NaN, as it does with an infinite scale; the
+// scores' log-sum does not.
+constexpr float kLiftLeast = -100.f, kLiftMost = 80.f;
+
+// Two maxima may be raised unlike, so what a sum is weighted by where it moves from one
+// to the other, 2^(m - most), may leave FP32's range where the weighted sum does not:
+// E4M3 sums take the weight's root twice. Returns the root (E4M3), or the weight.
+template <bool FP8>
+__device__ __forceinline__ float weight_root(float m, float most) { return exp2_of(FP8 ? 0.5f * (m - most) : m - most); }
+template <bool FP8>
+__device__ __forceinline__ float weight_of(float root) { return FP8 ? root * root : root; }
+template <bool FP8>
+__device__ __forceinline__ float add_weighted(float l, float root, float sum) {
+  return FP8 ? fmaf(l * root, root, sum) : fmaf(l, root, sum);
+}
+
 // The natural logarithm of sum * 2^most; the sum's own, good to 2^-22, by lg2.
 __device__ __forceinline__ float log_sum(float most, float sum) { return (most + log2_of(sum)) * kLn2; }
 
@@ -620,7 +640,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
           if (FP8) {
             const float2 two = *reinterpret_cast<const float2*>(ks + S::kScales + tok * 8);
             kscale = two.x, vscale[t][y] = two.y;
-            lift = fmaxf(log2_of(two.y), -100.f);
+            lift = fminf(fmaxf(log2_of(two.y), kLiftLeast), kLiftMost);
           }
           // (a token that is not seen has a key of zeros)
           const float bias = all ? 0.f : reinterpret_cast<const float*>(ks + S::kBias)[tok];
@@ -642,9 +662,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float to = fmaxf(tokens_max(top[n][x]), m[n][x]);
-            const float f = m[n][x] == -INFINITY ? 0.f : exp2_of(m[n][x] - to);
+            const float root = m[n][x] == -INFINITY ? 0.f : weight_root<FP8>(m[n][x], to), f = weight_of<FP8>(root);
             m[n][x] = to;
-            l[n][x] *= f;
+            l[n][x] = FP8 ? l[n][x] * root * root : l[n][x] * f;
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) o[d][n][x] *= f, o[d][n][2 + x] *= f;
           }
@@ -842,11 +862,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
 #pragma unroll 1
     for (int w = max(c.w0, 0); w < c.w1; ++w) {
       const int which = w == c.w0;
-      const float scale = exp2_of(part_m[w][which][row] - minus);
+      const float root = weight_root<FP8>(part_m[w][which][row], minus), scale = weight_of<FP8>(root);
       const float* from = (which || !away_a[w] ? reinterpret_cast<const float*>(shared + w * Y::kRing)
                                                : p.kept + (int64_t)(blockIdx.x * W + w) * ROWS * D) + row * D + col;
       const float4 x = *reinterpret_cast<const float4*>(from), y = *reinterpret_cast<const float4*>(from + 4);
-      sum = fmaf(part_l[w][which][row], scale, sum);
+      sum = add_weighted<FP8>(part_l[w][which][row], root, sum);
       f[0] = fmaf(x.x, scale, f[0]), f[1] = fmaf(x.y, scale, f[1]), f[2] = fmaf(x.z, scale, f[2]), f[3] = fmaf(x.w, scale, f[3]);
       f[4] = fmaf(y.x, scale, f[4]), f[5] = fmaf(y.y, scale, f[5]), f[6] = fmaf(y.z, scale, f[6]), f[7] = fmaf(y.w, scale, f[7]);
     }
@@ -867,7 +887,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
 
 // Joins what the blocks left open: a warp per row of a segment that began in
 // block `from`; its parts are that block's second and the next ones' first.
-template <int D, int NH>
+template <int D, bool FP8, int NH>
 __global__ void __launch_bounds__(256) decode_join_kernel(const AttentionParams p) {
   afd::pdl_wait();
   afd::pdl_launch_dependents();
@@ -906,9 +926,11 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const AttentionParams 
     float top = fmaxf(m, most);
 #pragma unroll
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-    const float minus = top == -INFINITY ? 0.f : top, before = exp2_of(most - minus), weight = exp2_of(m - minus);
+    const float minus = top == -INFINITY ? 0.f : top;
+    const float before_root = weight_root<FP8>(most, minus), before = weight_of<FP8>(before_root);
+    const float root = weight_root<FP8>(m, minus), weight = weight_of<FP8>(root);
     most = top;
-    sum = fmaf(sum, before, l * weight);  // (each lane's own parts)
+    sum = add_weighted<FP8>(sum, before_root, FP8 ? l * root * root : l * weight);  // (each lane's own parts)
 #pragma unroll
     for (int k = 0; k < N; ++k) f[k] *= before;
     for (int j = 0;;) {
@@ -965,7 +987,7 @@ cudaError_t launch_attention(const AttentionParams& p, int64_t tiles, int device
   const int blocks = (int)(tiles == 0 || (want > most && !p.solo) ? most : want);
   e = afd::launch_dependent(decode_attention_kernel<D, FP8, NH>, blocks, kWarps * 32, Y::kShared, stream, p);
   if (e != cudaSuccess || p.solo) return e;
-  return afd::launch_dependent(decode_join_kernel<D, NH>, blocks * NH, 256, 0, stream, p);
+  return afd::launch_dependent(decode_join_kernel<D, FP8, NH>, blocks * NH, 256, 0, stream, p);
 }
 
 template <int D>

@@ -602,7 +602,8 @@ typedef struct afd_cache {
   void* k;               /* device [num_pages][num_kv_heads][page_size][head_dim], BF16 or E4M3 bytes */
   void* v;               /* the same of the values */
   float* k_scale;        /* device FP32 [num_pages][num_kv_heads][page_size] (E4M3), else NULL */
-  float* v_scale;        /* not negative; zero or at least 2^-100 */
+  float* v_scale;        /* not negative; zero, or 2^-100 to 2^80: where a scale is above that (infinite), its head's
+                            attention may come out infinite or NaN, its lse stays that of the scores */
   int64_t k_page_stride; /* elements from a page to the next (the rest is dense): keys and values may */
   int64_t v_page_stride; /*   be two halves of one allocation's pages; multiples of 64 bytes */
   int32_t num_pages;     /* num_pages * page stride at most 256 GB each */
