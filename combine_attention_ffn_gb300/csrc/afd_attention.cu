@@ -176,12 +176,19 @@ __device__ __forceinline__ float log2_of(float v) {
 }
 
 // A token's values weigh p * their scale, so E4M3 caches raise the running maximum
-// by the scale's logarithm, within these bounds. A sum of exponentials then ends up to
-// 2^100 (with values of zero) or down to 2^-80 where the largest score is: the tokens
-// that leave FP32's range below that are 2^-46 of it each. Above 2^80 a weight passes
-// FP16 and the result becomes infinite or NaN, as it does with an infinite scale; the
-// scores' log-sum does not.
-constexpr float kLiftLeast = -100.f, kLiftMost = 80.f;
+// by the scale's logarithm, within these bounds, and all weights by 2^kRaise: the largest
+// of a warp's tokens is 2^7 (2^15 where the maximum lags, kLazy), and what FP16 loses is
+// below 2^-32 of it. Without the raise tokens of 2^-25 were lost, and long tails of them
+// counted in the sum alone. Scales from 2^-100 to 2^-93 have less: 2^-25.
+// A sum of exponentials then ends up to 2^100 (with values of zero) or down to 2^-73
+// where the largest score is: the tokens that leave FP32's range below that are 2^-53 of
+// it each. Above 2^80 a weight passes FP16 and the result becomes infinite or NaN, as it
+// does with an infinite scale; the scores' log-sum does not.
+// A second FP16 part for each weight (as BF16 caches have) changes the results by less
+// than their rounding to BF16 does: 64 sequences, 16 heads a KV head, 81.3 us against 71.8.
+constexpr float kLiftLeast = -93.f, kLiftMost = 80.f;
+template <bool FP8>
+constexpr float kRaise = FP8 ? 7.f : 0.f;
 
 // Two maxima may be raised unlike, so what a sum is weighted by where it moves from one
 // to the other, 2^(m - most), may leave FP32's range where the weighted sum does not:
@@ -624,10 +631,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
         }
       }
       // ---- softmax. E4M3: the weight of a token's values is p * its scale, so
-      // the running maximum is that of s + log2(scale): the FP16 weights stay
-      // small, and what they lose is small beside the largest contribution. The
+      // the running maximum is that of s + log2(scale): the FP16 weights stay in
+      // range, and what they lose is small beside the largest contribution. The
       // maximum moves, and what was summed is rescaled, only where a score is
-      // kLazy above it; weights are then at most 2^kLazy.
+      // kLazy above it; weights are then at most 2^(kLazy + kRaise).
       float top[NH][2], vscale[TB][2];
 #pragma unroll
       for (int n = 0; n < NH; ++n) top[n][0] = top[n][1] = -INFINITY;
@@ -673,7 +680,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
       for (int n = 0; n < NH; ++n)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float minus = m[n][x] == -INFINITY ? 0.f : m[n][x];
+          const float minus = (m[n][x] == -INFINITY ? 0.f : m[n][x]) - kRaise<FP8>;
 #pragma unroll
           for (int t = 0; t < TB; ++t)
 #pragma unroll
@@ -769,7 +776,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
                   for (int k = 0; k < 8; ++k) f[k] = o[(h * E + e + k) / 2][n][2 * (k & 1) + x] * inv;
                   *reinterpret_cast<uint4*>(out + (8 * h + g) * E + e) = afd::float_to_bf16x8(f);
                 }
-              if (p.lse && g == 0) p.lse[(int64_t)at.b * p.Hq + q0 + row] = l[n][x] == 0.f ? -INFINITY : log_sum(m[n][x], l[n][x]);
+              if (p.lse && g == 0)
+                p.lse[(int64_t)at.b * p.Hq + q0 + row] = l[n][x] == 0.f ? -INFINITY : log_sum(m[n][x] - kRaise<FP8>, l[n][x]);
             }
         } else {
           // Left open. What began in an earlier warp's share goes to the warp's own
@@ -794,7 +802,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_attention_kernel(const 
                   *reinterpret_cast<float4*>(to + row * D + (8 * h + g) * E + e) =
                       make_float4(o[d][n][x], o[d][n][2 + x], o[d + 1][n][x], o[d + 1][n][2 + x]);
                 }
-              if (g == 0) part_m[warp][which][row] = m[n][x], part_l[warp][which][row] = l[n][x];
+              if (g == 0) part_m[warp][which][row] = m[n][x] - kRaise<FP8>, part_l[warp][which][row] = l[n][x];
             }
           if (lane == 0) {
             if (which) seg_b[warp] = seg, end_b[warp] = lo + place + (at.span.end - at.tile);

@@ -655,7 +655,8 @@ AFD_API afd_status afd_cache_write(const void* q, int64_t q_stride, const void* 
  * that are not seen is not read.
  * Sums, maxima and exponentials are FP32; the probabilities are rounded for the
  * product with the values (BF16 caches: to two BF16 parts, 16 bits; E4M3: to
- * FP16, weighted by the values' scales first). Which tokens are summed together depends
+ * FP16, 11 bits, weighted by the values' scales first, and a token of less than
+ * 2^-32 of the largest such weight may be left out there). Which tokens are summed together depends
  * on all lengths of the call, so the last bits of a sequence's result may change
  * with what it is batched with; the same call gives the same bits.
  * A column with an infinity among the values that are seen may come out as NaN

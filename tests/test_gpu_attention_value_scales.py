@@ -1,6 +1,7 @@
 """Decode attention over E4M3 caches whose value scales are infinite, very large
 or very unlike each other: the scores' log-sum is of the scores alone, whatever
-the values weigh, in a warp, across a block's warps and across blocks."""
+the values weigh, in a warp, across a block's warps and across blocks; weak tokens
+beside strong ones keep their part of the result."""
 import math
 
 import pytest
@@ -126,3 +127,29 @@ def test_values_of_zero_beside_large_ones(first, e, n, G, D):
     out, lse, want, want_lse, err, lse_err = _call(*_scored(scores, vs, v, D, G))
     sh.check_lse(lse, want_lse, lse_err)
     eh.check_bf16(out, want, err, torch.ones(G, dtype=torch.bool, device="cuda"))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [1, 16])
+@pytest.mark.parametrize("n", [64, 700, 9000])
+@pytest.mark.parametrize("weak", [24.3, 25.5, 28.0])
+def test_a_weak_tail_beside_strong_tokens(weak, n, G, D):
+    """One token in 32 weighs 2^weak of every other one; in the odd columns only
+    the weak ones have values. Weights are FP16 with 2^7 for a warp's largest: half of
+    FP16's smallest step is 2^-32 of that. The rest of the bound: 2^-11 for a weight's own
+    rounding; scores up to 28 (base 2) with three roundings and the exponential's 2^-22, less
+    than 2^-18; sums as in the harness."""
+    strong = torch.arange(n, device="cuda") % 32 == 5
+    scores = torch.where(strong, 0.0, -weak * math.log(2))
+    vs = torch.full((n,), 0.01, device="cuda")
+    v = torch.rand(n, D, generator=_gen(5), device="cuda") * 400 + 40
+    v[:, 1::2] *= ~strong[:, None]
+    q, case = _scored(scores, vs, v, D, G)
+    out = lib.decode_attention(q, case[0], case[1], case[4], case[5], scale=1.0, k_scale=case[2], v_scale=case[3])[0]
+    p = torch.softmax(scores.double(), 0)
+    codes = case[1].view(-1, D)[:n].double()
+    want = p * vs.double() @ codes
+    rel = 2.0 ** -11 + 2.0 ** -17 + (n + 64) * 2 * sh.FP32_HALF
+    err = rel * want + 2.0 ** -32 * (p * vs.double()).max() * codes.sum(0)
+    assert (err[1::2] < 0.1 * want[1::2]).all()
+    eh.check_bf16(out, want.expand(G, D), err.expand(G, D), torch.ones(G, dtype=torch.bool, device="cuda"))
