@@ -43,17 +43,31 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
   return r;
 }
 
-// v / scale as v * (1 / scale), at most 2^-23 off. That moves a value in a hundred
-// thousand to its E4M3 neighbour, for values that are FP32 results; quotients of
-// BF16 values often lie on a tie (one in a few hundred), so those are divided.
-__device__ __forceinline__ uint2 to_e4m3x8(const float (&v)[8], float inv) {
-  return make_uint2(pack_e4m3(v[0] * inv, v[1] * inv) | pack_e4m3(v[2] * inv, v[3] * inv) << 16,
-                    pack_e4m3(v[4] * inv, v[5] * inv) | pack_e4m3(v[6] * inv, v[7] * inv) << 16);
-}
-
 __device__ __forceinline__ uint2 divided_e4m3x8(const float (&v)[8], float scale) {
   return make_uint2(pack_e4m3(v[0] / scale, v[1] / scale) | pack_e4m3(v[2] / scale, v[3] / scale) << 16,
                     pack_e4m3(v[4] / scale, v[5] / scale) | pack_e4m3(v[6] / scale, v[7] / scale) << 16);
+}
+
+// The same quotients where eight divisions cost more than the rest: the product with
+// the rounded reciprocal, corrected by its remainder, which an FMA gives exactly, is the
+// rounded quotient (P. W. Markstein, Computation of elementary functions on the IBM RISC
+// System/6000 processor, IBM J. Res. Dev. 34, 1990). The remainder is exact while its
+// last digit, the quotient's times the scale's, is 2^-149 or more: from scales of 2^-92 on,
+// as quotients below 2^-10 all go to zero. Where the scale is below 2^-90 both sides are
+// multiplied by 2^64.
+// Norm of 4,096 rows of 4,096: 24.4 us, 27.9 with divisions, 25.9 with divisions for the
+// small scales alone; 24.0 with the product alone, which put one value in 40,000 on the
+// wrong side of a border.
+__device__ __forceinline__ uint2 quotient_e4m3x8(const float (&v)[8], float scale) {
+  const float up = scale < 8.077935669463161e-28f ? 18446744073709551616.f : 1.f;
+  const float s = scale * up, inv = 1.f / s;
+  float q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float y = v[e] * up, near = y * inv;
+    q[e] = fmaf(-fmaf(near, s, -y), inv, near);  // (so ordered, a zero keeps its sign)
+  }
+  return make_uint2(pack_e4m3(q[0], q[1]) | pack_e4m3(q[2], q[3]) << 16, pack_e4m3(q[4], q[5]) | pack_e4m3(q[6], q[7]) << 16);
 }
 
 }  // namespace afd

@@ -7,7 +7,7 @@
 //
 // One pass: a block holds a row in registers between the sum of squares and
 // the products, so each input is read and each output written once, which is
-// what bounds it for many rows: 4,096 of 4,096 columns (151.5 MB) in 23.9 us, 6.3
+// what bounds it for many rows: 4,096 of 4,096 columns (151.5 MB) in 24.4 us, 6.2
 // TB/s, against 22.6 at the copy's rate. Decode steps are a launch and two trips to
 // memory: one row of 2,048 1.6 us, 128 of 7,168 2.1. Two groups of eight columns a
 // thread above 2,048 columns (against 25.2 us then, one took 27.6 and four 24.8, but
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(norm_threads(VPT)) norm_rows_kernel(const Norm
     if (p.q) {  // a block of 128 columns is 16 lanes' (H is a multiple of 128 then)
       const float scale = afd::block_scale(afd::lanes_absmax<16>(afd::absmax8(y)));
       if (in) {
-        *reinterpret_cast<uint2*>(p.q + t * p.H + c) = afd::to_e4m3x8(y, 1.f / scale);
+        *reinterpret_cast<uint2*>(p.q + t * p.H + c) = afd::quotient_e4m3x8(y, scale);
         if ((threadIdx.x & 15) == 0) p.q_scale[t * (p.H / 128) + c / 128] = scale;
       }
     }
