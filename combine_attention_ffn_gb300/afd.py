@@ -21,6 +21,7 @@ from typing import NamedTuple, Optional
 
 import numpy as np
 import torch
+import torch.autograd.forward_ad as _forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libafd.so")
@@ -447,7 +448,8 @@ def route_layout_noalloc(ids: torch.Tensor, num_experts: int, num_workers: int,
 
 
 # -- the experts' side of an exchange (afd.h: no context, no state) -----------
-# Forward only: with gradients enabled, inputs that require them are refused.
+# Forward only: with gradients enabled, inputs that require them are refused, and
+# forward-mode dual tensors always.
 # A decode step's call is shorter on the GPU than on the host, so the binding
 # asks PyTorch for the raw stream and device number where it has them: the
 # public objects around them cost 1 us a call.
@@ -482,10 +484,18 @@ def _too_large(*sizes: int) -> AfdError:
     return AfdError(ERR_UNSUPPORTED, f"sizes {sizes} must fit 32 bits")
 
 
-def _no_backward() -> AfdError:
-    """Autograd would take the result for a constant."""
-    return AfdError(ERR_UNSUPPORTED, "no backward pass: inputs that require gradients are taken "
-                    "under torch.no_grad() only, or detached")
+def _refuse_gradients(*tensors: Optional[torch.Tensor]) -> None:
+    """Autograd would take the result for a constant. (Tangents are there
+    inside a dual level only, whatever the gradients' mode.)"""
+    if _grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise AfdError(ERR_UNSUPPORTED, "no backward pass: inputs that require gradients are taken "
+                               "under torch.no_grad() only, or detached")
+    if getattr(_forward_ad, "_current_level", 0) >= 0:
+        for t in tensors:
+            if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+                raise AfdError(ERR_UNSUPPORTED, "no forward-mode derivative: dual tensors are not taken")
 
 
 def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
@@ -537,9 +547,7 @@ def route_topk(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
     T, E = logits.shape
     if T > _INT32 or E > _INT32 or not -_INT32 <= top_k <= _INT32:
         raise _too_large(T, E, top_k)
-    if _grad_enabled() and (logits.requires_grad or (bias is not None and bias.requires_grad)
-                            or (weights is not None and weights.requires_grad)):
-        raise _no_backward()
+    _refuse_gradients(logits, bias, weights)
     stride = _want_rows(logits, "logits", logits.dtype, (T, E))
     bias_ptr = None if bias is None else _want(bias, "bias", torch.float32, (E,))
     live_ptr = None if live_tokens is None else _want(live_tokens, "live_tokens", torch.int32, (1,))
@@ -579,10 +587,7 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, ends: torch.Tensor, *,
     G, W = weight.shape[0], weight.shape[1]
     if G > _INT32 or W > _INT32 or K > _INT32 or not -_INT32 <= expert_alignment <= _INT32:
         raise _too_large(G, W, K, expert_alignment)
-    if _grad_enabled() and (x.requires_grad or weight.requires_grad or (out is not None and out.requires_grad)
-                            or (x_scale is not None and x_scale.requires_grad)
-                            or (weight_scale is not None and weight_scale.requires_grad)):
-        raise _no_backward()
+    _refuse_gradients(x, weight, out, x_scale, weight_scale)
     fp8 = x.dtype == torch.float8_e4m3fn
     if gated and W % 2:
         raise AfdError(ERR_ARG, f"a gated weight has an even number of rows, got {W}")
@@ -632,8 +637,7 @@ def gated_rows(h: torch.Tensor, ends: torch.Tensor, *, expert_alignment: int = 1
     G = ends.numel()
     if G > _INT32 or N > _INT32 or not -_INT32 <= expert_alignment <= _INT32:
         raise _too_large(G, N, expert_alignment)
-    if _grad_enabled() and (h.requires_grad or (out is not None and out.requires_grad)):
-        raise _no_backward()
+    _refuse_gradients(h, out)
     ends_ptr = _want(ends, "ends", torch.int32, (G,))
     if out is None:
         out = _empty((R, N), torch.bfloat16, h.device, stream)
@@ -666,10 +670,7 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
     tokens = token_slots.numel()
     if tokens > _INT32 or S > _INT32 or rank > _INT32 or K > _INT32 or N > _INT32 or not -_INT32 <= top_k <= _INT32:
         raise _too_large(tokens, S, rank, K, N, top_k)
-    if _grad_enabled() and (base.requires_grad or x.requires_grad or down.requires_grad or up.requires_grad
-                            or scales.requires_grad or (out is not None and out.requires_grad)
-                            or (x_scale is not None and x_scale.requires_grad)):
-        raise _no_backward()
+    _refuse_gradients(base, x, down, up, scales, out, x_scale)
     slots_ptr = _want(token_slots, "token_slots", torch.int32, (tokens,))
     G, src_ptr, ends_ptr = 0, None, None
     if row_src is not None:
@@ -703,13 +704,6 @@ def adapter_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: tor
 _BF16_T = torch.bfloat16
 
 
-def _grad_of(*tensors) -> bool:
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            return True
-    return False
-
-
 class NormRows(NamedTuple):
     """What :func:`norm_rows` computed; None for what was not asked for."""
     rows: Optional[torch.Tensor]      # [T, H] bf16
@@ -738,8 +732,7 @@ def norm_rows(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, resid
     shape = T, H = x.shape
     if H > _INT32:
         raise _too_large(H)
-    if _grad_enabled() and _grad_of(x, weight, residual, out, residual_out, fp8_out, scale_out):
-        raise _no_backward()
+    _refuse_gradients(x, weight, residual, out, residual_out, fp8_out, scale_out)
     bf16, device = _BF16_T, x.device
     x_stride = _want_rows(x, "x", bf16, shape)
     weight_ptr = _want(weight, "weight", bf16, (H,))
@@ -843,8 +836,7 @@ def cache_write(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pos
     `v_cache` are [pages, Hkv, page_size, D], bf16, or float8_e4m3fn with
     `k_scale` and `v_scale` float32 [pages, Hkv, page_size]. See
     afd_cache_write in include/afd.h."""
-    if _grad_enabled() and _grad_of(q, k, v, inv_freq, k_cache, v_cache, k_scale, v_scale, q_out):
-        raise _no_backward()
+    _refuse_gradients(q, k, v, inv_freq, k_cache, v_cache, k_scale, v_scale, q_out)
     cache = _cache(k_cache, v_cache, k_scale, v_scale)
     dim, heads = cache.head_dim, cache.num_kv_heads
     T = k.shape[0] if k.dim() else 0
@@ -895,8 +887,7 @@ def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     new one counted; with `window` only that many last ones are seen. `scale`
     defaults to D ** -0.5. A sequence that sees nothing gets zeros and an lse of
     -inf. See afd_decode_attention in include/afd.h."""
-    if _grad_enabled() and _grad_of(q, k_cache, v_cache, k_scale, v_scale, out, lse):
-        raise _no_backward()
+    _refuse_gradients(q, k_cache, v_cache, k_scale, v_scale, out, lse)
     cache = _cache(k_cache, v_cache, k_scale, v_scale)
     dim, heads = cache.head_dim, cache.num_kv_heads
     if q.dim() != 3 or page_table.dim() != 2:
