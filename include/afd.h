@@ -566,15 +566,16 @@ AFD_API int64_t afd_adapter_workspace_bytes(int64_t num_rows, int32_t num_tokens
  * They take at most 2^31 - 2^20 - 1 rows or tokens.
  * Where values go to E4M3, a vector of them shares one FP32 scale,
  *   scale = max(max |v| / 448, 2^-100), value = e4m3(v / scale),
- * the scale to a step of FP32, values rounded to nearest even; all of a vector with an infinity or a NaN decodes to
- * NaN. */
+ * the scale to a step of FP32, the FP32 quotients rounded to nearest even; all of
+ * a vector with an infinity or a NaN decodes to NaN. */
 
 /* The rows a source dispatches, from its residual stream:
  *   r = x + residual                     residual_out = bf16(r)
  *   y = r / sqrt(mean(r^2) + eps) * weight        out = bf16(y)
  *   and y in E4M3 with a scale for each block of 128 columns, in the form
  *   afd_source_dispatch takes (fp8_out, scale_out)
- * in FP32, from the unrounded r; the sum of squares has to be finite in FP32.
+ * in FP32, from the unrounded r; the sum of squares has to be finite in FP32,
+ * and with eps = 0 a normal number or 0 (a row of zeros is NaN then).
  *   x             device BF16 [num_rows, features], row stride x_stride elements
  *   residual      device BF16 [num_rows, features], row stride residual_stride,
  *                 or NULL (then residual_out is NULL too)
@@ -606,7 +607,7 @@ typedef struct afd_cache {
                             attention may come out infinite or NaN, its lse stays that of the scores */
   int64_t k_page_stride; /* elements from a page to the next (the rest is dense): keys and values may */
   int64_t v_page_stride; /*   be two halves of one allocation's pages; multiples of 64 bytes */
-  int32_t num_pages;     /* num_pages * page stride at most 256 GB each */
+  int32_t num_pages;     /* num_pages * page stride at most 256 GB each, num_pages * page_size below 2^31 */
   int32_t page_size;     /* tokens of a page, any number; multiples of 16 are read fastest */
   int32_t num_kv_heads;
   int32_t head_dim;      /* 64 or 128 */
@@ -634,7 +635,7 @@ typedef struct afd_cache {
  *   q_out      device BF16 [num_tokens, num_q_heads, head_dim], row stride
  *              q_out_stride; may be q itself (the same address and stride)
  * Limits: at most 1,024 heads of either kind; q, k, v, q_out, the caches
- * and the rows' strides multiples of 16 bytes; num_pages * page_size below 2^31.
+ * and the rows' strides multiples of 16 bytes.
  * Buffers may be device, managed or page-locked host memory.
  * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (limits), AFD_ERR_CUDA. */
 AFD_API afd_status afd_cache_write(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -660,7 +661,9 @@ AFD_API afd_status afd_cache_write(const void* q, int64_t q_stride, const void* 
  * on all lengths of the call, so the last bits of a sequence's result may change
  * with what it is batched with; the same call gives the same bits.
  * A column with an infinity among the values that are seen may come out as NaN
- * (its weight's second part may be zero or negative).
+ * (its weight's second part may be zero or negative). A head with a score of
+ * +infinity or NaN gets NaN for out and lse; one whose scores are all -infinity is
+ * one that sees nothing.
  *   q           device BF16 [num_seqs, num_q_heads, head_dim], row stride q_stride
  *   page_table  device int32 [num_seqs, max_pages], row stride table_stride
  *   lengths     device int32 [num_seqs]
@@ -672,7 +675,9 @@ AFD_API afd_status afd_cache_write(const void* q, int64_t q_stride, const void* 
  *               mean nothing afterwards. Calls that may run at the same time
  *               (other streams, other captured graphs) need one each.
  * Limits: num_q_heads a multiple of num_kv_heads, at most 1,024; max_pages *
- * page_size below 2^31 - 2^10; q, out and their strides multiples of 16 bytes.
+ * page_size below 2^31 - 2^10; num_seqs * num_kv_heads below 2^31 - 2^20, counted
+ * once for each 16 query heads of a KV head; q, out and their strides
+ * multiples of 16 bytes.
  * Buffers may be device, managed or page-locked host memory.
  * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (limits), AFD_ERR_CUDA. */
 AFD_API afd_status afd_decode_attention(const void* q, int64_t q_stride, const afd_cache* cache,
