@@ -1008,6 +1008,9 @@ cudaError_t launch_of(const AttentionParams& p, bool fp8, int64_t tiles, int dev
 }
 
 constexpr int64_t kMaxTokens = INT32_MAX - 1024;  // of a table's row
+// Places on the line that the tables allow (tiles of 16 tokens, the beginnings): a warp
+// counts its own in 32 bits, and there are more than 1,024 warps.
+constexpr int64_t kMaxPlaces = (int64_t)1 << 41;
 
 }  // namespace
 
@@ -1039,6 +1042,7 @@ AFD_API afd_status afd_decode_attention(const void* q, int64_t q_stride, const a
   if (num_q_heads > afd::kMaxHeads || tokens > kMaxTokens || (int64_t)num_seqs * Hkv * groups > afd::kMaxRows ||
       q_stride % 8 || out_stride % 8)
     return AFD_ERR_UNSUPPORTED;
+  if (segments(num_seqs, num_q_heads, Hkv) * (tokens / 16 + 3) > kMaxPlaces) return AFD_ERR_UNSUPPORTED;
   if (num_seqs == 0) return AFD_OK;
   if (!q || !out || !lengths || (max_pages > 0 && !page_table)) return AFD_ERR_ARG;
   const int64_t need = afd_decode_workspace_bytes(num_seqs, num_q_heads, Hkv, D, max_pages, cache->page_size);

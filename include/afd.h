@@ -676,8 +676,8 @@ AFD_API afd_status afd_cache_write(const void* q, int64_t q_stride, const void* 
  *               (other streams, other captured graphs) need one each.
  * Limits: num_q_heads a multiple of num_kv_heads, at most 1,024; max_pages *
  * page_size below 2^31 - 2^10; num_seqs * num_kv_heads below 2^31 - 2^20, counted
- * once for each 16 query heads of a KV head; q, out and their strides
- * multiples of 16 bytes.
+ * once for each 16 query heads of a KV head, and that times max_pages * page_size
+ * below 2^44; q, out and their strides multiples of 16 bytes.
  * Buffers may be device, managed or page-locked host memory.
  * Errors: AFD_ERR_ARG, AFD_ERR_UNSUPPORTED (limits), AFD_ERR_CUDA. */
 AFD_API afd_status afd_decode_attention(const void* q, int64_t q_stride, const afd_cache* cache,
