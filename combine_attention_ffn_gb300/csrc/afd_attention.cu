@@ -23,12 +23,14 @@
 // long as both sides agree, so a lane takes 16 neighbouring bytes of a key at a
 // time, and 16 of four tokens' values, whose pairs are then interleaved.
 //
-// Measured: 128 sequences of up to 8,192 tokens (64 query and 8 KV heads of 128, BF16,
-// 1.36 GB) 206 us, 6.6 TB/s; one of 131,072 tokens 87.9 (floor 80.1); 64 of up to
-// 16,384 over E4M3, 16 heads a KV head, 71.2 (53.3); 250 of up to 1,000 (64 columns,
-// pages of 16) 36.4 (24.5). The loop itself streams at the copy's rate; about 10 us go
-// to what is around it: 2 to find the shares, 2.5 to the first tile, 2 to 5 between the
-// mean and the last block, 2 for the block's join and 2.5 for the second kernel.
+// Measured (us, a copy's time of the same bytes behind it): 128 sequences of up to 8,192
+// tokens (64 query and 8 KV heads of 128, BF16, 1.36 GB) 207.7 (203.4); one of 131,072
+// tokens 87.9 (80.1); 64 of up to 16,384 over E4M3, 16 heads a KV head, 71.8 (53.3); 250 of
+// up to 1,000 (64 columns, pages of 16) 36.4 (24.5); 96 windows of 1,024 over E4M3, 64
+// columns, 25.3 (13.0). Inside the loop that is 6.4 to 7.5 TB/s, as reads alone are faster than
+// a copy. What is around it, in the same order: 4.6, 3.7, 4.6, 4.5 and 4.6 to the first
+// tile; from the warps' mean end to the last one's 7.9, 4.5, 3.8, 3.2 and 2.3; the
+// blocks' joins 4.1, 2.8, 5.9, 2.3 and 2.0; the second launch 2.6, 3.6, 3.9, 2.5 and 2.0.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -104,10 +106,14 @@ struct Shape {
   static constexpr int kStage = kBias + 4 * kTile;
   static constexpr int E = FP8 && D == 128 ? 16 : 8;         // neighbouring columns of a lane
   static constexpr int H = D / 8 / E;                        // ... and how many such groups
-  // What a segment counts beside its tiles, in tiles. With 0, 1/2, 1, 3/2 and 2:
-  // 64 unlike sequences (E4M3, 128 columns) 79.6, 77.5, 74.3, 73.4, 72.0 us; 250
-  // short ones (BF16, 64 columns) 43.7, 38.4, 36.6, 37.2, 37.5.
+  // What a segment counts beside its tiles, in tiles (1 at least: a step of more than one
+  // is how a cursor tells of a new segment). With 1 and 2, us: E4M3, 128 columns, 64 unlike
+  // sequences 74.4, 71.8 (16 heads a KV head) and 40.1, 40.1 (8), 250 short ones 41.5, 42.0;
+  // E4M3, 64 columns, 96 windows 25.3, 25.5, 250 short ones 26.7, 28.0; BF16, 128 columns,
+  // 128 sequences 207.9, 208.4, 64 62.7, 62.4, 250 short ones 62.6, 63.2; BF16, 64 columns,
+  // 250 short ones 36.4, 37.2.
   static constexpr int kBegin = FP8 && D == 128 ? 2 : 1;
+  static_assert(kBegin >= 1, "a new segment looks like the last one's next tile otherwise");
 };
 
 // NH: query heads of a chunk, in eights.
