@@ -7,9 +7,9 @@
 //
 // One pass: a block holds a row in registers between the sum of squares and
 // the products, so each input is read and each output written once, which is
-// what bounds it for many rows: 4,096 of 4,096 columns (151.5 MB) in 24.4 us, 6.2
+// what bounds it for many rows: 4,096 of 4,096 columns (151.5 MB) in 24.3 us, 6.2
 // TB/s, against 22.6 at the copy's rate. Decode steps are a launch and two trips to
-// memory: one row of 2,048 1.6 us, 128 of 7,168 2.1. Two groups of eight columns a
+// memory: one row of 2,048 1.7 us, 128 of 7,168 2.1. Two groups of eight columns a
 // thread above 2,048 columns (against 25.2 us then, one took 27.6 and four 24.8, but
 // 2.3 for the 128 rows).
 

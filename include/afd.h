@@ -654,12 +654,14 @@ AFD_API afd_status afd_cache_write(const void* q, int64_t q_stride, const void* 
  * table's pages ends there. A sequence that sees nothing (a bucket's padding:
  * length 0) gets out = +0 and lse = -infinity. What the cache holds in places
  * that are not seen is not read.
- * Sums, maxima and exponentials are FP32; the probabilities are rounded for the
- * product with the values (BF16 caches: to two BF16 parts, 16 bits; E4M3: to
- * FP16, 11 bits, weighted by the values' scales first, and a token of less than
- * 2^-32 of the largest such weight may be left out there). Which tokens are summed together depends
- * on all lengths of the call, so the last bits of a sequence's result may change
- * with what it is batched with; the same call gives the same bits.
+ * Sums, maxima and exponentials are FP32. The probabilities are rounded for the
+ * product with the values: BF16 caches, to two BF16 parts (16 bits); E4M3, to FP16
+ * (11 bits), weighted by the values' scales first, and a token of less than 2^-32 of
+ * the largest such weight (up to 2^-25 with scales below 2^-93) may be left out there. With
+ * E4M3 caches the queries' columns are rounded to 2^-24 of their head's largest.
+ * Which tokens are summed together depends on all lengths of the call, so the last
+ * bits of a sequence's result may change with what it is batched with; the same
+ * call gives the same bits.
  * A column with an infinity among the values that are seen may come out as NaN
  * (its weight's second part may be zero or negative). A head with a score of
  * +infinity or NaN gets NaN for out and lse; one whose scores are all -infinity is
